@@ -206,7 +206,6 @@ def prepare(case, seed):
             s["pos"] = torch.empty((T, k), dtype=torch.int32, device="cuda")
             s["order"] = torch.empty(rows, dtype=torch.int32, device="cuda")
             s["offsets"] = torch.empty(E + 1, dtype=torch.int32, device="cuda")
-            s["workspace"] = torch.empty(sk.expert_dispatch_workspace(T, k, E), dtype=torch.uint8, device="cuda")
         return s
     s["pos"], s["order"], s["offsets"] = _positions(ids, E)
     if op == "experts":
@@ -242,7 +241,7 @@ def _run_own(s):
     op = s["case"]["op"]
     if op == "dispatch":
         xs, pos, order, offsets = sk.expert_dispatch(s["ids"], s["case"]["E"], x=s["x"], xs=s["xs"], pos=s["pos"],
-                                                     order=s["order"], offsets=s["offsets"], workspace=s["workspace"])
+                                                     order=s["order"], offsets=s["offsets"])
         return {"xs": xs, "pos": pos, "order": order, "offsets": offsets}
     if op == "combine":
         return sk.expert_combine(s["ys"], s["pos"], s["weights"], out=s["out"])
