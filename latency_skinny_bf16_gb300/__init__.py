@@ -133,6 +133,7 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.skinny_status_string.restype = ctypes.c_char_p
     lib.skinny_version.argtypes = []
     lib.skinny_version.restype = i
+    experts.bind(lib)
     return lib
 
 
@@ -371,3 +372,10 @@ def rmsnorm_gemm(x, gamma, eps, w, out=None, xn=None, stream=None):
     if st != SKINNY_OK:
         raise SkinnyError(st, "skinny_rmsnorm_gemm_bf16")
     return out, xn
+
+
+from . import experts  # noqa: E402  (its functions call back into this module)
+from .experts import *  # noqa: E402,F401,F403
+
+__all__ += experts.__all__
+EXPORTED_SYMBOLS += experts.SYMBOLS

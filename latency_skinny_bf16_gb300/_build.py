@@ -21,8 +21,8 @@ LIB_NAME = "libskinny_gemm.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "dotprod.cu", "dotprod_f32w.cu", "dotmma.cu", "dotmma_f32w.cu", "splitk.cu", "stream.cu",
-           "topk.cu", "rmsnorm.cu", "tmem_gemm.cu"]
-HEADERS = ["common.cuh", "internal.h", "tuning_table.inc", "tma.cuh", "dotmma_f32w.h"]
+           "topk.cu", "rmsnorm.cu", "tmem_gemm.cu", "expert_rows.cu", "experts_api.cu"]
+HEADERS = ["common.cuh", "internal.h", "tuning_table.inc", "tma.cuh", "dotmma_f32w.h", "expert_rows.h"]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -37,7 +37,8 @@ def nvcc_path() -> str:
 
 
 def _inputs() -> list[str]:
-    return [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "skinny_gemm.h"), __file__]
+    return [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
+        os.path.join(INCLUDE, "skinny_gemm.h"), os.path.join(INCLUDE, "skinny_experts.h"), __file__]
 
 
 def up_to_date() -> bool:

@@ -20,6 +20,7 @@
 
 #include "internal.h"
 #include "dotmma_f32w.h"
+#include "expert_rows.h"
 
 namespace skinny {
 namespace {
@@ -124,7 +125,8 @@ skinny_status_t init_device_current(DeviceState &d, int device) {
     if (major != 10 || minor != 3) return SKINNY_ERR_NO_DEVICE;   // built for sm_103a only
     if (dotprod_prepare() != cudaSuccess || dotmma_prepare() != cudaSuccess || splitk_prepare() != cudaSuccess ||
         stream_prepare() != cudaSuccess || dotprod_f32w_prepare() != cudaSuccess ||
-        dotmma_f32w_prepare() != cudaSuccess || tc_prepare() != cudaSuccess)
+        dotmma_f32w_prepare() != cudaSuccess || tc_prepare() != cudaSuccess ||
+        expert_rows_prepare() != cudaSuccess)
         return SKINNY_ERR_LAUNCH;
     void *sym = nullptr;
     if (cudaGetSymbolAddress(&sym, g_status_word) != cudaSuccess) return SKINNY_ERR_LAUNCH;
@@ -152,8 +154,21 @@ skinny_status_t current_device(int *device) {
     return ensure_device(*device);
 }
 
+}  // namespace
+
+skinny_status_t call_context(CallCtx *c) {
+    int device = 0;
+    const skinny_status_t st = current_device(&device);
+    if (st != SKINNY_OK) return st;
+    const DeviceState &d = g_dev[device];
+    *c = {d.num_sms, d.status_word, (uint64_t)g_opt_wait_us.load() * 1000ull, opt_pdl() != 0};
+    return SKINNY_OK;
+}
+
 // ------------------------------------------------------------------ argument checks
 bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
+
+namespace {
 
 // Host-only validation; no CUDA call.  *noop is set when there is nothing to launch.
 // y_bytes: size of one Y element (4 for fp32, 2 for bf16).
@@ -609,7 +624,18 @@ void log_plan(int M, int N, int K, int ldw, const skinny_plan_t &p) {
 using namespace skinny;
 
 namespace skinny {
-namespace {
+skinny_status_t check_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const void *Y, int ldy, int M,
+                           int N, int K, int out_bf16) {
+    bool noop = false;
+    skinny_status_t st = validate(X, ldx, W, ldw, Y, ldy, M, N, K, &noop, out_bf16 ? 2 : 4);
+    if (st != SKINNY_OK || noop || K == 0) return st;
+    CallCtx c;
+    st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    skinny_plan_t plan;
+    return make_plan(X, ldx, W, ldw, M, N, K, c.num_sms, &plan);
+}
+
 // One call: checks, plan, launch.  out_bf16 selects a bf16 Y (2-byte elements).
 skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, void *Y, int ldy,
                          int M, int N, int K, void *stream, int out_bf16) {
@@ -646,6 +672,7 @@ skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw,
     return e == cudaSuccess ? SKINNY_OK : SKINNY_ERR_LAUNCH;
 }
 
+namespace {
 // fp32 weights, tensor-core dot-product (two tf32 terms per weight): 16-row
 // blocks (or the forced block_n), K over a cluster of S CTAs, S the largest
 // power of two up to 8 that keeps the grid within two CTAs per SM and gives

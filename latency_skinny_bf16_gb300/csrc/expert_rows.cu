@@ -1,0 +1,565 @@
+// expert_rows.cu -- rows to experts and back: the stable sort of the router's
+// choices by expert with the copies of the tokens' rows, the weighted sum of
+// the experts' rows per token, and its gradient.
+//
+// With f = t * k + j, id_f = ids[t][j], live when 0 <= id_f < E:
+//     pos_f      = #{live f': id_f' < id_f} + #{live f' < f: id_f' = id_f}
+//     Xs[pos_f]  = X[t]                                     (dispatch)
+//     Y[t]       = sum_j w[t][j] Ys[pos_tj]                 (combine; w = 1: the gradient of dispatch)
+//     dYs[pos_f] = w_f dY[t],  dw_f = <dY[t], Ys[pos_f]>    (the gradient of combine)
+// No arithmetic to speak of: each is bound by the bytes of the rows (read or
+// written once each), and at decode sizes by launch latency.
+#include "common.cuh"
+#include "expert_rows.h"
+
+namespace skinny {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kSortCluster = 8;
+
+// ------------------------------------------------------------------ vectors
+template <int BYTES> struct Vec;
+template <> struct Vec<16> { using T = uint4; };
+template <> struct Vec<8> { using T = uint2; };
+template <> struct Vec<4> { using T = uint32_t; };
+template <> struct Vec<2> { using T = uint16_t; };
+
+__device__ __forceinline__ int load_id(const int32_t *ids, int64_t ldid, int k, int f, int E) {
+    const int64_t at = ldid == k ? (int64_t)f : (int64_t)(f / k) * ldid + f % k;
+    const int id = __ldcg(ids + at);
+    return (unsigned)id < (unsigned)E ? id : -1;
+}
+
+// Exclusive prefix sum over the block of one value per thread; *total gets the
+// sum.  scratch: 33 ints.  Every thread of the block takes part.
+__device__ __forceinline__ int block_exclusive_scan(int v, int *scratch, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int own = lane < warps ? scratch[lane] : 0;
+        int s = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += u;
+        }
+        scratch[lane] = s - own;
+        if (lane == 31) scratch[32] = s;
+    }
+    __syncthreads();
+    *total = scratch[32];
+    return scratch[warp] + inc - v;
+}
+
+// The copies of one token's row: vectors [v0, v1) of X[t] to the rows pos[0..k).
+// The row is read once and stored once per live entry.
+template <int VB>
+__device__ __forceinline__ void copy_row(const char *src, char *Xs, int64_t ldxs_bytes, const int *pos, int k, int v0,
+                                         int v1) {
+    using T = typename Vec<VB>::T;
+    constexpr int U = 4;
+    for (int v = v0 + (int)threadIdx.x; v < v1; v += U * kRowThreads) {
+        T r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * kRowThreads < v1) r[u] = __ldcg(reinterpret_cast<const T *>(src) + v + u * kRowThreads);
+        for (int j = 0; j < k; ++j) {
+            const int p = pos[j];
+            if (p < 0) continue;
+            T *dst = reinterpret_cast<T *>(Xs + (int64_t)p * ldxs_bytes);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * kRowThreads < v1) dst[v + u * kRowThreads] = r[u];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dispatch, few entries: one launch
+// Grid (T + 1, chunks).  Every CTA of a token reads all n ids (a few KB, from
+// L2) and counts for its own k entries, one warp each, the entries before
+// them: no CTA waits for another and there is no second launch.  The work is
+// n / 32 steps a warp, so this form is kept for small n.  CTA (T, 0) counts
+// the experts for the offsets.
+template <int VB>
+__global__ void __launch_bounds__(kRowThreads)
+dispatch_small_kernel(const int32_t *__restrict__ ids, int64_t ldid, const char *__restrict__ X, int64_t ldx_bytes,
+                      int T, int k, int E, int nvec, int32_t *__restrict__ pos, int32_t *__restrict__ order,
+                      int32_t *__restrict__ offsets, char *__restrict__ Xs, int64_t ldxs_bytes)
+{
+    extern __shared__ int s_ids[];
+    __shared__ int s_pos[kMaxTopk];
+    __shared__ int scratch[33];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = T * k, t = blockIdx.x;
+    if (t == T) {
+        if (blockIdx.y) return;
+        int *hist = s_ids;                          // E ints
+        for (int e = tid; e < E; e += kRowThreads) hist[e] = 0;
+        __syncthreads();
+        for (int f = tid; f < n; f += kRowThreads) {
+            const int id = load_id(ids, ldid, k, f, E);
+            if (id >= 0) atomicAdd(&hist[id], 1);   // whole numbers: any order gives the same counts
+        }
+        __syncthreads();
+        const int per = (E + kRowThreads - 1) / kRowThreads;
+        int sum = 0, total = 0;
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < E) sum += hist[tid * per + i];
+        int run = block_exclusive_scan(sum, scratch, &total);
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < E) {
+                offsets[e] = run;
+                run += hist[e];
+            }
+        }
+        if (tid == 0) offsets[E] = total;
+        if (order)
+            for (int p = total + tid; p < n; p += kRowThreads) order[p] = -1;
+        return;
+    }
+    for (int f = tid; f < n; f += kRowThreads) s_ids[f] = load_id(ids, ldid, k, f, E);
+    __syncthreads();
+    for (int j = warp; j < k; j += kRowThreads / 32) {
+        const int f = t * k + j, id = s_ids[f];
+        int before = 0;
+        for (int i = lane; i < n; i += 32) {
+            const int o = s_ids[i];
+            before += (o >= 0 && (o < id || (o == id && i < f))) ? 1 : 0;
+        }
+        before = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)before);
+        if (lane == 0) {
+            const int p = id >= 0 ? before : -1;
+            s_pos[j] = p;
+            if (blockIdx.y == 0) {
+                pos[f] = p;
+                if (order && p >= 0) order[p] = f;
+            }
+        }
+    }
+    if (nvec == 0) return;
+    __syncthreads();
+    const int per = (nvec + gridDim.y - 1) / gridDim.y;
+    const int v0 = blockIdx.y * per, v1 = min(nvec, v0 + per);
+    copy_row<VB>(X + (int64_t)t * ldx_bytes, Xs, ldxs_bytes, s_pos, k, v0, v1);
+}
+
+// ------------------------------------------------------------------ dispatch, many entries: sort, then copy
+// One cluster of 8 CTAs sorts: each warp owns a run of consecutive entries, so
+// counting per (CTA, warp, expert) and adding in that order keeps the sort
+// stable.  Pass 1 counts (entries of the same expert among 32 lanes found by
+// match_any; one lane adds for all), then counts are summed over the warps and,
+// through distributed shared memory, over the CTAs, and pass 2 walks the same
+// entries handing out places.  No workspace, no atomics, no second launch.
+__global__ void __launch_bounds__(1024)
+expert_sort_kernel(const int32_t *__restrict__ ids, int64_t ldid, int k, int n, int E, int32_t *__restrict__ pos,
+                   int32_t *__restrict__ order, int32_t *__restrict__ offsets)
+{
+    extern __shared__ int smem[];
+    __shared__ int scratch[33];
+    const int W = blockDim.x >> 5;
+    int *hist = smem;                  // [W][E]
+    int *mine = smem + W * E;          // [E] counts of this CTA, read by the others
+    int *base = mine + E;              // [E] first place of this CTA's entries
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster_ctarank();
+    griddep_launch_dependents();
+    for (int i = tid; i < W * E; i += blockDim.x) hist[i] = 0;
+    griddep_wait();
+    __syncthreads();
+    const int seg = ((n + kSortCluster * W - 1) / (kSortCluster * W) + 31) / 32 * 32;
+    const int64_t f0 = (int64_t)(rank * W + warp) * seg;
+    const int steps = f0 < n ? (int)((min((int64_t)n, f0 + seg) - f0 + 31) / 32) : 0;
+    int *wh = hist + warp * E;
+    constexpr int U = 4;
+    for (int s = 0; s < steps; s += U) {
+        int id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
+            id[u] = (s + u < steps && f < n) ? load_id(ids, ldid, k, (int)f, E) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, id[u]);
+            if (id[u] >= 0 && lane == __ffs(same) - 1) wh[id[u]] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) {
+        int run = 0;
+        for (int w = 0; w < W; ++w) {
+            const int c = hist[w * E + e];
+            hist[w * E + e] = run;
+            run += c;
+        }
+        mine[e] = run;
+    }
+    cluster_arrive_release();          // every CTA's counts are in place
+    cluster_wait_acquire();
+    const int per = (E + blockDim.x - 1) / blockDim.x;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e >= E) break;
+        int before = 0, all = 0;
+        const uint32_t at = smem_u32(mine + e);
+#pragma unroll
+        for (int r = 0; r < kSortCluster; ++r) {
+            uint32_t c;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(mapa_shared(at, r)) : "memory");
+            if (r < rank) before += (int)c;
+            all += (int)c;
+        }
+        base[e] = sum + before;        // less the threads before this one: added below
+        if (rank == 0) offsets[e] = sum;
+        sum += all;
+    }
+    cluster_arrive_release();          // this CTA reads the others' counts no more
+    int total = 0;
+    const int first = block_exclusive_scan(sum, scratch, &total);
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e >= E) break;
+        base[e] += first;
+        if (rank == 0) offsets[e] += first;
+    }
+    if (rank == 0 && tid == 0) offsets[E] = total;
+    if (order)
+        for (int64_t p = (int64_t)total + rank * blockDim.x + tid; p < n; p += kSortCluster * blockDim.x) order[p] = -1;
+    __syncthreads();
+    for (int s = 0; s < steps; s += U) {
+        int id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
+            id[u] = (s + u < steps && f < n) ? load_id(ids, ldid, k, (int)f, E) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, id[u]);
+            const int p = id[u] >= 0 ? base[id[u]] + wh[id[u]] + __popc(same & ((1u << lane) - 1)) : -1;
+            __syncwarp();
+            if (id[u] >= 0 && lane == __ffs(same) - 1) wh[id[u]] += __popc(same);
+            __syncwarp();
+            if (s + u < steps && f < n) {
+                pos[f] = p;
+                if (order && p >= 0) order[p] = (int)f;
+            }
+        }
+    }
+    cluster_wait_acquire();            // no CTA leaves while its counts may be read
+}
+
+// Grid (T, chunks): the copies of a token's row, the places read from `pos`.
+template <int VB>
+__global__ void __launch_bounds__(kRowThreads)
+dispatch_copy_kernel(const int32_t *__restrict__ pos, const char *__restrict__ X, int64_t ldx_bytes, int k, int nvec,
+                     char *__restrict__ Xs, int64_t ldxs_bytes)
+{
+    __shared__ int s_pos[kMaxTopk];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t t = blockIdx.x;
+    for (int j = threadIdx.x; j < k; j += kRowThreads) s_pos[j] = __ldcg(pos + t * k + j);
+    __syncthreads();
+    const int per = (nvec + gridDim.y - 1) / gridDim.y;
+    const int v0 = blockIdx.y * per, v1 = min(nvec, v0 + per);
+    copy_row<VB>(X + t * ldx_bytes, Xs, ldxs_bytes, s_pos, k, v0, v1);
+}
+
+// ------------------------------------------------------------------ fp32 <-> stored types
+// V elements of a bf16 or fp32 row as fp32, through L2 (rows may have just been
+// written by the preceding kernel).  V is 8 (bf16) or 4 (fp32): 16 bytes; or 1.
+template <bool BF16, int V>
+__device__ __forceinline__ void load_row(const char *row, int64_t el, float (&v)[V]) {
+    if constexpr (BF16 && V == 8) {
+        const uint4 q = ldg_v4(row + el * 2);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
+    } else if constexpr (!BF16 && V == 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(row + el * 4));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else if constexpr (BF16) {
+        v[0] = bf16_one(ldg_u16(row + el * 2));
+    } else {
+        v[0] = __ldcg(reinterpret_cast<const float *>(row + el * 4));
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_rn(lo) | ((uint32_t)f32_to_bf16_rn(hi) << 16);
+}
+template <bool BF16, int V>
+__device__ __forceinline__ void store_row(char *row, int64_t el, const float (&v)[V]) {
+    if constexpr (BF16 && V == 8) {
+        *reinterpret_cast<uint4 *>(row + el * 2) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else if constexpr (BF16 && V == 4) {
+        *reinterpret_cast<uint2 *>(row + el * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (BF16) {
+        *reinterpret_cast<uint16_t *>(row + el * 2) = f32_to_bf16_rn(v[0]);
+    } else if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(row + el * 4 + 4 * i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+        *reinterpret_cast<float *>(row + el * 4) = v[0];
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// Grid (T, chunks), one vector of the token's row per thread: its k rows'
+// vectors are loaded eight at a time before they are added, in order of j.
+constexpr int kCombineThreads = 128;
+template <bool IN16, bool OUT16, int V>
+__global__ void __launch_bounds__(kCombineThreads)
+combine_kernel(const char *__restrict__ Ys, int64_t ldys_bytes, int rows, const int32_t *__restrict__ pos,
+               const float *__restrict__ weights, int64_t ldw, int k, int H, char *__restrict__ Y, int64_t ldy_bytes)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t t = blockIdx.x;
+    const int64_t el = ((int64_t)blockIdx.y * kCombineThreads + threadIdx.x) * V;
+    if (el >= H) return;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    constexpr int U = 8;
+    for (int j0 = 0; j0 < k; j0 += U) {
+        float r[U][V], w[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = j0 + u < k ? __ldcg(pos + t * k + j0 + u) : -1;
+            live[u] = (unsigned)p < (unsigned)rows;
+            if (live[u]) {
+                w[u] = weights ? __ldcg(weights + t * ldw + j0 + u) : 1.f;
+                load_row<IN16, V>(Ys + (int64_t)p * ldys_bytes, el, r[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (live[u]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u], r[u][i], acc[i]);
+            }
+    }
+    store_row<OUT16, V>(Y + t * ldy_bytes, el, acc);
+}
+
+// ------------------------------------------------------------------ gradient of combine
+// One CTA per token, eight entries at a time: dY[t] is read once per eight
+// entries, each Ys row read and each dYs row written once; the dot products
+// stay in registers until one block reduction in a fixed order.
+template <bool B16, int V, bool DW>
+__global__ void __launch_bounds__(kRowThreads)
+combine_grad_kernel(const char *__restrict__ dY, int64_t lddy_bytes, const char *__restrict__ Ys, int64_t ldys_bytes,
+                    int rows, const int32_t *__restrict__ pos, const float *__restrict__ weights, int64_t ldw, int k,
+                    int H, char *__restrict__ dYs, int64_t lddys_bytes, float *__restrict__ dw, int64_t lddw)
+{
+    constexpr int U = 8;
+    __shared__ float part[kRowThreads / 32][U];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const char *dy = dY + t * lddy_bytes;
+    for (int j0 = 0; j0 < k; j0 += U) {
+        int p[U];
+        float w[U], dot[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u] = j0 + u < k ? __ldcg(pos + t * k + j0 + u) : -1;
+            if ((unsigned)p[u] >= (unsigned)rows) p[u] = -1;
+            w[u] = (weights && p[u] >= 0) ? __ldcg(weights + t * ldw + j0 + u) : 1.f;
+            dot[u] = 0.f;
+        }
+        for (int64_t el = (int64_t)tid * V; el < H; el += kRowThreads * V) {
+            float g[V], r[U][V];
+            load_row<B16, V>(dy, el, g);
+            if constexpr (DW) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (p[u] >= 0) load_row<B16, V>(Ys + (int64_t)p[u] * ldys_bytes, el, r[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (p[u] >= 0) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        o[i] = w[u] * g[i];
+                        if constexpr (DW) dot[u] = fmaf(g[i], r[u][i], dot[u]);
+                    }
+                    store_row<B16, V>(dYs + (int64_t)p[u] * lddys_bytes, el, o);
+                }
+        }
+        if constexpr (DW) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
+                if (lane == 0) part[warp][u] = dot[u];
+            }
+            __syncthreads();
+            if (tid < U && j0 + tid < k) {
+                float s = 0.f;
+                for (int v = 0; v < kRowThreads / 32; ++v) s += part[v][tid];
+                dw[t * lddw + j0 + tid] = s;       // a dropped entry added nothing: 0
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launches
+cudaError_t launch(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl, int cluster,
+                   void **args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Widest vector that every row start and the row length allow.
+int vec_bytes(int64_t row_bytes, int el_bytes, uintptr_t all) {
+    for (int v = 16; v > el_bytes; v >>= 1)
+        if (all % v == 0 && row_bytes % v == 0) return v;
+    return el_bytes;
+}
+
+// CTAs along a row of `nvec` vectors for T tokens: two CTAs per SM while each
+// still has a vector per thread.
+int row_chunks(int64_t T, int nvec, int num_sms) {
+    const int64_t want = (2ll * num_sms + T - 1) / T;
+    const int64_t most = (nvec + kRowThreads - 1) / kRowThreads;
+    return (int)(want < most ? want : (most > 0 ? most : 1));
+}
+
+// Entries up to which the one-launch form is taken.
+constexpr int kSmallEntries = 1024;
+
+template <int VB>
+cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStream_t stream, bool pdl) {
+    const char *X = static_cast<const char *>(a.X);
+    char *Xs = static_cast<char *>(a.Xs);
+    int64_t ldx = a.ldx * a.el_bytes, ldxs = a.ldxs * a.el_bytes, ldid = a.ldid;
+    int T = a.T, k = a.k, E = a.E, n = a.T * a.k;
+    const int32_t *ids = a.ids;
+    int32_t *pos = a.pos, *order = a.order, *offsets = a.offsets;
+    if (n <= kSmallEntries) {
+        const int smem = 4 * (n > E ? n : E);
+        void *args[] = {&ids, &ldid, &X, &ldx, &T, &k, &E, &nvec, &pos, &order, &offsets, &Xs, &ldxs};
+        return launch((const void *)dispatch_small_kernel<VB>, dim3(T + 1, T ? row_chunks(T, nvec, num_sms) : 1),
+                      kRowThreads, smem, stream, pdl, 1, args);
+    }
+    int W = kSortSmem / 4 / E - 2;
+    if (W > 32) W = 32;
+    void *args[] = {&ids, &ldid, &k, &n, &E, &pos, &order, &offsets};
+    cudaError_t e = launch((const void *)expert_sort_kernel, dim3(kSortCluster), 32 * W, 4 * (W + 2) * E, stream, pdl,
+                           kSortCluster, args);
+    if (e != cudaSuccess || nvec == 0) return e;
+    const int32_t *cpos = pos;
+    void *cargs[] = {&cpos, &X, &ldx, &k, &nvec, &Xs, &ldxs};
+    return launch((const void *)dispatch_copy_kernel<VB>, dim3(T, row_chunks(T, nvec, num_sms)), kRowThreads, 0,
+                  stream, pdl, 1, cargs);
+}
+
+template <bool IN16, bool OUT16, int V>
+cudaError_t combine_vec(const CombineArgs &a, cudaStream_t stream, bool pdl) {
+    const char *Ys = static_cast<const char *>(a.Ys);
+    char *Y = static_cast<char *>(a.Y);
+    int64_t ldys = a.ldys * (IN16 ? 2 : 4), ldy = a.ldy * (OUT16 ? 2 : 4), ldw = a.ldw;
+    int rows = a.rows, k = a.k, H = a.H;
+    const int32_t *pos = a.pos;
+    const float *w = a.weights;
+    const int per = kCombineThreads * V;
+    void *args[] = {&Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &Y, &ldy};
+    return launch((const void *)combine_kernel<IN16, OUT16, V>, dim3(a.T, (H + per - 1) / per), kCombineThreads, 0,
+                  stream, pdl, 1, args);
+}
+
+template <bool B16, int V, bool DW>
+cudaError_t grad_vec(const CombineGradArgs &a, cudaStream_t stream, bool pdl) {
+    const int b = B16 ? 2 : 4;
+    const char *dY = static_cast<const char *>(a.dY), *Ys = static_cast<const char *>(a.Ys);
+    char *dYs = static_cast<char *>(a.dYs);
+    int64_t lddy = a.lddy * b, ldys = a.ldys * b, lddys = a.lddys * b, ldw = a.ldw, lddw = a.lddw;
+    int rows = a.rows, k = a.k, H = a.H;
+    const int32_t *pos = a.pos;
+    const float *w = a.weights;
+    float *dw = a.dweights;
+    void *args[] = {&dY, &lddy, &Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &dYs, &lddys, &dw, &lddw};
+    return launch((const void *)combine_grad_kernel<B16, V, DW>, dim3(a.T), kRowThreads, 0, stream, pdl, 1, args);
+}
+
+uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+}  // namespace
+
+cudaError_t expert_rows_prepare() { return set_max_dyn_smem(&expert_sort_kernel); }
+
+cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    const int64_t row = (int64_t)a.H * a.el_bytes;
+    const bool rows = a.X != nullptr && row > 0;
+    const int vb = rows ? vec_bytes(row, a.el_bytes,
+                                    u(a.X) | u(a.Xs) | (uintptr_t)(a.ldx * a.el_bytes) | (uintptr_t)(a.ldxs * a.el_bytes))
+                        : 16;
+    const int nvec = rows ? (int)(row / vb) : 0;
+    switch (vb) {
+        case 16: return dispatch_vec<16>(a, nvec, num_sms, stream, pdl);
+        case 8: return dispatch_vec<8>(a, nvec, num_sms, stream, pdl);
+        case 4: return dispatch_vec<4>(a, nvec, num_sms, stream, pdl);
+        default: return dispatch_vec<2>(a, nvec, num_sms, stream, pdl);
+    }
+}
+
+cudaError_t launch_combine(const CombineArgs &a, cudaStream_t stream, bool pdl) {
+    // 16-byte loads where every row starts and ends on one, element by element elsewhere
+    const int ib = a.in16 ? 2 : 4, ob = a.out16 ? 2 : 4, V = 16 / ib;
+    const bool wide = a.H % V == 0 && u(a.Ys) % 16 == 0 && (a.ldys * ib) % 16 == 0 && u(a.Y) % (V * ob > 16 ? 16 : V * ob) == 0 &&
+                      (a.ldy * ob) % (V * ob > 16 ? 16 : V * ob) == 0;
+    if (a.in16 && a.out16) return wide ? combine_vec<true, true, 8>(a, stream, pdl) : combine_vec<true, true, 1>(a, stream, pdl);
+    if (a.in16) return wide ? combine_vec<true, false, 8>(a, stream, pdl) : combine_vec<true, false, 1>(a, stream, pdl);
+    if (a.out16) return wide ? combine_vec<false, true, 4>(a, stream, pdl) : combine_vec<false, true, 1>(a, stream, pdl);
+    return wide ? combine_vec<false, false, 4>(a, stream, pdl) : combine_vec<false, false, 1>(a, stream, pdl);
+}
+
+cudaError_t launch_combine_grad(const CombineGradArgs &a, cudaStream_t stream, bool pdl) {
+    const int b = a.b16 ? 2 : 4;
+    const uintptr_t all = u(a.dY) | u(a.dYs) | (uintptr_t)(a.lddy * b) | (uintptr_t)(a.lddys * b) |
+                          (a.dweights ? u(a.Ys) | (uintptr_t)(a.ldys * b) : 0);
+    const bool wide = all % 16 == 0 && a.H % (16 / b) == 0;
+    if (a.b16) {
+        if (a.dweights) return wide ? grad_vec<true, 8, true>(a, stream, pdl) : grad_vec<true, 1, true>(a, stream, pdl);
+        return wide ? grad_vec<true, 8, false>(a, stream, pdl) : grad_vec<true, 1, false>(a, stream, pdl);
+    }
+    if (a.dweights) return wide ? grad_vec<false, 4, true>(a, stream, pdl) : grad_vec<false, 1, true>(a, stream, pdl);
+    return wide ? grad_vec<false, 4, false>(a, stream, pdl) : grad_vec<false, 1, false>(a, stream, pdl);
+}
+
+}  // namespace skinny

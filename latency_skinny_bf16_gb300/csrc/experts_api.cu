@@ -1,0 +1,135 @@
+// experts_api.cu -- the C ABI of skinny_experts.h: argument checks and
+// launches.  Every argument is checked on the host before anything is
+// launched; no entry point throws, allocates or synchronises.
+#include <initializer_list>
+
+#include "expert_rows.h"
+#include "skinny_experts.h"
+
+namespace skinny {
+namespace {
+
+int el_bytes(int dtype) { return dtype == SKINNY_BF16 ? 2 : 4; }
+bool dtype_ok(int d) { return d == SKINNY_BF16 || d == SKINNY_F32; }
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+bool aligned(const void *p, int bytes) { return addr(p) % (uintptr_t)bytes == 0; }
+
+// The bytes [lo, hi) that a matrix of `rows` rows of `cols` elements occupies.
+struct Range {
+    uintptr_t lo, hi;
+};
+Range span(const void *p, int64_t rows, int64_t cols, int64_t ld, int el) {
+    if (!p || rows <= 0 || cols <= 0) return {0, 0};
+    return {addr(p), addr(p) + (uintptr_t)(((rows - 1) * ld + cols) * el)};
+}
+// Whether a range that is written meets one of the others.
+bool meets(const Range &w, std::initializer_list<Range> others) {
+    for (const Range &o : others)
+        if (w.lo < w.hi && o.lo < o.hi && ranges_overlap(w.lo, w.hi, o.lo, o.hi)) return true;
+    return false;
+}
+
+skinny_status_t launched(cudaError_t e) { return e == cudaSuccess ? SKINNY_OK : SKINNY_ERR_LAUNCH; }
+
+// T, k and H of a call on the router's entries.
+skinny_status_t check_entries(int T, int k, int H) {
+    if (T < 0 || k < 0 || H < 0) return SKINNY_ERR_INVALID_VALUE;
+    if (k > kMaxTopk || (int64_t)T * k >= (1ll << 31) || H > SKINNY_MAX_WIDTH) return SKINNY_ERR_UNSUPPORTED;
+    return SKINNY_OK;
+}
+
+}  // namespace
+}  // namespace skinny
+
+using namespace skinny;
+
+extern "C" {
+
+skinny_status_t skinny_expert_dispatch(const int32_t *ids, int ldid, const void *X, int ldx, int T, int k, int E,
+                                       int H, int dtype, int32_t *pos, int32_t *order, int32_t *offsets, void *Xs,
+                                       int ldxs, void *stream) {
+    skinny_status_t st = check_entries(T, k, X ? H : 0);
+    if (st != SKINNY_OK) return st;
+    if (E < 1) return SKINNY_ERR_INVALID_VALUE;
+    if (E > kMaxSortExperts) return SKINNY_ERR_UNSUPPORTED;
+    if (!offsets) return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(offsets, 4)) return SKINNY_ERR_MISALIGNED;
+    if (k == 0) T = 0;
+    DispatchArgs a{ids, ldid, nullptr, 0, T, k, E, 0, 2, pos, order, offsets, nullptr, 0};
+    if (T > 0) {
+        const int64_t n = (int64_t)T * k;
+        if (!ids || !pos || ldid < k) return SKINNY_ERR_INVALID_VALUE;
+        if (!aligned(ids, 4) || !aligned(pos, 4) || !aligned(order, 4)) return SKINNY_ERR_MISALIGNED;
+        Range x{0, 0}, xs{0, 0};
+        if (X && H != 0) {
+            if (!dtype_ok(dtype) || !Xs || ldx < H || ldxs < H) return SKINNY_ERR_INVALID_VALUE;
+            const int b = el_bytes(dtype);
+            if (!aligned(X, b) || !aligned(Xs, b)) return SKINNY_ERR_MISALIGNED;
+            x = span(X, T, H, ldx, b);
+            xs = span(Xs, n, H, ldxs, b);
+            a.X = X; a.ldx = ldx; a.H = H; a.el_bytes = b; a.Xs = Xs; a.ldxs = ldxs;
+        }
+        const Range i = span(ids, T, k, ldid, 4), p = span(pos, 1, n, n, 4), o = span(order, 1, n, n, 4),
+                    f = span(offsets, 1, E + 1, E + 1, 4);
+        if (meets(xs, {x, i, p, o, f}) || meets(p, {x, i, o, f}) || meets(o, {x, i, f}) || meets(f, {x, i}))
+            return SKINNY_ERR_INVALID_VALUE;
+    }
+    CallCtx c;
+    st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    return launched(launch_dispatch(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
+}
+
+skinny_status_t skinny_expert_combine(const void *Ys, int ldys, int rows, const int32_t *pos, const float *weights,
+                                      int ldw, int T, int k, int H, int in_dtype, int out_dtype, void *Y, int ldy,
+                                      void *stream) {
+    skinny_status_t st = check_entries(T, k, H);
+    if (st != SKINNY_OK) return st;
+    if (rows < 0 || !dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return SKINNY_ERR_INVALID_VALUE;
+    if (T == 0 || H == 0) return SKINNY_OK;
+    const int ib = el_bytes(in_dtype), ob = el_bytes(out_dtype);
+    if (!Y || ldy < H) return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(Y, ob)) return SKINNY_ERR_MISALIGNED;
+    if (k > 0) {
+        if (!pos || (rows > 0 && (!Ys || ldys < H)) || (weights && ldw < k)) return SKINNY_ERR_INVALID_VALUE;
+        if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(Ys, ib)) return SKINNY_ERR_MISALIGNED;
+        if (meets(span(Y, T, H, ldy, ob), {span(Ys, rows, H, ldys, ib), span(pos, 1, (int64_t)T * k, 0, 4),
+                                           span(weights, T, k, ldw, 4)}))
+            return SKINNY_ERR_INVALID_VALUE;
+    }
+    CallCtx c;
+    st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    const CombineArgs a{Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype == SKINNY_BF16, out_dtype == SKINNY_BF16,
+                        Y, ldy};
+    return launched(launch_combine(a, static_cast<cudaStream_t>(stream), c.pdl));
+}
+
+skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void *Ys, int ldys, int rows,
+                                           const int32_t *pos, const float *weights, int ldw, int T, int k, int H,
+                                           int dtype, void *dYs, int lddys, float *dweights, int lddw, void *stream) {
+    skinny_status_t st = check_entries(T, k, H);
+    if (st != SKINNY_OK) return st;
+    if (rows < 0 || !dtype_ok(dtype)) return SKINNY_ERR_INVALID_VALUE;
+    if (T == 0 || k == 0 || (H == 0 && !dweights)) return SKINNY_OK;
+    const int b = el_bytes(dtype);
+    if (!pos || (weights && ldw < k) || (dweights && lddw < k)) return SKINNY_ERR_INVALID_VALUE;
+    if (H > 0 && (!dY || lddy < H || (rows > 0 && (!dYs || lddys < H)) ||
+                  (rows > 0 && dweights && (!Ys || ldys < H))))
+        return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dweights, 4) || !aligned(dY, b) || !aligned(dYs, b) ||
+        (dweights && !aligned(Ys, b)))
+        return SKINNY_ERR_MISALIGNED;
+    const Range g = span(dY, T, H, lddy, b), y = dweights ? span(Ys, rows, H, ldys, b) : Range{0, 0},
+                p = span(pos, 1, (int64_t)T * k, 0, 4), w = span(weights, T, k, ldw, 4),
+                gy = span(dYs, rows, H, lddys, b), gw = span(dweights, T, k, lddw, 4);
+    if (meets(gy, {g, y, p, w, gw}) || meets(gw, {g, y, p, w})) return SKINNY_ERR_INVALID_VALUE;
+    CallCtx c;
+    st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    const CombineGradArgs a{dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype == SKINNY_BF16, dYs, lddys,
+                            dweights, lddw};
+    return launched(launch_combine_grad(a, static_cast<cudaStream_t>(stream), c.pdl));
+}
+
+}  // extern "C"

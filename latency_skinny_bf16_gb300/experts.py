@@ -1,0 +1,240 @@
+"""Around the router and the decode projections of a mixture-of-experts layer:
+tokens sorted by expert and back with their gradients, the experts' products,
+and a shared projection with a low-rank adapter per token.
+
+As in the package itself, the ``skinny_*`` functions carry the C names of
+``include/skinny_experts.h`` and only marshal arguments; the tensor functions
+(:func:`expert_dispatch`, :func:`expert_combine`, :func:`expert_combine_grad`,
+:func:`experts_gemm`, :func:`lora_gemm`) take CUDA tensors, allocate what is
+not given on the stream they launch on, and raise on a refusal.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import latency_skinny_bf16_gb300 as _sk
+
+SKINNY_BF16 = 0
+SKINNY_F32 = 1
+SKINNY_ACT_NONE = 0
+SKINNY_ACT_SWIGLU = 1
+SKINNY_MAX_TOPK = 64
+SKINNY_MAX_SORT_EXPERTS = 8192
+SKINNY_MAX_EXPERTS = 1024
+SKINNY_MAX_RANK = 256
+SKINNY_MAX_WIDTH = 1 << 20
+
+__all__ = [
+    "SKINNY_BF16", "SKINNY_F32", "SKINNY_ACT_NONE", "SKINNY_ACT_SWIGLU", "SKINNY_MAX_TOPK", "SKINNY_MAX_SORT_EXPERTS",
+    "SKINNY_MAX_EXPERTS", "SKINNY_MAX_RANK", "SKINNY_MAX_WIDTH",
+    "skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad",
+    "expert_dispatch", "expert_combine", "expert_combine_grad",
+]
+
+_ACTS = {"none": SKINNY_ACT_NONE, None: SKINNY_ACT_NONE, "swiglu": SKINNY_ACT_SWIGLU}
+
+SYMBOLS = ("skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad")
+
+
+def bind(lib: ctypes.CDLL) -> None:
+    vp, i = ctypes.c_void_p, ctypes.c_int
+    lib.skinny_expert_dispatch.argtypes = [vp, i, vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp]
+    lib.skinny_expert_combine.argtypes = [vp, i, i, vp, vp, i, i, i, i, i, i, vp, i, vp]
+    lib.skinny_expert_combine_grad.argtypes = [vp, i, vp, i, i, vp, vp, i, i, i, i, i, vp, i, vp, i, vp]
+    for name in SYMBOLS:
+        getattr(lib, name).restype = i
+
+
+# ---------------------------------------------------------------- C-named wrappers (raw pointers)
+
+def skinny_expert_dispatch(ids: int, ldid: int, X: int, ldx: int, T: int, k: int, E: int, H: int, dtype: int,
+                           pos: int, order: int, offsets: int, Xs: int, ldxs: int, stream: int = 0) -> int:
+    """Raw C call; returns the skinny_status_t."""
+    return _sk.load_library().skinny_expert_dispatch(ids, ldid, X, ldx, T, k, E, H, dtype, pos, order, offsets, Xs,
+                                                     ldxs, stream)
+
+
+def skinny_expert_combine(Ys: int, ldys: int, rows: int, pos: int, weights: int, ldw: int, T: int, k: int, H: int,
+                          in_dtype: int, out_dtype: int, Y: int, ldy: int, stream: int = 0) -> int:
+    """Raw C call; returns the skinny_status_t."""
+    return _sk.load_library().skinny_expert_combine(Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype, out_dtype,
+                                                    Y, ldy, stream)
+
+
+def skinny_expert_combine_grad(dY: int, lddy: int, Ys: int, ldys: int, rows: int, pos: int, weights: int, ldw: int,
+                               T: int, k: int, H: int, dtype: int, dYs: int, lddys: int, dweights: int, lddw: int,
+                               stream: int = 0) -> int:
+    """Raw C call; returns the skinny_status_t."""
+    return _sk.load_library().skinny_expert_combine_grad(dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype,
+                                                         dYs, lddys, dweights, lddw, stream)
+
+
+# ---------------------------------------------------------------- tensors
+
+def _dtype(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return SKINNY_BF16
+    if t.dtype == torch.float32:
+        return SKINNY_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+
+
+def _rows(t, name, dtype=None):
+    """Row stride of a CUDA matrix with unit column stride."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA matrix, not {tuple(t.shape)} on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    m, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} needs unit column stride")
+    if m <= 1:
+        return max(n, 1)
+    ld = t.stride(0)
+    if ld < n:
+        raise ValueError(f"{name} needs rows that do not overlap")
+    return ld
+
+
+def _flat(t, name, n, dtype):
+    """A contiguous CUDA tensor of n elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
+    return t
+
+
+class _On:
+    """The stream a call runs on: torch's current one, or the one that is given.
+    Tensors made inside are made on it, so their memory is not handed to
+    another stream's work while the call may still use it."""
+
+    def __init__(self, stream, device):
+        import torch
+        self.guard = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.handle = stream.cuda_stream
+            self.guard = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def expert_dispatch(ids, num_experts, x=None, xs=None, pos=None, order=None, offsets=None, stream=None):
+    """Tokens sorted by expert: for the router's ``ids`` int32 [T, k] (an id
+    outside ``[0, num_experts)`` drops the entry) returns ``(xs, pos, order,
+    offsets)``: ``xs`` [T*k, H] with ``x``'s rows in expert order (rows from
+    ``offsets[num_experts]`` on are left as they are; None without ``x``),
+    ``pos`` int32 [T, k] (-1: dropped), ``order`` int32 [T*k], ``offsets``
+    int32 [num_experts + 1].  See ``skinny_expert_dispatch``."""
+    import torch
+    ldid = _rows(ids, "ids", torch.int32)
+    T, k = ids.shape
+    with _On(stream, ids.device) as s:
+        if pos is None:
+            pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+        if order is None:
+            order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
+        if offsets is None:
+            offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
+        _flat(pos, "pos", T * k, torch.int32)
+        _flat(order, "order", T * k, torch.int32)
+        _flat(offsets, "offsets", num_experts + 1, torch.int32)
+        if x is None:
+            st = skinny_expert_dispatch(ids.data_ptr(), ldid, 0, 0, T, k, num_experts, 0, 0, pos.data_ptr(),
+                                        order.data_ptr(), offsets.data_ptr(), 0, 0, s)
+        else:
+            ldx, dt = _rows(x, "x"), _dtype(x, "x")
+            H = x.shape[1]
+            if x.shape[0] != T:
+                raise ValueError(f"x has {x.shape[0]} rows, ids {T}")
+            if xs is None:
+                xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+            ldxs = _rows(xs, "xs", x.dtype)
+            if tuple(xs.shape) != (T * k, H):
+                raise ValueError(f"xs must be {(T * k, H)}, not {tuple(xs.shape)}")
+            st = skinny_expert_dispatch(ids.data_ptr(), ldid, x.data_ptr(), ldx, T, k, num_experts, H, dt,
+                                        pos.data_ptr(), order.data_ptr(), offsets.data_ptr(), xs.data_ptr(), ldxs, s)
+    if st != _sk.SKINNY_OK:
+        raise _sk.SkinnyError(st, "skinny_expert_dispatch")
+    return xs, pos, order, offsets
+
+
+def _weights(weights, T, k):
+    import torch
+    if weights is None:
+        return 0, 0
+    if tuple(weights.shape) != (T, k):
+        raise ValueError(f"weights must be {(T, k)}, not {tuple(weights.shape)}")
+    return weights.data_ptr(), _rows(weights, "weights", torch.float32)
+
+
+def expert_combine(ys, pos, weights=None, out=None, stream=None):
+    """``out[t] = sum_j weights[t, j] * ys[pos[t, j]]`` over the live entries
+    (``0 <= pos < ys.shape[0]``), summed in fp32: ``ys`` bf16 or fp32 [rows,
+    H], ``pos`` int32 [T, k] from :func:`expert_dispatch`, ``weights`` fp32
+    [T, k] or None (ones: the gradient of dispatch's copies), ``out`` bf16 or
+    fp32 [T, H] (default: as ``ys``).  See ``skinny_expert_combine``."""
+    import torch
+    ldys, it = _rows(ys, "ys"), _dtype(ys, "ys")
+    rows, H = ys.shape
+    if pos.dim() != 2:
+        raise ValueError(f"pos must be [T, k], not {tuple(pos.shape)}")
+    T, k = pos.shape
+    _flat(pos, "pos", T * k, torch.int32)
+    wp, ldw = _weights(weights, T, k)
+    with _On(stream, ys.device) as s:
+        if out is None:
+            out = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+        ldy, ot = _rows(out, "out"), _dtype(out, "out")
+        if tuple(out.shape) != (T, H):
+            raise ValueError(f"out must be {(T, H)}, not {tuple(out.shape)}")
+        st = skinny_expert_combine(ys.data_ptr(), ldys, rows, pos.data_ptr(), wp, ldw, T, k, H, it, ot,
+                                   out.data_ptr(), ldy, s)
+    if st != _sk.SKINNY_OK:
+        raise _sk.SkinnyError(st, "skinny_expert_combine")
+    return out
+
+
+def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stream=None):
+    """The gradient of :func:`expert_combine` for ``dy`` [T, H]: returns
+    ``(dys, dweights)`` with ``dys[pos[t, j]] = weights[t, j] * dy[t]`` (the
+    type of ``dy``; rows no entry names are left as they are) and
+    ``dweights[t, j] = <dy[t], ys[pos[t, j]]>`` (fp32; 0 for a dropped entry).
+    See ``skinny_expert_combine_grad``."""
+    import torch
+    lddy, dt = _rows(dy, "dy"), _dtype(dy, "dy")
+    ldys = _rows(ys, "ys", dy.dtype)
+    T, H = dy.shape
+    rows = ys.shape[0]
+    if pos.dim() != 2 or pos.shape[0] != T or ys.shape[1] != H:
+        raise ValueError(f"shape mismatch: dy {tuple(dy.shape)}, ys {tuple(ys.shape)}, pos {tuple(pos.shape)}")
+    k = pos.shape[1]
+    _flat(pos, "pos", T * k, torch.int32)
+    wp, ldw = _weights(weights, T, k)
+    with _On(stream, dy.device) as s:
+        if dys is None:
+            dys = torch.empty((rows, H), dtype=dy.dtype, device=dy.device)
+        if dweights is None:
+            dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        lddys, lddw = _rows(dys, "dys", dy.dtype), _rows(dweights, "dweights", torch.float32)
+        if tuple(dys.shape) != (rows, H) or tuple(dweights.shape) != (T, k):
+            raise ValueError(f"dys must be {(rows, H)} and dweights {(T, k)}")
+        st = skinny_expert_combine_grad(dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, pos.data_ptr(), wp, ldw, T, k,
+                                        H, dt, dys.data_ptr(), lddys, dweights.data_ptr(), lddw, s)
+    if st != _sk.SKINNY_OK:
+        raise _sk.SkinnyError(st, "skinny_expert_combine_grad")
+    return dys, dweights
