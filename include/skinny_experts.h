@@ -96,6 +96,61 @@ SKINNY_API skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, 
                                                       int H, int dtype, void *dYs, int lddys, float *dweights,
                                                       int lddw, void *stream);
 
+/*
+ * The experts' products on rows in expert order: for every expert e and row r
+ * with offsets[e] <= r < offsets[e+1],
+ *
+ *     SKINNY_ACT_NONE:    Y[r,n] = sum_k Xs[r,k] * W[e][n][k]                         n < N, W [E, N, K]
+ *     SKINNY_ACT_SWIGLU:  Y[r,n] = g / (1 + exp(-g)) * u,  g = sum_k Xs[r,k] * W[e][n][k],
+ *                         u = sum_k Xs[r,k] * W[e][N+n][k]                             n < N, W [E, 2N, K]
+ *
+ * fp32 accumulation (sums as in skinny_gemm_bf16: bounded tensor-core chains,
+ * rounded adds), one rounding to out_dtype.  An expert without rows is not
+ * read.  Rows from offsets[E] on are left as they are.
+ *
+ *   Xs       device, bf16 [rows, K], row stride ldx >= K
+ *   offsets  device, int32 [E + 1], non-decreasing, from skinny_expert_dispatch (entries are
+ *            clamped to [0, rows])
+ *   W        device, bf16, row stride ldw >= K, expert stride ldwe >= (rows of an expert) * ldw (elements)
+ *   Y        device, out_dtype [rows, N], row stride ldy >= N; overlaps no input
+ *   1 <= E <= 1024; rows, N, K >= 0 (rows or N 0: no-op; K 0: zeros).
+ *
+ * With 16-byte aligned rows (pointers, ldx, ldw and ldwe multiples of 8
+ * elements) the tcgen05 kernel runs, else a CUDA-core kernel.  Both take any
+ * number of rows for an expert; they are built for decode (up to 64).
+ */
+SKINNY_API skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, const int32_t *offsets,
+                                                    const uint16_t *W, int ldw, int64_t ldwe, int E, int N, int K,
+                                                    int act, int out_dtype, void *Y, int ldy, void *stream);
+
+/*
+ * A shared projection with a low-rank adapter per token beside it: with
+ * a = adapters[m] and r_a = ranks[a] (R when ranks == NULL),
+ *
+ *     Y[m,n] = sum_k X[m,k] W[n,k] + scales[a] * sum_{r < r_a} ( sum_k X[m,k] A[a][r][k] ) * B[a][n][r]
+ *
+ * A token whose id is outside [0, L) has no adapter.  The inner sum is kept
+ * in fp32; Y is rounded once to out_dtype.  What A and B hold past r_a is not
+ * used.  ranks are clamped to [0, R]; scales == NULL takes 1.
+ *
+ *   X, W     as in skinny_gemm_bf16 (M <= 64, and its rules for M > 16)
+ *   A        device, bf16 [L, R, K], row stride lda >= K, adapter stride ldae
+ *   B        device, bf16 [L, N, R], row stride ldb >= R, adapter stride ldbe
+ *   adapters device, int32 [M];  ranks device, int32 [L] or NULL;  scales device, fp32 [L] or NULL
+ *   workspace  device, 16-byte aligned, skinny_lora_workspace(M, N, R, out_dtype) bytes, not shared
+ *            with a call that may run at the same time
+ *   0 <= R <= 256, L >= 0 (either 0: the projection alone).
+ */
+SKINNY_API skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t *W, int ldw,
+                                                 const uint16_t *A, int lda, int64_t ldae, const uint16_t *B, int ldb,
+                                                 int64_t ldbe, const int32_t *adapters, const int32_t *ranks,
+                                                 const float *scales, int L, int R, void *Y, int ldy, int M, int N,
+                                                 int K, int out_dtype, void *workspace, int64_t workspace_bytes,
+                                                 void *stream);
+
+/* Bytes of workspace skinny_lora_gemm_bf16 needs; 0 for sizes it refuses.  Host only. */
+SKINNY_API int64_t skinny_lora_workspace(int M, int N, int R, int out_dtype);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,6 +4,7 @@
 #include <initializer_list>
 
 #include "expert_rows.h"
+#include "experts_gemm.h"
 #include "skinny_experts.h"
 
 namespace skinny {
@@ -130,6 +131,85 @@ skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void 
     const CombineGradArgs a{dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype == SKINNY_BF16, dYs, lddys,
                             dweights, lddw};
     return launched(launch_combine_grad(a, static_cast<cudaStream_t>(stream), c.pdl));
+}
+
+skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, const int32_t *offsets,
+                                         const uint16_t *W, int ldw, int64_t ldwe, int E, int N, int K, int act,
+                                         int out_dtype, void *Y, int ldy, void *stream) {
+    if (E < 1 || rows < 0 || N < 0 || K < 0 || !dtype_ok(out_dtype) ||
+        (act != SKINNY_ACT_NONE && act != SKINNY_ACT_SWIGLU))
+        return SKINNY_ERR_INVALID_VALUE;
+    if (E > SKINNY_MAX_EXPERTS || N > SKINNY_MAX_WIDTH || K > SKINNY_MAX_WIDTH) return SKINNY_ERR_UNSUPPORTED;
+    if (rows == 0 || N == 0) return SKINNY_OK;
+    const int ob = el_bytes(out_dtype);
+    const int64_t wrows = act == SKINNY_ACT_SWIGLU ? 2ll * N : N;
+    if (!offsets || !Y || ldy < N) return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(offsets, 4) || !aligned(Y, ob)) return SKINNY_ERR_MISALIGNED;
+    const Range y = span(Y, rows, N, ldy, ob);
+    if (meets(y, {span(offsets, 1, E + 1, 0, 4)})) return SKINNY_ERR_INVALID_VALUE;
+    if (K > 0) {
+        if (!Xs || !W || ldx < K || ldw < K || (E > 1 && ldwe < wrows * ldw)) return SKINNY_ERR_INVALID_VALUE;
+        if (!aligned(Xs, 2) || !aligned(W, 2)) return SKINNY_ERR_MISALIGNED;
+        // the experts' matrices: E - 1 strides and the last one's rows
+        const Range w = {addr(W), addr(W) + (uintptr_t)(2 * ((E - 1) * ldwe + (wrows - 1) * ldw + K))};
+        if (meets(y, {span(Xs, rows, K, ldx, 2), w})) return SKINNY_ERR_INVALID_VALUE;
+    }
+    CallCtx c;
+    const skinny_status_t st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    const ExpertsArgs a{Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act == SKINNY_ACT_SWIGLU,
+                        out_dtype == SKINNY_BF16, Y, ldy};
+    return launched(launch_experts_dot(a, c, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t skinny_lora_workspace(int M, int N, int R, int out_dtype) {
+    if (M < 0 || M > SKINNY_MAX_M || N < 0 || R < 0 || R > SKINNY_MAX_RANK || !dtype_ok(out_dtype)) return 0;
+    // V, then (bf16 output) the projection in fp32 that the adapters are added to before the one rounding
+    const int64_t v = ((int64_t)M * R * 4 + 15) / 16 * 16;
+    return v + (out_dtype == SKINNY_BF16 ? (int64_t)M * N * 4 : 0);
+}
+
+skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const uint16_t *A,
+                                      int lda, int64_t ldae, const uint16_t *B, int ldb, int64_t ldbe,
+                                      const int32_t *adapters, const int32_t *ranks, const float *scales, int L, int R,
+                                      void *Y, int ldy, int M, int N, int K, int out_dtype, void *workspace,
+                                      int64_t workspace_bytes, void *stream) {
+    if (L < 0 || R < 0 || !dtype_ok(out_dtype)) return SKINNY_ERR_INVALID_VALUE;
+    if (R > SKINNY_MAX_RANK) return SKINNY_ERR_UNSUPPORTED;
+    const int ob = out_dtype == SKINNY_BF16;
+    const bool none = L == 0 || R == 0 || M <= 0 || N <= 0 || K <= 0;
+    skinny_status_t st = SKINNY_OK;
+    if (none) return run_gemm(X, ldx, W, ldw, Y, ldy, M, N, K, stream, ob);
+    if (M > SKINNY_MAX_M) return SKINNY_ERR_UNSUPPORTED;
+    if (!Y || ldy < N || !A || !B || !adapters || !workspace || lda < K || ldb < R ||
+        (L > 1 && (ldae < (int64_t)R * lda || ldbe < (int64_t)N * ldb)) ||
+        workspace_bytes < skinny_lora_workspace(M, N, R, out_dtype))
+        return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(Y, el_bytes(out_dtype)) || !aligned(A, 2) || !aligned(B, 2) || !aligned(adapters, 4) ||
+        !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(workspace, 16))
+        return SKINNY_ERR_MISALIGNED;
+    float *V = static_cast<float *>(workspace);
+    float *base = ob ? V + ((int64_t)M * R + 3) / 4 * 4 : static_cast<float *>(Y);
+    const int ldbase = ob ? N : ldy;
+    const Range y = span(Y, M, N, ldy, el_bytes(out_dtype)), x = span(X, M, K, ldx, 2), w = span(W, N, K, ldw, 2),
+                ws = {addr(workspace), addr(workspace) + (uintptr_t)skinny_lora_workspace(M, N, R, out_dtype)},
+                ra = {addr(A), addr(A) + (uintptr_t)(2 * ((L - 1) * ldae + (int64_t)(R - 1) * lda + K))},
+                rb = {addr(B), addr(B) + (uintptr_t)(2 * ((L - 1) * ldbe + (int64_t)(N - 1) * ldb + R))},
+                id = span(adapters, 1, M, 0, 4), rk = span(ranks, 1, L, 0, 4), sc = span(scales, 1, L, 0, 4);
+    if (meets(y, {x, w, ws, ra, rb, id, rk, sc}) || meets(ws, {x, w, ra, rb, id, rk, sc}))
+        return SKINNY_ERR_INVALID_VALUE;
+    st = check_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, 0);
+    if (st != SKINNY_OK) return st;
+    CallCtx c;
+    st = call_context(&c);
+    if (st != SKINNY_OK) return st;
+    const LoraArgs a{X, ldx, A, lda, ldae, B, ldb, ldbe, adapters, ranks, scales, L, R, M, N, K, V, base, ldbase, Y,
+                     ldy, ob};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_lora_shrink(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+    st = run_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, stream, 0);
+    if (st != SKINNY_OK) return st;
+    return launched(launch_lora_expand(a, c, s));
 }
 
 }  // extern "C"

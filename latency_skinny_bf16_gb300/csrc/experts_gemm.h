@@ -1,0 +1,64 @@
+// experts_gemm.h -- host-side declarations of the experts' products and of the
+// adapters beside a projection.
+#pragma once
+
+#include "internal.h"
+#include "skinny_experts.h"
+
+namespace skinny {
+
+struct ExpertsArgs {
+    const uint16_t *X;
+    int64_t ldx;
+    int rows;
+    const int32_t *offsets;
+    const uint16_t *W;
+    int64_t ldw, ldwe;   // row stride, expert stride (elements)
+    int E, N, K;
+    int swiglu;          // W holds 2N rows an expert: gates, then ups
+    int out_bf16;
+    void *Y;
+    int64_t ldy;
+};
+// CUDA cores, any alignment (experts_dot.cu); K == 0 included
+cudaError_t launch_experts_dot(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
+
+struct LoraArgs {
+    const uint16_t *X;
+    int64_t ldx;
+    const uint16_t *A;
+    int64_t lda, ldae;
+    const uint16_t *B;
+    int64_t ldb, ldbe;
+    const int32_t *adapters, *ranks;
+    const float *scales;
+    int L, R, M, N, K;
+    float *V;            // [M, R], written by the first kernel, read by the second
+    const float *base;   // fp32 [M, N] of the shared projection, row stride ldbase
+    int64_t ldbase;
+    void *Y;             // base itself (fp32), or bf16
+    int64_t ldy;
+    int out_bf16;
+};
+cudaError_t launch_lora_shrink(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
+cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
+
+// Elements per vector load (8, 4, 2 or 1 bf16) that every address and stride in `all` (bytes) allows.
+inline int bf16_vec(uintptr_t all) { return all % 16 == 0 ? 8 : all % 8 == 0 ? 4 : all % 4 == 0 ? 2 : 1; }
+
+inline cudaError_t launch_plain(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl,
+                                void **args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace skinny

@@ -28,12 +28,14 @@ __all__ = [
     "SKINNY_BF16", "SKINNY_F32", "SKINNY_ACT_NONE", "SKINNY_ACT_SWIGLU", "SKINNY_MAX_TOPK", "SKINNY_MAX_SORT_EXPERTS",
     "SKINNY_MAX_EXPERTS", "SKINNY_MAX_RANK", "SKINNY_MAX_WIDTH",
     "skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad",
-    "expert_dispatch", "expert_combine", "expert_combine_grad",
+    "skinny_experts_gemm_bf16", "skinny_lora_gemm_bf16", "skinny_lora_workspace",
+    "expert_dispatch", "expert_combine", "expert_combine_grad", "experts_gemm", "lora_gemm", "lora_workspace",
 ]
 
 _ACTS = {"none": SKINNY_ACT_NONE, None: SKINNY_ACT_NONE, "swiglu": SKINNY_ACT_SWIGLU}
 
-SYMBOLS = ("skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad")
+SYMBOLS = ("skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad", "skinny_experts_gemm_bf16",
+           "skinny_lora_gemm_bf16", "skinny_lora_workspace")
 
 
 def bind(lib: ctypes.CDLL) -> None:
@@ -41,8 +43,14 @@ def bind(lib: ctypes.CDLL) -> None:
     lib.skinny_expert_dispatch.argtypes = [vp, i, vp, i, i, i, i, i, i, vp, vp, vp, vp, i, vp]
     lib.skinny_expert_combine.argtypes = [vp, i, i, vp, vp, i, i, i, i, i, i, vp, i, vp]
     lib.skinny_expert_combine_grad.argtypes = [vp, i, vp, i, i, vp, vp, i, i, i, i, i, vp, i, vp, i, vp]
+    ll = ctypes.c_int64
+    lib.skinny_experts_gemm_bf16.argtypes = [vp, i, i, vp, vp, i, ll, i, i, i, i, i, vp, i, vp]
+    lib.skinny_lora_gemm_bf16.argtypes = [vp, i, vp, i, vp, i, ll, vp, i, ll, vp, vp, vp, i, i, vp, i, i, i, i, i, vp,
+                                          ll, vp]
+    lib.skinny_lora_workspace.argtypes = [i, i, i, i]
     for name in SYMBOLS:
         getattr(lib, name).restype = i
+    lib.skinny_lora_workspace.restype = ll
 
 
 # ---------------------------------------------------------------- C-named wrappers (raw pointers)
@@ -67,6 +75,28 @@ def skinny_expert_combine_grad(dY: int, lddy: int, Ys: int, ldys: int, rows: int
     """Raw C call; returns the skinny_status_t."""
     return _sk.load_library().skinny_expert_combine_grad(dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype,
                                                          dYs, lddys, dweights, lddw, stream)
+
+
+def skinny_experts_gemm_bf16(Xs: int, ldx: int, rows: int, offsets: int, W: int, ldw: int, ldwe: int, E: int, N: int,
+                             K: int, act: int, out_dtype: int, Y: int, ldy: int, stream: int = 0) -> int:
+    """Raw C call; returns the skinny_status_t."""
+    return _sk.load_library().skinny_experts_gemm_bf16(Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act, out_dtype,
+                                                       Y, ldy, stream)
+
+
+def skinny_lora_gemm_bf16(X: int, ldx: int, W: int, ldw: int, A: int, lda: int, ldae: int, B: int, ldb: int,
+                          ldbe: int, adapters: int, ranks: int, scales: int, L: int, R: int, Y: int, ldy: int, M: int,
+                          N: int, K: int, out_dtype: int, workspace: int, workspace_bytes: int,
+                          stream: int = 0) -> int:
+    """Raw C call; returns the skinny_status_t."""
+    return _sk.load_library().skinny_lora_gemm_bf16(X, ldx, W, ldw, A, lda, ldae, B, ldb, ldbe, adapters, ranks,
+                                                    scales, L, R, Y, ldy, M, N, K, out_dtype, workspace,
+                                                    workspace_bytes, stream)
+
+
+def skinny_lora_workspace(M: int, N: int, R: int, out_dtype: int) -> int:
+    """Bytes of workspace of skinny_lora_gemm_bf16; 0 for sizes it refuses."""
+    return _sk.load_library().skinny_lora_workspace(M, N, R, out_dtype)
 
 
 # ---------------------------------------------------------------- tensors
@@ -238,3 +268,92 @@ def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stre
     if st != _sk.SKINNY_OK:
         raise _sk.SkinnyError(st, "skinny_expert_combine_grad")
     return dys, dweights
+
+
+def _stack(t, name, rows, cols):
+    """(row stride, matrix stride) of a CUDA bf16 stack of matrices [n, rows, cols]."""
+    import torch
+    if t.dim() != 3 or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor of three dimensions")
+    if t.shape[1] != rows or t.shape[2] != cols:
+        raise ValueError(f"{name} must hold {rows} x {cols} matrices, not {tuple(t.shape[1:])}")
+    if cols > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} needs unit stride along its last dimension")
+    ld = t.stride(1) if rows > 1 else max(cols, 1)
+    return ld, t.stride(0) if t.shape[0] > 1 else max(rows, 1) * ld
+
+
+def experts_gemm(xs, offsets, w, out=None, activation=None, stream=None):
+    """The experts' products on rows in expert order: ``out[r] = xs[r] .
+    w[e]^T`` for ``offsets[e] <= r < offsets[e+1]``, ``xs`` bf16 [rows, K],
+    ``offsets`` int32 [E+1] from :func:`expert_dispatch`, ``w`` bf16 [E, N, K].
+    ``activation="swiglu"``: ``w`` is [E, 2N, K] and ``out`` the gate's SiLU
+    times the up product.  ``out`` bf16 or fp32 [rows, N] (default bf16); rows
+    from ``offsets[E]`` on are left as they are.  See
+    ``skinny_experts_gemm_bf16``."""
+    import torch
+    ldx = _rows(xs, "xs", torch.bfloat16)
+    rows, K = xs.shape
+    if activation not in _ACTS:
+        raise ValueError(f"activation must be 'swiglu' or None, not {activation!r}")
+    act = _ACTS[activation]
+    E, wrows = w.shape[0], w.shape[1]
+    if act and wrows % 2:
+        raise ValueError(f"swiglu needs gate and up rows, not {wrows} rows")
+    N = wrows // 2 if act else wrows
+    ldw, ldwe = _stack(w, "w", wrows, K)
+    _flat(offsets, "offsets", E + 1, torch.int32)
+    with _On(stream, xs.device) as s:
+        if out is None:
+            out = torch.empty((rows, N), dtype=torch.bfloat16, device=xs.device)
+        ldy, ot = _rows(out, "out"), _dtype(out, "out")
+        if tuple(out.shape) != (rows, N):
+            raise ValueError(f"out must be {(rows, N)}, not {tuple(out.shape)}")
+        st = skinny_experts_gemm_bf16(xs.data_ptr(), ldx, rows, offsets.data_ptr(), w.data_ptr(), ldw, ldwe, E, N, K,
+                                      act, ot, out.data_ptr(), ldy, s)
+    if st != _sk.SKINNY_OK:
+        raise _sk.SkinnyError(st, "skinny_experts_gemm_bf16")
+    return out
+
+
+def lora_workspace(M, N, R, out_dtype):
+    """Bytes of workspace of :func:`lora_gemm` for an ``out`` of ``out_dtype``."""
+    import torch
+    return skinny_lora_workspace(M, N, R, SKINNY_BF16 if out_dtype == torch.bfloat16 else SKINNY_F32)
+
+
+def lora_gemm(x, w, a, b, adapters, ranks=None, scales=None, out=None, workspace=None, stream=None):
+    """A shared projection with a low-rank adapter per token: ``out[m] = x[m] .
+    w^T + scales[i] (x[m] . a[i]^T) . b[i]^T`` with ``i = adapters[m]`` (none
+    when outside ``[0, L)``), ``x`` bf16 [M, K], ``w`` bf16 [N, K], ``a`` bf16
+    [L, R, K], ``b`` bf16 [L, N, R], ``ranks`` int32 [L] (what lies past an
+    adapter's rank is not used), ``scales`` fp32 [L], ``out`` fp32 (default)
+    or bf16 [M, N].  See ``skinny_lora_gemm_bf16``."""
+    import torch
+    ldx, ldw = _rows(x, "x", torch.bfloat16), _rows(w, "w", torch.bfloat16)
+    M, K = x.shape
+    N = w.shape[0]
+    L, R = a.shape[0], a.shape[1]
+    if w.shape[1] != K or b.shape[0] != L:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, a {tuple(a.shape)}, b {tuple(b.shape)}")
+    lda, ldae = _stack(a, "a", R, K)
+    ldb, ldbe = _stack(b, "b", N, R)
+    _flat(adapters, "adapters", M, torch.int32)
+    rp = 0 if ranks is None else _flat(ranks, "ranks", L, torch.int32).data_ptr()
+    sp = 0 if scales is None else _flat(scales, "scales", L, torch.float32).data_ptr()
+    with _On(stream, x.device) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        ldy, ot = _rows(out, "out"), _dtype(out, "out")
+        if tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be {(M, N)}, not {tuple(out.shape)}")
+        if workspace is None:
+            workspace = torch.empty(skinny_lora_workspace(M, N, R, ot), dtype=torch.uint8, device=x.device)
+        elif not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        st = skinny_lora_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), ldw, a.data_ptr(), lda, ldae, b.data_ptr(), ldb,
+                                   ldbe, adapters.data_ptr(), rp, sp, L, R, out.data_ptr(), ldy, M, N, K, ot,
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    if st != _sk.SKINNY_OK:
+        raise _sk.SkinnyError(st, "skinny_lora_gemm_bf16")
+    return out

@@ -73,3 +73,49 @@ def combine_grad(dy, ys, pos, w):
 def rounded(ref, err, out):
     """How far a value computed within `err` of `ref` and rounded once to `out` may be from ref."""
     return err + HALF[out] * (np.abs(ref) + err) + TINY[out]
+
+
+def silu_mul(g, u):
+    return g / (1.0 + np.exp(-g)) * u
+
+
+def experts(xs, offsets, w, swiglu):
+    """(y, bound on the error of an fp32 evaluation): every sum of products within 1e-5 of the
+    sum of their magnitudes, SiLU's slope below 1.1, its evaluation within 8 roundings."""
+    rows, K = xs.shape
+    N = w.shape[1] // 2 if swiglu else w.shape[1]
+    y, err = np.full((rows, N), np.nan), np.zeros((rows, N))
+    for e in range(w.shape[0]):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if a == b:
+            continue
+        h = xs[a:b] @ w[e].T
+        mag = 1e-5 * (np.abs(xs[a:b]) @ np.abs(w[e]).T)
+        if swiglu:
+            g, u, dg, du = h[:, :N], h[:, N:], mag[:, :N], mag[:, N:]
+            y[a:b] = silu_mul(g, u)
+            s = np.abs(g / (1.0 + np.exp(-g)))
+            err[a:b] = 1.1 * dg * np.abs(u) + (s + 1.1 * dg) * du + 8 * U32 * np.abs(y[a:b])
+        else:
+            y[a:b], err[a:b] = h, mag
+    return y, err
+
+
+def lora(x, w, a, b, adapters, ranks, scales):
+    """(y, bound on the error of an fp32 evaluation)."""
+    M, K = x.shape
+    L, R = a.shape[0], a.shape[1]
+    y = x @ w.T
+    err = 1e-5 * (np.abs(x) @ np.abs(w).T)
+    for m in range(M):
+        i = int(adapters[m])
+        if not 0 <= i < L:
+            continue
+        r = R if ranks is None else max(0, min(R, int(ranks[i])))
+        s = 1.0 if scales is None else float(scales[i])
+        v = s * (a[i, :r] @ x[m])
+        dv = abs(s) * (8 + K / 256 + 16) * U32 * (np.abs(a[i, :r]) @ np.abs(x[m]))
+        y[m] += b[i, :, :r] @ v
+        # the products of a row in eight at a time, then across the lanes, then the base
+        err[m] += np.abs(b[i, :, :r]) @ dv + 48 * U32 * (np.abs(b[i, :, :r]) @ np.abs(v)) + U32 * np.abs(y[m])
+    return y, 1.01 * err

@@ -71,3 +71,55 @@ def test_tensor_functions_refuse_what_they_cannot_take():
         sk.expert_dispatch(ids, 8)                       # not on a GPU
     with pytest.raises(ValueError):
         sk.expert_combine(torch.zeros((8, 4)), ids)
+
+
+def experts(Xs=A, ldx=64, rows=32, offsets=B, W=C, ldw=64, ldwe=64 * 48, E=8, N=48, K=64, act=0, ot=0, Y=D, ldy=48):
+    return sk.skinny_experts_gemm_bf16(Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act, ot, Y, ldy)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(rows=0), sk.SKINNY_OK), (dict(N=0), sk.SKINNY_OK),
+    (dict(E=0), INVALID), (dict(rows=-1), INVALID), (dict(N=-1), INVALID), (dict(K=-1), INVALID), (dict(act=2), INVALID),
+    (dict(ot=2), INVALID), (dict(E=1025), UNSUPPORTED), (dict(N=(1 << 20) + 1, ldy=1 << 21), UNSUPPORTED),
+    (dict(K=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21), UNSUPPORTED),
+    (dict(Xs=0), INVALID), (dict(offsets=0), INVALID), (dict(W=0), INVALID), (dict(Y=0), INVALID),
+    (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(ldwe=64 * 48 - 1), INVALID), (dict(ldy=47), INVALID),
+    (dict(act=1), INVALID),                              # the stride of an expert holds 48 rows, not 96
+    (dict(Xs=A + 1), MISALIGNED), (dict(W=C + 1), MISALIGNED), (dict(offsets=B + 2), MISALIGNED),
+    (dict(Y=D + 1), MISALIGNED), (dict(ot=1, Y=D + 2), MISALIGNED),
+    (dict(Y=A), INVALID), (dict(Y=C + 7 * 64 * 48 * 2), INVALID), (dict(Y=B), INVALID),
+])
+def test_experts_gemm_refusals(kw, expect):
+    assert experts(**kw) == expect
+
+
+def lora(X=A, ldx=64, W=B, ldw=64, Aw=C, lda=64, ldae=8 * 64, Bw=D, ldb=8, ldbe=48 * 8, ids=F, ranks=F + 4096,
+         scales=F + 8192, L=4, R=8, Y=G, ldy=48, M=5, N=48, K=64, ot=0, ws=G + (1 << 20), wsb=1 << 20):
+    return sk.skinny_lora_gemm_bf16(X, ldx, W, ldw, Aw, lda, ldae, Bw, ldb, ldbe, ids, ranks, scales, L, R, Y, ldy, M, N,
+                                    K, ot, ws, wsb)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(M=0), sk.SKINNY_OK), (dict(N=0), sk.SKINNY_OK),
+    (dict(L=-1), INVALID), (dict(R=-1), INVALID), (dict(ot=2), INVALID), (dict(M=-1), INVALID),
+    (dict(R=257, ldb=257), UNSUPPORTED), (dict(M=65), UNSUPPORTED),
+    (dict(X=0), INVALID), (dict(W=0), INVALID), (dict(Aw=0), INVALID), (dict(Bw=0), INVALID), (dict(ids=0), INVALID),
+    (dict(Y=0), INVALID), (dict(ws=0), INVALID), (dict(ot=1, wsb=5 * 8 * 4 - 1), INVALID), (dict(ot=0, wsb=5 * 8 * 4), INVALID),
+    (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(lda=63), INVALID), (dict(ldb=7), INVALID),
+    (dict(ldae=511), INVALID), (dict(ldbe=383), INVALID), (dict(ldy=47), INVALID),
+    (dict(X=A + 1), MISALIGNED), (dict(Aw=C + 1), MISALIGNED), (dict(Bw=D + 1), MISALIGNED), (dict(ids=F + 2), MISALIGNED),
+    (dict(ranks=F + 4098), MISALIGNED), (dict(scales=F + 8193), MISALIGNED), (dict(ws=G + (1 << 20) + 8), MISALIGNED),
+    (dict(Y=G + 1), MISALIGNED), (dict(ot=1, Y=G + 2), MISALIGNED),
+    (dict(Y=A), INVALID), (dict(Y=B), INVALID), (dict(Y=C), INVALID), (dict(Y=D), INVALID), (dict(Y=F), INVALID),
+    (dict(Y=F + 4096), INVALID), (dict(Y=F + 8192), INVALID), (dict(ws=A), INVALID), (dict(ws=D), INVALID),
+    (dict(ws=G), INVALID), (dict(ws=F), INVALID),
+])
+def test_lora_refusals(kw, expect):
+    assert lora(**kw) == expect
+
+
+def test_lora_workspace():
+    assert sk.skinny_lora_workspace(5, 48, 8, sk.SKINNY_F32) == 160
+    assert sk.skinny_lora_workspace(5, 48, 3, sk.SKINNY_BF16) == 64 + 5 * 48 * 4
+    for bad in ((65, 48, 8, 0), (5, -1, 8, 0), (5, 48, 257, 0), (5, 48, 8, 2), (-1, 48, 8, 0)):
+        assert sk.skinny_lora_workspace(*bad) == 0
