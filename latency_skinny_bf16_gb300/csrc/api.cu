@@ -21,6 +21,7 @@
 #include "internal.h"
 #include "dotmma_f32w.h"
 #include "expert_rows.h"
+#include "experts_gemm.h"
 
 namespace skinny {
 namespace {
@@ -126,7 +127,7 @@ skinny_status_t init_device_current(DeviceState &d, int device) {
     if (dotprod_prepare() != cudaSuccess || dotmma_prepare() != cudaSuccess || splitk_prepare() != cudaSuccess ||
         stream_prepare() != cudaSuccess || dotprod_f32w_prepare() != cudaSuccess ||
         dotmma_f32w_prepare() != cudaSuccess || tc_prepare() != cudaSuccess ||
-        expert_rows_prepare() != cudaSuccess)
+        expert_rows_prepare() != cudaSuccess || experts_tc_prepare() != cudaSuccess)
         return SKINNY_ERR_LAUNCH;
     void *sym = nullptr;
     if (cudaGetSymbolAddress(&sym, g_status_word) != cudaSuccess) return SKINNY_ERR_LAUNCH;

@@ -143,6 +143,7 @@ skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, 
     if (rows == 0 || N == 0) return SKINNY_OK;
     const int ob = el_bytes(out_dtype);
     const int64_t wrows = act == SKINNY_ACT_SWIGLU ? 2ll * N : N;
+    if (E == 1) ldwe = wrows * ldw;     // no other expert: the stride is not used
     if (!offsets || !Y || ldy < N) return SKINNY_ERR_INVALID_VALUE;
     if (!aligned(offsets, 4) || !aligned(Y, ob)) return SKINNY_ERR_MISALIGNED;
     const Range y = span(Y, rows, N, ldy, ob);
@@ -159,7 +160,8 @@ skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, 
     if (st != SKINNY_OK) return st;
     const ExpertsArgs a{Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act == SKINNY_ACT_SWIGLU,
                         out_dtype == SKINNY_BF16, Y, ldy};
-    return launched(launch_experts_dot(a, c, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launched(experts_tc_supported(a) ? launch_experts_tc(a, c, s) : launch_experts_dot(a, c, s));
 }
 
 int64_t skinny_lora_workspace(int M, int N, int R, int out_dtype) {

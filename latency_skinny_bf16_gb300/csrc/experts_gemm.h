@@ -23,6 +23,11 @@ struct ExpertsArgs {
 // CUDA cores, any alignment (experts_dot.cu); K == 0 included
 cudaError_t launch_experts_dot(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
 
+// tcgen05 (experts_tc.cu): 16-byte aligned rows of X and W, K >= 1
+bool experts_tc_supported(const ExpertsArgs &a);
+cudaError_t experts_tc_prepare();
+cudaError_t launch_experts_tc(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
+
 struct LoraArgs {
     const uint16_t *X;
     int64_t ldx;

@@ -185,3 +185,19 @@ def test_weights_past_32_bits():
     y = sk.experts_gemm(xs, off, w, out=torch.empty((5, N), device="cuda"))
     assert (y[:2] == 2.0).all()
     assert torch.equal(y[2:], torch.arange(2, 5, device="cuda")[:, None] * (torch.arange(N, device="cuda") % 128).float())
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_bounded_waits_report_and_recover(act):
+    """A wait without any budget gives up at once, the status says so, and the next call is right."""
+    xs, off, w, _ = run([3, 0, 20, 1], 200, 640, act, "fp32")
+    offsets = torch.from_numpy(off).cuda()
+    want = sk.experts_gemm(xs, offsets, w, activation=act)
+    with sk.options(wait_timeout_us=0):
+        sk.experts_gemm(xs, offsets, w, activation=act)
+        torch.cuda.synchronize()
+    assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
+    n = int(off[-1])
+    for _ in range(3):
+        assert torch.equal(sk.experts_gemm(xs, offsets, w, activation=act)[:n], want[:n])
+    assert sk.skinny_get_device_status() == 0
