@@ -162,7 +162,7 @@ skinny_status_t call_context(CallCtx *c) {
     const skinny_status_t st = current_device(&device);
     if (st != SKINNY_OK) return st;
     const DeviceState &d = g_dev[device];
-    *c = {d.num_sms, d.status_word, (uint64_t)g_opt_wait_us.load() * 1000ull, opt_pdl() != 0};
+    *c = {d.num_sms, d.status_word, (uint64_t)g_opt_wait_us.load() * 1000ull, opt_pdl() != 0, g_opt_force_backend.load()};
     return SKINNY_OK;
 }
 

@@ -281,151 +281,241 @@ dispatch_copy_kernel(const int32_t *__restrict__ pos, const char *__restrict__ X
 }
 
 // ------------------------------------------------------------------ fp32 <-> stored types
-// V elements of a bf16 or fp32 row as fp32, through L2 (rows may have just been
-// written by the preceding kernel).  V is 8 (bf16) or 4 (fp32): 16 bytes; or 1.
-template <bool BF16, int V>
-__device__ __forceinline__ void load_row(const char *row, int64_t el, float (&v)[V]) {
-    if constexpr (BF16 && V == 8) {
-        const uint4 q = ldg_v4(row + el * 2);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
-    } else if constexpr (!BF16 && V == 4) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(row + el * 4));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else if constexpr (BF16) {
-        v[0] = bf16_one(ldg_u16(row + el * 2));
+// VB bytes of a bf16 or fp32 row, as loaded (through L2: rows may have just been
+// written by the preceding kernel), and as fp32.
+template <int VB> struct Raw {
+    uint32_t w[VB >= 4 ? VB / 4 : 1];
+};
+template <int VB>
+__device__ __forceinline__ Raw<VB> load_raw(const char *at) {
+    Raw<VB> r;
+    if constexpr (VB == 16) {
+        const uint4 q = ldg_v4(at);
+        r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+    } else if constexpr (VB == 8) {
+        const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(at));
+        r.w[0] = q.x; r.w[1] = q.y;
+    } else if constexpr (VB == 4) {
+        r.w[0] = __ldcg(reinterpret_cast<const uint32_t *>(at));
     } else {
-        v[0] = __ldcg(reinterpret_cast<const float *>(row + el * 4));
+        r.w[0] = ldg_u16(at);
     }
+    return r;
+}
+template <int VB>
+__device__ __forceinline__ Raw<VB> zero_raw() {
+    Raw<VB> r;
+#pragma unroll
+    for (int i = 0; i < (VB >= 4 ? VB / 4 : 1); ++i) r.w[i] = 0;
+    return r;
+}
+template <bool BF16, int VB> constexpr int raw_els() { return VB / (BF16 ? 2 : 4); }
+template <bool BF16, int VB>
+__device__ __forceinline__ float raw_el(const Raw<VB> &r, int i) {
+    if constexpr (!BF16) return __uint_as_float(r.w[i]);
+    else return (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return (uint32_t)f32_to_bf16_rn(lo) | ((uint32_t)f32_to_bf16_rn(hi) << 16);
 }
-template <bool BF16, int V>
-__device__ __forceinline__ void store_row(char *row, int64_t el, const float (&v)[V]) {
-    if constexpr (BF16 && V == 8) {
-        *reinterpret_cast<uint4 *>(row + el * 2) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else if constexpr (BF16 && V == 4) {
-        *reinterpret_cast<uint2 *>(row + el * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    } else if constexpr (BF16) {
-        *reinterpret_cast<uint16_t *>(row + el * 2) = f32_to_bf16_rn(v[0]);
-    } else if constexpr (V % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<float4 *>(row + el * 4 + 4 * i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+// N consecutive elements from element `el` of a row, each rounded once.
+template <bool BF16, int N>
+__device__ __forceinline__ void store_els(char *row, int64_t el, const float (&v)[N]) {
+    if constexpr (BF16) {
+        char *at = row + el * 2;
+        if constexpr (N == 8)
+            *reinterpret_cast<uint4 *>(at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                        pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        else if constexpr (N == 4)
+            *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else if constexpr (N == 2)
+            *reinterpret_cast<uint32_t *>(at) = pack_bf16(v[0], v[1]);
+        else
+            *reinterpret_cast<uint16_t *>(at) = f32_to_bf16_rn(v[0]);
     } else {
-        *reinterpret_cast<float *>(row + el * 4) = v[0];
+        char *at = row + el * 4;
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4 *>(at + 4 * i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else if constexpr (N == 2) {
+            *reinterpret_cast<float2 *>(at) = make_float2(v[0], v[1]);
+        } else {
+            *reinterpret_cast<float *>(at) = v[0];
+        }
     }
 }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// A token's places and weights in the lanes of a warp: lane j holds entry j and
+// entry 32 + j.  A dropped entry has place -1 and weight 0 (its own may be NaN).
+struct Entries {
+    int p[2];
+    float w[2];
+    __device__ __forceinline__ void load(const int32_t *pos, const float *weights, int64_t ldw, int64_t t, int k,
+                                         int rows, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = 32 * h + lane;
+            p[h] = j < k ? __ldcg(pos + t * k + j) : -1;
+            w[h] = j < k && weights ? __ldcg(weights + t * ldw + j) : 1.f;
+            if ((unsigned)p[h] >= (unsigned)rows) { p[h] = -1; w[h] = 0.f; }
+        }
+    }
+    __device__ __forceinline__ int place(int j) const { return __shfl_sync(0xFFFFFFFFu, j < 32 ? p[0] : p[1], j & 31); }
+    __device__ __forceinline__ float weight(int j) const { return __shfl_sync(0xFFFFFFFFu, j < 32 ? w[0] : w[1], j & 31); }
+};
 
 // ------------------------------------------------------------------ combine
-// Grid (T, chunks), one vector of the token's row per thread: its k rows'
-// vectors are loaded eight at a time before they are added, in order of j.
-constexpr int kCombineThreads = 128;
-template <bool IN16, bool OUT16, int V>
-__global__ void __launch_bounds__(kCombineThreads)
+// A warp takes one of S pieces of a token's row: the token's places are read
+// once, then U rows x IT loads are in flight per lane before they are added, in
+// order of j.  What limits it is the bytes in flight: a first form with a
+// thread per vector spent half its time waiting for the places.
+template <bool IN16, bool OUT16, int VB, int U, int IT>
+__global__ void __launch_bounds__(128)
 combine_kernel(const char *__restrict__ Ys, int64_t ldys_bytes, int rows, const int32_t *__restrict__ pos,
-               const float *__restrict__ weights, int64_t ldw, int k, int H, char *__restrict__ Y, int64_t ldy_bytes)
+               const float *__restrict__ weights, int64_t ldw, int T, int k, int nvec, int S, char *__restrict__ Y,
+               int64_t ldy_bytes)
 {
+    constexpr int NE = raw_els<IN16, VB>();
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t t = blockIdx.x;
-    const int64_t el = ((int64_t)blockIdx.y * kCombineThreads + threadIdx.x) * V;
-    if (el >= H) return;
-    float acc[V];
+    const int lane = threadIdx.x & 31;
+    const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t t = job / S;
+    if (t >= T) return;
+    const int seg = (int)(job - t * S);
+    Entries e;
+    e.load(pos, weights, ldw, t, k, rows, lane);
+    const int per = (nvec + S - 1) / S;
+    const int v0 = seg * per, v1 = min(nvec, v0 + per);
+    char *y = Y + t * ldy_bytes;
+    for (int vb = v0; vb < v1; vb += 32 * IT) {
+        float acc[IT][NE];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    constexpr int U = 8;
-    for (int j0 = 0; j0 < k; j0 += U) {
-        float r[U][V], w[U];
-        bool live[U];
+        for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = j0 + u < k ? __ldcg(pos + t * k + j0 + u) : -1;
-            live[u] = (unsigned)p < (unsigned)rows;
-            if (live[u]) {
-                w[u] = weights ? __ldcg(weights + t * ldw + j0 + u) : 1.f;
-                load_row<IN16, V>(Ys + (int64_t)p * ldys_bytes, el, r[u]);
-            }
-        }
+            for (int x = 0; x < NE; ++x) acc[i][x] = 0.f;
+        for (int j0 = 0; j0 < k; j0 += U) {
+            Raw<VB> r[U][IT];
+            float w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (live[u]) {
+            for (int u = 0; u < U; ++u) {
+                const int p = j0 + u < k ? e.place(j0 + u) : -1;
+                w[u] = j0 + u < k ? e.weight(j0 + u) : 0.f;
+                const char *row = Ys + (int64_t)p * ldys_bytes;
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u], r[u][i], acc[i]);
-            }
-    }
-    store_row<OUT16, V>(Y + t * ldy_bytes, el, acc);
-}
-
-// ------------------------------------------------------------------ gradient of combine
-// One CTA per token, eight entries at a time: dY[t] is read once per eight
-// entries, each Ys row read and each dYs row written once; the dot products
-// stay in registers until one block reduction in a fixed order.
-template <bool B16, int V, bool DW>
-__global__ void __launch_bounds__(kRowThreads)
-combine_grad_kernel(const char *__restrict__ dY, int64_t lddy_bytes, const char *__restrict__ Ys, int64_t ldys_bytes,
-                    int rows, const int32_t *__restrict__ pos, const float *__restrict__ weights, int64_t ldw, int k,
-                    int H, char *__restrict__ dYs, int64_t lddys_bytes, float *__restrict__ dw, int64_t lddw)
-{
-    constexpr int U = 8;
-    __shared__ float part[kRowThreads / 32][U];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const char *dy = dY + t * lddy_bytes;
-    for (int j0 = 0; j0 < k; j0 += U) {
-        int p[U];
-        float w[U], dot[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            p[u] = j0 + u < k ? __ldcg(pos + t * k + j0 + u) : -1;
-            if ((unsigned)p[u] >= (unsigned)rows) p[u] = -1;
-            w[u] = (weights && p[u] >= 0) ? __ldcg(weights + t * ldw + j0 + u) : 1.f;
-            dot[u] = 0.f;
-        }
-        for (int64_t el = (int64_t)tid * V; el < H; el += kRowThreads * V) {
-            float g[V], r[U][V];
-            load_row<B16, V>(dy, el, g);
-            if constexpr (DW) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p[u] >= 0) load_row<B16, V>(Ys + (int64_t)p[u] * ldys_bytes, el, r[u]);
+                for (int i = 0; i < IT; ++i) {
+                    const int v = vb + 32 * i + lane;
+                    r[u][i] = (p >= 0 && v < v1) ? load_raw<VB>(row + (int64_t)v * VB) : zero_raw<VB>();
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p[u] >= 0) {
-                    float o[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        o[i] = w[u] * g[i];
-                        if constexpr (DW) dot[u] = fmaf(g[i], r[u][i], dot[u]);
-                    }
-                    store_row<B16, V>(dYs + (int64_t)p[u] * lddys_bytes, el, o);
-                }
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int x = 0; x < NE; ++x) acc[i][x] = fmaf(w[u], raw_el<IN16, VB>(r[u][i], x), acc[i][x]);
         }
-        if constexpr (DW) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int v = vb + 32 * i + lane;
+            if (v < v1) store_els<OUT16, NE>(y, (int64_t)v * NE, acc[i]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gradient of combine
+// S warps of a CTA share a token (8 / S tokens a CTA), eight entries at a time:
+// dY[t] is read once per eight entries, each Ys row read and each dYs row
+// written once; the dot products stay in registers until the end of the row,
+// then one butterfly and, for S > 1, the warps' sums in order.
+template <bool B16, int VB, bool DW>
+__global__ void __launch_bounds__(kRowThreads, 2)
+combine_grad_kernel(const char *__restrict__ dY, int64_t lddy_bytes, const char *__restrict__ Ys, int64_t ldys_bytes,
+                    int rows, const int32_t *__restrict__ pos, const float *__restrict__ weights, int64_t ldw, int T,
+                    int k, int nvec, int S, char *__restrict__ dYs, int64_t lddys_bytes, float *__restrict__ dw,
+                    int64_t lddw)
+{
+    constexpr int U = 8, NE = raw_els<B16, VB>(), IT = VB == 16 ? 1 : VB == 8 ? 2 : 4;
+    __shared__ float part[kRowThreads / 32][kMaxTopk];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32 / S) + warp / S;
+    const int seg = warp % S;
+    if (t < T) {
+        Entries e;
+        e.load(pos, weights, ldw, t, k, rows, lane);
+        const char *dy = dY + t * lddy_bytes;
+        const int per = (nvec + S - 1) / S;
+        const int v0 = seg * per, v1 = min(nvec, v0 + per);
+        for (int j0 = 0; j0 < k; j0 += U) {
+            int p[U];
+            float w[U], dot[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                p[u] = j0 + u < k ? e.place(j0 + u) : -1;
+                w[u] = j0 + u < k ? e.weight(j0 + u) : 0.f;
+                dot[u] = 0.f;
+            }
+            for (int vb = v0 + lane; vb < v1; vb += 32 * IT) {
+                Raw<VB> g[IT], r[U][IT];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
-                if (lane == 0) part[warp][u] = dot[u];
+                for (int i = 0; i < IT; ++i) g[i] = vb + 32 * i < v1 ? load_raw<VB>(dy + (int64_t)(vb + 32 * i) * VB) : zero_raw<VB>();
+                if constexpr (DW) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < IT; ++i)
+                            r[u][i] = (p[u] >= 0 && vb + 32 * i < v1)
+                                          ? load_raw<VB>(Ys + (int64_t)p[u] * ldys_bytes + (int64_t)(vb + 32 * i) * VB)
+                                          : zero_raw<VB>();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (p[u] < 0) continue;
+                    char *to = dYs + (int64_t)p[u] * lddys_bytes;
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        if (vb + 32 * i >= v1) continue;
+                        float o[NE];
+#pragma unroll
+                        for (int x = 0; x < NE; ++x) {
+                            const float gx = raw_el<B16, VB>(g[i], x);
+                            o[x] = w[u] * gx;
+                            if constexpr (DW) dot[u] = fmaf(gx, raw_el<B16, VB>(r[u][i], x), dot[u]);
+                        }
+                        store_els<B16, NE>(to, (int64_t)(vb + 32 * i) * NE, o);
+                    }
+                }
             }
-            __syncthreads();
-            if (tid < U && j0 + tid < k) {
-                float s = 0.f;
-                for (int v = 0; v < kRowThreads / 32; ++v) s += part[v][tid];
-                dw[t * lddw + j0 + tid] = s;       // a dropped entry added nothing: 0
+            if constexpr (DW) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float s = warp_sum(dot[u]);
+                    if (lane == 0 && j0 + u < k) part[warp][j0 + u] = s;   // a dropped entry added nothing: 0
+                }
             }
-            __syncthreads();
         }
+    }
+    if constexpr (DW) {
+        __syncthreads();
+        if (t < T && seg == 0)
+            for (int j = lane; j < k; j += 32) {
+                float s = part[warp][j];
+                for (int i = 1; i < S; ++i) s += part[warp + i][j];
+                dw[t * lddw + j] = s;
+            }
     }
 }
 
 // ------------------------------------------------------------------ launches
+uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
 cudaError_t launch(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl, int cluster,
                    void **args) {
     cudaLaunchConfig_t cfg = {};
@@ -489,35 +579,78 @@ cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStrea
                   stream, pdl, 1, cargs);
 }
 
-template <bool IN16, bool OUT16, int V>
-cudaError_t combine_vec(const CombineArgs &a, cudaStream_t stream, bool pdl) {
+template <bool IN16, bool OUT16, int VB, int U, int IT>
+cudaError_t combine_as(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
     const char *Ys = static_cast<const char *>(a.Ys);
     char *Y = static_cast<char *>(a.Y);
     int64_t ldys = a.ldys * (IN16 ? 2 : 4), ldy = a.ldy * (OUT16 ? 2 : 4), ldw = a.ldw;
-    int rows = a.rows, k = a.k, H = a.H;
+    int rows = a.rows, T = a.T, k = a.k, nvec = (int)((int64_t)a.H * (IN16 ? 2 : 4) / VB);
     const int32_t *pos = a.pos;
     const float *w = a.weights;
-    const int per = kCombineThreads * V;
-    void *args[] = {&Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &Y, &ldy};
-    return launch((const void *)combine_kernel<IN16, OUT16, V>, dim3(a.T, (H + per - 1) / per), kCombineThreads, 0,
-                  stream, pdl, 1, args);
+    // pieces of a row: enough warps to fill the SMs twice, at least one step of the loop each
+    const int64_t want = (40ll * num_sms + T - 1) / T, most = (nvec + 32 * IT - 1) / (32 * IT);
+    int S = (int)(want < most ? want : most);
+    const int64_t jobs = (int64_t)T * S;
+    void *args[] = {&Ys, &ldys, &rows, &pos, &w, &ldw, &T, &k, &nvec, &S, &Y, &ldy};
+    return launch((const void *)combine_kernel<IN16, OUT16, VB, U, IT>, dim3((unsigned)((jobs + 3) / 4)), 128, 0, stream,
+                  pdl, 1, args);
+}
+template <bool IN16, bool OUT16, int VB>
+cudaError_t combine_vec(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    // rows in flight as the token has entries, loads of each to match
+    if (a.k <= 2) return combine_as<IN16, OUT16, VB, 2, 4>(a, num_sms, stream, pdl);
+    if (a.k <= 4) return combine_as<IN16, OUT16, VB, 4, (VB >= 8 ? 2 : 4)>(a, num_sms, stream, pdl);
+    return combine_as<IN16, OUT16, VB, 8, (VB >= 8 ? 2 : 4)>(a, num_sms, stream, pdl);
+}
+template <bool IN16, bool OUT16>
+cudaError_t combine_types(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    constexpr int ib = IN16 ? 2 : 4, ob = OUT16 ? 2 : 4;
+    // the widest load at which every row of Ys starts, ends and is stored aligned
+    const uintptr_t in = u(a.Ys) | (uintptr_t)(a.ldys * ib), out = u(a.Y) | (uintptr_t)(a.ldy * ob);
+    auto fits = [&](int vb) {
+        const int st = vb / ib * ob;
+        return in % vb == 0 && (int64_t)a.H * ib % vb == 0 && out % (st > 16 ? 16 : st) == 0;
+    };
+    if (fits(16)) return combine_vec<IN16, OUT16, 16>(a, num_sms, stream, pdl);
+    if (fits(8)) return combine_vec<IN16, OUT16, 8>(a, num_sms, stream, pdl);
+    if constexpr (IN16) {
+        if (fits(4)) return combine_vec<IN16, OUT16, 4>(a, num_sms, stream, pdl);
+        return combine_vec<IN16, OUT16, 2>(a, num_sms, stream, pdl);
+    } else {
+        return combine_vec<IN16, OUT16, 4>(a, num_sms, stream, pdl);
+    }
 }
 
-template <bool B16, int V, bool DW>
-cudaError_t grad_vec(const CombineGradArgs &a, cudaStream_t stream, bool pdl) {
+template <bool B16, int VB, bool DW>
+cudaError_t grad_as(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
     const int b = B16 ? 2 : 4;
     const char *dY = static_cast<const char *>(a.dY), *Ys = static_cast<const char *>(a.Ys);
     char *dYs = static_cast<char *>(a.dYs);
     int64_t lddy = a.lddy * b, ldys = a.ldys * b, lddys = a.lddys * b, ldw = a.ldw, lddw = a.lddw;
-    int rows = a.rows, k = a.k, H = a.H;
+    int rows = a.rows, T = a.T, k = a.k, nvec = (int)((int64_t)a.H * b / VB);
     const int32_t *pos = a.pos;
     const float *w = a.weights;
     float *dw = a.dweights;
-    void *args[] = {&dY, &lddy, &Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &dYs, &lddys, &dw, &lddw};
-    return launch((const void *)combine_grad_kernel<B16, V, DW>, dim3(a.T), kRowThreads, 0, stream, pdl, 1, args);
+    // warps per token: as few as fill the SMs
+    int S = 1;
+    while (S < kRowThreads / 32 && (int64_t)T * S < 32ll * num_sms) S *= 2;
+    void *args[] = {&dY, &lddy, &Ys, &ldys, &rows, &pos, &w, &ldw, &T, &k, &nvec, &S, &dYs, &lddys, &dw, &lddw};
+    const int per = kRowThreads / 32 / S;
+    return launch((const void *)combine_grad_kernel<B16, VB, DW>, dim3((T + per - 1) / per), kRowThreads, 0, stream, pdl,
+                  1, args);
 }
-
-uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+template <bool B16, bool DW>
+cudaError_t grad_types(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    constexpr int b = B16 ? 2 : 4;
+    const uintptr_t all = u(a.dY) | u(a.dYs) | (uintptr_t)(a.lddy * b) | (uintptr_t)(a.lddys * b) |
+                          (DW ? u(a.Ys) | (uintptr_t)(a.ldys * b) : 0);
+    switch (vec_bytes((int64_t)a.H * b, b, all)) {
+        case 16: return grad_as<B16, 16, DW>(a, num_sms, stream, pdl);
+        case 8: return grad_as<B16, 8, DW>(a, num_sms, stream, pdl);
+        case 4: return grad_as<B16, 4, DW>(a, num_sms, stream, pdl);
+        default: return grad_as<B16, B16 ? 2 : 4, DW>(a, num_sms, stream, pdl);
+    }
+}
 
 }  // namespace
 
@@ -538,28 +671,14 @@ cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t str
     }
 }
 
-cudaError_t launch_combine(const CombineArgs &a, cudaStream_t stream, bool pdl) {
-    // 16-byte loads where every row starts and ends on one, element by element elsewhere
-    const int ib = a.in16 ? 2 : 4, ob = a.out16 ? 2 : 4, V = 16 / ib;
-    const bool wide = a.H % V == 0 && u(a.Ys) % 16 == 0 && (a.ldys * ib) % 16 == 0 && u(a.Y) % (V * ob > 16 ? 16 : V * ob) == 0 &&
-                      (a.ldy * ob) % (V * ob > 16 ? 16 : V * ob) == 0;
-    if (a.in16 && a.out16) return wide ? combine_vec<true, true, 8>(a, stream, pdl) : combine_vec<true, true, 1>(a, stream, pdl);
-    if (a.in16) return wide ? combine_vec<true, false, 8>(a, stream, pdl) : combine_vec<true, false, 1>(a, stream, pdl);
-    if (a.out16) return wide ? combine_vec<false, true, 4>(a, stream, pdl) : combine_vec<false, true, 1>(a, stream, pdl);
-    return wide ? combine_vec<false, false, 4>(a, stream, pdl) : combine_vec<false, false, 1>(a, stream, pdl);
+cudaError_t launch_combine(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    if (a.in16) return a.out16 ? combine_types<true, true>(a, num_sms, stream, pdl) : combine_types<true, false>(a, num_sms, stream, pdl);
+    return a.out16 ? combine_types<false, true>(a, num_sms, stream, pdl) : combine_types<false, false>(a, num_sms, stream, pdl);
 }
 
-cudaError_t launch_combine_grad(const CombineGradArgs &a, cudaStream_t stream, bool pdl) {
-    const int b = a.b16 ? 2 : 4;
-    const uintptr_t all = u(a.dY) | u(a.dYs) | (uintptr_t)(a.lddy * b) | (uintptr_t)(a.lddys * b) |
-                          (a.dweights ? u(a.Ys) | (uintptr_t)(a.ldys * b) : 0);
-    const bool wide = all % 16 == 0 && a.H % (16 / b) == 0;
-    if (a.b16) {
-        if (a.dweights) return wide ? grad_vec<true, 8, true>(a, stream, pdl) : grad_vec<true, 1, true>(a, stream, pdl);
-        return wide ? grad_vec<true, 8, false>(a, stream, pdl) : grad_vec<true, 1, false>(a, stream, pdl);
-    }
-    if (a.dweights) return wide ? grad_vec<false, 4, true>(a, stream, pdl) : grad_vec<false, 1, true>(a, stream, pdl);
-    return wide ? grad_vec<false, 4, false>(a, stream, pdl) : grad_vec<false, 1, false>(a, stream, pdl);
+cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+    if (a.b16) return a.dweights ? grad_types<true, true>(a, num_sms, stream, pdl) : grad_types<true, false>(a, num_sms, stream, pdl);
+    return a.dweights ? grad_types<false, true>(a, num_sms, stream, pdl) : grad_types<false, false>(a, num_sms, stream, pdl);
 }
 
 }  // namespace skinny

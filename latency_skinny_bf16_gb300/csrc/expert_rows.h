@@ -51,7 +51,7 @@ struct CombineGradArgs {
 
 cudaError_t expert_rows_prepare();
 cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t launch_combine(const CombineArgs &a, cudaStream_t stream, bool pdl);
-cudaError_t launch_combine_grad(const CombineGradArgs &a, cudaStream_t stream, bool pdl);
+cudaError_t launch_combine(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
 }  // namespace skinny

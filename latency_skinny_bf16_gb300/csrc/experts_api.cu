@@ -103,7 +103,7 @@ skinny_status_t skinny_expert_combine(const void *Ys, int ldys, int rows, const 
     if (st != SKINNY_OK) return st;
     const CombineArgs a{Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype == SKINNY_BF16, out_dtype == SKINNY_BF16,
                         Y, ldy};
-    return launched(launch_combine(a, static_cast<cudaStream_t>(stream), c.pdl));
+    return launched(launch_combine(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
 }
 
 skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void *Ys, int ldys, int rows,
@@ -130,7 +130,7 @@ skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void 
     if (st != SKINNY_OK) return st;
     const CombineGradArgs a{dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype == SKINNY_BF16, dYs, lddys,
                             dweights, lddw};
-    return launched(launch_combine_grad(a, static_cast<cudaStream_t>(stream), c.pdl));
+    return launched(launch_combine_grad(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
 }
 
 skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, const int32_t *offsets,
@@ -161,14 +161,16 @@ skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, 
     const ExpertsArgs a{Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act == SKINNY_ACT_SWIGLU,
                         out_dtype == SKINNY_BF16, Y, ldy};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launched(experts_tc_supported(a) ? launch_experts_tc(a, c, s) : launch_experts_dot(a, c, s));
+    if (c.force_backend == SKINNY_BACKEND_TCGEN05)
+        return experts_tc_supported(a) ? launched(launch_experts_tc(a, c, s)) : SKINNY_ERR_UNSUPPORTED;
+    const bool tc = c.force_backend != SKINNY_BACKEND_DOTPROD && experts_tc_supported(a) && experts_tc_faster(a, c.num_sms);
+    return launched(tc ? launch_experts_tc(a, c, s) : launch_experts_mma(a, c, s));
 }
 
 int64_t skinny_lora_workspace(int M, int N, int R, int out_dtype) {
     if (M < 0 || M > SKINNY_MAX_M || N < 0 || R < 0 || R > SKINNY_MAX_RANK || !dtype_ok(out_dtype)) return 0;
     // V, then (bf16 output) the projection in fp32 that the adapters are added to before the one rounding
-    const int64_t v = ((int64_t)M * R * 4 + 15) / 16 * 16;
-    return v + (out_dtype == SKINNY_BF16 ? (int64_t)M * N * 4 : 0);
+    return (int64_t)M * 3 * lora_padded_rank(R) * 2 + (out_dtype == SKINNY_BF16 ? (int64_t)M * N * 4 : 0);
 }
 
 skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const uint16_t *A,
@@ -190,8 +192,8 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
     if (!aligned(Y, el_bytes(out_dtype)) || !aligned(A, 2) || !aligned(B, 2) || !aligned(adapters, 4) ||
         !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(workspace, 16))
         return SKINNY_ERR_MISALIGNED;
-    float *V = static_cast<float *>(workspace);
-    float *base = ob ? V + ((int64_t)M * R + 3) / 4 * 4 : static_cast<float *>(Y);
+    uint16_t *V = static_cast<uint16_t *>(workspace);
+    float *base = ob ? reinterpret_cast<float *>(V + (int64_t)M * 3 * lora_padded_rank(R)) : static_cast<float *>(Y);
     const int ldbase = ob ? N : ldy;
     const Range y = span(Y, M, N, ldy, el_bytes(out_dtype)), x = span(X, M, K, ldx, 2), w = span(W, N, K, ldw, 2),
                 ws = {addr(workspace), addr(workspace) + (uintptr_t)skinny_lora_workspace(M, N, R, out_dtype)},
@@ -200,8 +202,16 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
                 id = span(adapters, 1, M, 0, 4), rk = span(ranks, 1, L, 0, 4), sc = span(scales, 1, L, 0, 4);
     if (meets(y, {x, w, ws, ra, rb, id, rk, sc}) || meets(ws, {x, w, ra, rb, id, rk, sc}))
         return SKINNY_ERR_INVALID_VALUE;
-    st = check_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, 0);
-    if (st != SKINNY_OK) return st;
+    if (!X || !W || ldx < K || ldw < K) return SKINNY_ERR_INVALID_VALUE;
+    if (!aligned(X, 2) || !aligned(W, 2)) return SKINNY_ERR_MISALIGNED;
+    // The projection: skinny_gemm_bf16 where its rows are 16-byte aligned; else the experts' mma.sync
+    // kernel on the one matrix, which reads whole 16-byte pieces at any alignment (GB300, 8 tokens,
+    // 2645 -> 896: see its figures) and takes every M.
+    const bool rows16 = ((addr(X) | addr(W)) % 16 | (ldx | ldw) % 8) == 0;
+    if (rows16) {
+        st = check_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, 0);
+        if (st != SKINNY_OK) return st;
+    }
     CallCtx c;
     st = call_context(&c);
     if (st != SKINNY_OK) return st;
@@ -209,8 +219,13 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
                      ldy, ob};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (launch_lora_shrink(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
-    st = run_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, stream, 0);
-    if (st != SKINNY_OK) return st;
+    if (rows16) {
+        st = run_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, stream, 0);
+        if (st != SKINNY_OK) return st;
+    } else {
+        const ExpertsArgs b{X, ldx, M, nullptr, W, ldw, (int64_t)N * ldw, 1, N, K, 0, 0, base, ldbase};
+        if (launch_experts_mma(b, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+    }
     return launched(launch_lora_expand(a, c, s));
 }
 

@@ -20,14 +20,17 @@ struct ExpertsArgs {
     void *Y;
     int64_t ldy;
 };
-// CUDA cores, any alignment (experts_dot.cu); K == 0 included
-cudaError_t launch_experts_dot(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
+// mma.sync, any alignment (experts_mma.cu); K == 0 included
+cudaError_t launch_experts_mma(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
 
 // tcgen05 (experts_tc.cu): 16-byte aligned rows of X and W, K >= 1
 bool experts_tc_supported(const ExpertsArgs &a);
+bool experts_tc_faster(const ExpertsArgs &a, int num_sms);   // than the mma.sync kernel
 cudaError_t experts_tc_prepare();
 cudaError_t launch_experts_tc(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream);
 
+// Columns of a token's V: whole MMA steps.
+__host__ __device__ constexpr int lora_padded_rank(int R) { return (R + 31) / 32 * 32; }
 struct LoraArgs {
     const uint16_t *X;
     int64_t ldx;
@@ -38,7 +41,7 @@ struct LoraArgs {
     const int32_t *adapters, *ranks;
     const float *scales;
     int L, R, M, N, K;
-    float *V;            // [M, R], written by the first kernel, read by the second
+    uint16_t *V;         // [M][3][lora_padded_rank(R)], written by the first kernel, read by the second
     const float *base;   // fp32 [M, N] of the shared projection, row stride ldbase
     int64_t ldbase;
     void *Y;             // base itself (fp32), or bf16
@@ -47,9 +50,6 @@ struct LoraArgs {
 };
 cudaError_t launch_lora_shrink(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
 cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
-
-// Elements per vector load (8, 4, 2 or 1 bf16) that every address and stride in `all` (bytes) allows.
-inline int bf16_vec(uintptr_t all) { return all % 16 == 0 ? 8 : all % 8 == 0 ? 4 : all % 4 == 0 ? 2 : 1; }
 
 inline cudaError_t launch_plain(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl,
                                 void **args) {

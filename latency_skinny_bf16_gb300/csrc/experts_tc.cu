@@ -4,23 +4,28 @@
 //
 // At decode an expert has a few rows, so the weights of the experts that occur
 // are the traffic: the kernel is a stream of W through shared memory, once.
-//   * Work split.  The rows of W of all experts that have rows form one line
-//     of 8-row groups (an expert after the other; SwiGLU: a group is 8 gates
-//     and their 8 ups).  The CTAs, two per SM, each take an equal piece of
-//     that line, whatever the experts' number and sizes, and walk it in tiles
-//     of at most 128 rows of W that do not cross an expert.
-//   * Per tile, W (up to 128 rows) is the MMA's M side, up to NT rows of X its
+//   * Work split.  An expert's rows of W are 16-row groups (SwiGLU: a group is 8
+//     gates and their 8 ups), dealt evenly to tiles of at most 8 groups; the
+//     tiles of all experts that have rows are dealt evenly to the CTAs, two per
+//     SM.  The tiles' size is chosen in the kernel, where the number of experts
+//     that have rows is known.  (Equal pieces of the line of groups, whatever
+//     the tiles, left CTAs whose piece met an expert's end with twice the
+//     stages: 32 experts, 2 x 512 x 4096, 16 rows each: 80 us.)
+//   * Per tile, W (up to 128 rows) is the MMA's M side, up to 64 rows of X its
 //     N side (16, 32, 48 or 64, as the expert has rows).  An expert with more
-//     than NT rows is walked again for the next NT, its tile of W then in L2.
-//   * Thread 0 loads 64-element boxes of W and X by tensor-map TMA into a ring;
+//     than 64 rows is walked again for the next 64, its tile of W then in L2.
+//   * Thread 0 loads 64-element boxes of W and X by tensor-map TMA into a ring,
+//     a tile's height of W in one box (there is a map for each height: with
+//     boxes of 128, 64, 32, 16 and 8 rows put together the copies' number, about
+//     0.1 us each, was the limit of short tiles);
 //     thread 32 issues tcgen05.mma into four sets of tensor-memory
 //     accumulators in rotation, at most 16 MMAs a set; warps 2..5 add each set
 //     into fp32 registers (one row of W per thread, its tokens in registers)
 //     and store the tile at its end: the same bounded chains and rounded adds
 //     as the shared projections (the tensor core's own sums are biased).
-//   * SwiGLU: a tile is 64 gates on the MMA's rows 0..63 and their ups on rows
-//     64..127; at its end the ups go through shared memory to the gates'
-//     threads.
+//   * SwiGLU: a tile is up to 64 gates on the MMA's first rows and their ups on
+//     as many rows behind them; at its end the ups go through shared memory to
+//     the gates' threads.
 // Every wait is bounded.  A wait that gives up records an error and the CTA
 // winds down without storing: copies in flight and issued MMAs are waited for
 // (bounded) and the draining warps still meet at every barrier.
@@ -38,15 +43,16 @@ namespace {
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 enum : int { kWaitAcc = 5, kWaitAccEmpty = 6 };
 constexpr int kThreads = 192;          // TMA warp, MMA warp, four draining warps
-constexpr int kHeights = 5;            // W boxes of 128, 64, 32, 16, 8 rows
+constexpr int kGroups = 8;             // groups per tile: W boxes of 1 to 8 of them
+constexpr int kXBoxes = 4;             // X boxes of 16, 32, 48, 64 rows
 constexpr int kSets = 4;               // accumulator sets in rotation
 constexpr int kSetCols = 64;           // fp32 columns of a set
 constexpr int kTmemCols = kSets * kSetCols;
 constexpr int kCtasPerSm = 2;          // 2 x 256 columns fill an SM's tensor memory
 
 struct Maps {
-    CUtensorMap w[kHeights];
-    CUtensorMap x;                     // boxes of 16 rows
+    CUtensorMap w[kGroups];            // box heights of 1 to 8 groups (16 rows, SwiGLU 8)
+    CUtensorMap x[kXBoxes];
 };
 
 struct Params {
@@ -59,65 +65,70 @@ struct Params {
     uint64_t budget_ns;
 };
 
-// A stage: KB boxes of 128 rows of W, then KB boxes of NT rows of X.
-template <int NT> struct Shape {
-    static constexpr int kKB = 1;
-    static constexpr int kStage = kKB * (128 + NT) * 128;
-    static constexpr int kStages = (100 * 1024) / kStage;
-    static constexpr int kChunk = 4 / kKB;             // stages per accumulator set: 16 MMAs
-};
+// A stage holds up to 128 rows of W and 64 rows of X, 64 elements of K each; a
+// tile of half or a quarter of that takes 2 or 4 times the elements of K per
+// stage, so that short tiles keep as many bytes in flight and a CTA whose piece
+// meets an expert's end runs no more stages than the others (GB300, 16 experts,
+// 2048 x 2048, 2 rows each: 43 us with one box a stage).
+constexpr int kNT = 64;
+constexpr int kStage = (128 + kNT) * 128;
+constexpr int kStages = 4;
+__host__ __device__ inline int tile_boxes(int groups, int xb) {
+    return groups <= 2 && xb <= 1 ? 4 : groups <= 4 && xb <= 2 ? 2 : 1;
+}
 constexpr int kExBytes = 16 * 64 * 4;                  // SwiGLU: 16 tokens of 64 ups
-// after the ring: barriers, tensor-memory address, flags, the exchange, the experts' rows and list
-template <int NT> constexpr int bar_bytes() { return 8 * (2 * Shape<NT>::kStages + 2 * kSets + 1); }
-template <int NT> int smem_bytes(int E) {
-    const int b = 1024 + Shape<NT>::kStages * Shape<NT>::kStage + bar_bytes<NT>() + 16 + kExBytes + 4 * (E + 1) + 2 * E + 16;
-    return b < 78 * 1024 ? 78 * 1024 : b;              // never three CTAs on an SM: tensor memory holds two
+constexpr int kBarBytes = 8 * (2 * kStages + 2 * kSets + 1);
+// After the ring: barriers, tensor-memory address, flags, the exchange, the
+// experts' rows and list; 12 KB at least, for an MMA reads 128 rows from each
+// box of W, past the stage's end in the last one (those rows are not stored).
+int smem_bytes(int E) {
+    int tail = kBarBytes + 16 + kExBytes + 4 * (E + 1) + 2 * E + 16;
+    if (tail < 12 * 1024) tail = 12 * 1024;
+    return 1024 + kStages * kStage + tail;             // 110 KB: two CTAs on an SM, as tensor memory holds
 }
 
-// A piece of the line of groups: groups [g, g + ng) of expert e.
+// Groups [g, g + ng) of expert e.
 struct Tile {
     int e, g, ng, row0, count;
+    // X boxes of 16 rows for the rows from m0 on
+    __device__ __forceinline__ int xb(int m0) const { return (min(kNT, count - m0) + 15) / 16; }
 };
 
-// Walks a CTA's piece [i, i1) of the line; every role walks it for itself.
+// Walks a CTA's tiles [i, i1); every role walks them for itself.
 struct Walk {
-    int64_t i, i1;
-    int GN, most;                      // groups per expert, groups per tile
+    int i, i1;
+    int GN, nt;                        // groups and tiles per expert
     const int *row;                    // clamped offsets [E + 1]
     const uint16_t *active;            // the experts that have rows
     __device__ __forceinline__ bool next(Tile &t) {
         if (i >= i1) return false;
-        const int a = (int)(i / GN);
-        t.g = (int)(i - (int64_t)a * GN);
-        const int64_t end = (int64_t)(a + 1) * GN;
-        const int left = (int)((i1 < end ? i1 : end) - i);
-        const int n = (left + most - 1) / most;        // tiles left of this run, evenly
-        t.ng = (left + n - 1) / n;
+        const int a = i / nt, at = i - a * nt;
+        t.g = (int)((int64_t)at * GN / nt);
+        t.ng = (int)((int64_t)(at + 1) * GN / nt) - t.g;
         t.e = active[a];
         t.row0 = row[t.e];
         t.count = row[t.e + 1] - t.row0;
-        i += t.ng;
+        ++i;
         return true;
     }
 };
 
-template <int NT, bool SWIGLU>
+template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
 {
-    using S = Shape<NT>;
     extern __shared__ uint8_t smem_raw[];
     griddep_launch_dependents();
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
-    const uint32_t bars = base + S::kStages * S::kStage;
+    const uint32_t bars = base + kStages * kStage;
     auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
-    auto accf = [&](int b) { return bars + 8u * (2 * S::kStages + b); };
-    auto acce = [&](int b) { return bars + 8u * (2 * S::kStages + kSets + b); };
-    const uint32_t done = bars + 8u * (2 * S::kStages + 2 * kSets);
-    uint8_t *tail = smem + S::kStages * S::kStage + bar_bytes<NT>();
+    auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+    auto accf = [&](int b) { return bars + 8u * (2 * kStages + b); };
+    auto acce = [&](int b) { return bars + 8u * (2 * kStages + kSets + b); };
+    const uint32_t done = bars + 8u * (2 * kStages + 2 * kSets);
+    uint8_t *tail = smem + kStages * kStage + kBarBytes;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *mma_ok = reinterpret_cast<volatile int *>(tail + 4);
     float *ex = reinterpret_cast<float *>(tail + 16);
@@ -127,9 +138,9 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < kHeights; ++i) prefetch_tensormap(&maps.w[i]);
-        prefetch_tensormap(&maps.x);
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int i = 0; i < kGroups; ++i) prefetch_tensormap(&maps.w[i]);
+        for (int i = 0; i < kXBoxes; ++i) prefetch_tensormap(&maps.x[i]);
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -162,13 +173,23 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
         if (has) active[before + __popc(ball & ((1u << lane) - 1))] = (uint16_t)e;
         __syncthreads();
     }
-    const int GN = (p.N + 7) / 8;
-    const int64_t line = (int64_t)found * GN;
-    Walk walk{line * blockIdx.x / gridDim.x, line * (blockIdx.x + 1) / gridDim.x, GN, SWIGLU ? 8 : 16, row, active};
+    constexpr int kRows = SWIGLU ? 8 : 16;             // rows of W's first half per group
+    const int GN = (p.N + kRows - 1) / kRows;
+    // tiles per expert: the number for which the CTA with the most tiles has the
+    // least to do, a tile costing its groups and about one and a half of fixed work
+    int nt = 0;
+    float least = 0.f;
+    for (int ts = kGroups; ts >= 1; --ts) {
+        const int n = (GN + ts - 1) / ts;
+        const int64_t rounds = ((int64_t)found * n + gridDim.x - 1) / gridDim.x;
+        const float cost = (float)rounds * ((float)((GN + n - 1) / n) + 1.5f);
+        if (nt == 0 || cost < least) { nt = n; least = cost; }
+    }
+    const int64_t tiles = (int64_t)found * nt;
+    Walk walk{(int)(tiles * blockIdx.x / gridDim.x), (int)(tiles * (blockIdx.x + 1) / gridDim.x), GN, nt, row, active};
     if (walk.i >= walk.i1) return;     // the whole CTA
 
     const int boxes = (p.K + 63) / 64;
-    const int nk = (boxes + S::kKB - 1) / S::kKB;      // stages per tile and pass
 
     if (warp == 0) {
         if (lane == 0) {
@@ -177,44 +198,33 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
             bool go = true;
             Tile t;
             while (go && walk.next(t)) {
-                const int h = 8 * t.ng, n0 = 8 * t.g;
-                for (int m0 = 0; go && m0 < t.count; m0 += NT) {
-                    const int xb = (min(NT, t.count - m0) + 15) / 16;
-                    for (int ks = 0; ks < nk; ++ks, ++i) {
-                        const int s = (int)(i % S::kStages);
-                        if (i >= S::kStages &&
-                            !mbar_wait_bounded(empty(s), (uint32_t)((i / S::kStages - 1) & 1), p.budget_ns)) {
+                const int n0 = kRows * t.g;
+                for (int m0 = 0; go && m0 < t.count; m0 += kNT) {
+                    const int xb = t.xb(m0), kb = tile_boxes(t.ng, xb);
+                    for (int k0 = 0; k0 < boxes; k0 += kb, ++i) {
+                        const int s = (int)(i % kStages);
+                        if (i >= kStages &&
+                            !mbar_wait_bounded(empty(s), (uint32_t)((i / kStages - 1) & 1), p.budget_ns)) {
                             report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitProducerEmpty);
                             go = false;
                             break;
                         }
-                        const int nb = min(S::kKB, boxes - ks * S::kKB);
-                        mbar_arrive_expect_tx(full(s), (uint32_t)(nb * ((SWIGLU ? 2 : 1) * h + 16 * xb) * 128));
-                        const uint32_t st = base + s * S::kStage;
+                        const int nb = min(kb, boxes - k0);
+                        mbar_arrive_expect_tx(full(s), (uint32_t)(nb * 16 * (t.ng + xb) * 128));
+                        const uint32_t st = base + s * kStage;
                         for (int b = 0; b < nb; ++b) {
-                            const int k = (ks * S::kKB + b) * 64;
-                            int off = 0;
-#pragma unroll
-                            for (int q = 0; q < kHeights; ++q) {
-                                const int height = 128 >> q;
-                                if (SWIGLU && height == 128) continue;
-                                if (h - off >= height) {
-                                    const uint32_t dst = st + b * 128 * 128 + off * 128;
-                                    tma_load_stack(dst, &maps.w[q], k, n0 + off, t.e, full(s));
-                                    if (SWIGLU) tma_load_stack(dst + 64 * 128, &maps.w[q], k, p.N + n0 + off, t.e, full(s));
-                                    off += height;
-                                }
-                            }
-                            const uint32_t xd = st + S::kKB * 128 * 128 + b * NT * 128;
-                            for (int x = 0; x < xb; ++x)
-                                tma_load_2d(xd + x * 16 * 128, &maps.x, k, t.row0 + m0 + 16 * x, full(s));
+                            const int k = (k0 + b) * 64;
+                            const uint32_t dst = st + b * (128 / kb) * 128;
+                            tma_load_stack(dst, &maps.w[t.ng - 1], k, n0, t.e, full(s));
+                            if (SWIGLU) tma_load_stack(dst + (64 / kb) * 128, &maps.w[t.ng - 1], k, p.N + n0, t.e, full(s));
+                            tma_load_2d(st + 128 * 128 + b * (kNT / kb) * 128, &maps.x[xb - 1], k, t.row0 + m0, full(s));
                         }
                     }
                 }
             }
             // every copy issued has landed before the CTA exits
-            for (int64_t j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
-                if (!mbar_wait_bounded(full((int)(j % S::kStages)), (uint32_t)((j / S::kStages) & 1), kDrainNs))
+            for (int64_t j = i > kStages ? i - kStages : 0; j < i; ++j)
+                if (!mbar_wait_bounded(full((int)(j % kStages)), (uint32_t)((j / kStages) & 1), kDrainNs))
                     report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
         }
         __syncwarp();
@@ -230,35 +240,36 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
             bool go = true;
             Tile t;
             while (go && walk.next(t)) {
-                for (int m0 = 0; go && m0 < t.count; m0 += NT) {
-                    const uint32_t n = 16u * (uint32_t)((min(NT, t.count - m0) + 15) / 16);
+                for (int m0 = 0; go && m0 < t.count; m0 += kNT) {
+                    const int xb = t.xb(m0), kb = tile_boxes(t.ng, xb);
+                    const uint32_t n = 16u * (uint32_t)xb;
                     const uint32_t P = kSetCols / n;   // accumulators of a set, taken in turn
                     const uint32_t idesc = idesc_bf16_n<128>(n);
-                    for (int ks = 0; ks < nk; ++ks, ++i) {
-                        const int s = (int)(i % S::kStages), b = (int)(c % kSets);
-                        if (ks % S::kChunk == 0 && c >= kSets &&
+                    for (int k0 = 0; k0 < boxes; k0 += kb, ++i) {
+                        const int s = (int)(i % kStages), b = (int)(c % kSets);
+                        if (k0 % 4 == 0 && c >= kSets &&
                             !mbar_wait_bounded(acce(b), (uint32_t)((c / kSets - 1) & 1), p.budget_ns)) {
                             report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
                             go = false;
                             break;
                         }
-                        if (!mbar_wait_bounded(full(s), (uint32_t)((i / S::kStages) & 1), p.budget_ns)) {
+                        if (!mbar_wait_bounded(full(s), (uint32_t)((i / kStages) & 1), p.budget_ns)) {
                             report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
                             go = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t st = base + s * S::kStage;
-                        const int nb = min(S::kKB, boxes - ks * S::kKB);
-                        uint32_t q = (uint32_t)(ks % S::kChunk) * 4 * S::kKB;
+                        const uint32_t st = base + s * kStage;
+                        const int nb = min(kb, boxes - k0);
+                        uint32_t q = (uint32_t)(k0 % 4) * 4;   // a set takes four boxes: 16 MMAs
                         for (int bx = 0; bx < nb; ++bx)
 #pragma unroll
                             for (int j = 0; j < 4; ++j, ++q)
-                                umma_bf16(tmem + b * kSetCols + (q % P) * n, sw128_desc(st + bx * 128 * 128 + 32 * j),
-                                          sw128_desc(st + S::kKB * 128 * 128 + bx * NT * 128 + 32 * j), idesc,
+                                umma_bf16(tmem + b * kSetCols + (q % P) * n, sw128_desc(st + bx * (128 / kb) * 128 + 32 * j),
+                                          sw128_desc(st + 128 * 128 + bx * (kNT / kb) * 128 + 32 * j), idesc,
                                           q < P ? 0u : 1u);
                         umma_commit(empty(s));
-                        if (ks % S::kChunk == S::kChunk - 1 || ks == nk - 1) {
+                        if ((k0 + nb) % 4 == 0 || k0 + nb == boxes) {
                             umma_commit(accf(b));
                             ++c;
                         }
@@ -286,7 +297,7 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
             float acc[16 * XB];
 #pragma unroll
             for (int j = 0; j < 16 * XB; ++j) acc[j] = 0.f;
-            const int chunks = (nk + S::kChunk - 1) / S::kChunk;
+            const int chunks = (boxes + 3) / 4;
             for (int k = 0; k < chunks; ++k, ++c) {
                 const int b = (int)(c % kSets);
                 if (ok) {
@@ -300,11 +311,9 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
                 }
                 if (!ok) continue;     // the barriers below are still met
                 tc_fence_after();
-                // the chunk's MMAs reached min(P, MMAs) accumulators
-                const int mmas = 4 * min(boxes - k * 4, 4);
+                // the set's sums, in order (a chunk has four MMAs at least, P is four at most)
 #pragma unroll
                 for (int pp = 0; pp < P; ++pp) {
-                    if (pp >= mmas) break;
 #pragma unroll
                     for (int cc = 0; cc < XB; ++cc) {
                         uint32_t r[16];
@@ -318,27 +327,28 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acce(b));
             }
-            const int cols = min(NT, t.count - m0);
+            const int cols = min(kNT, t.count - m0);
             const int64_t y0 = (int64_t)(t.row0 + m0) * p.ldy;
             if constexpr (!SWIGLU) {
-                const int n = 8 * t.g + arow;
-                if (ok && arow < 8 * t.ng && n < p.N) {
+                const int n = kRows * t.g + arow;
+                if (ok && arow < kRows * t.ng && n < p.N) {
 #pragma unroll
                     for (int m = 0; m < 16 * XB; ++m)
                         if (m < cols) store_y(p.Y, p.out_bf16, y0 + m * p.ldy + n, acc[m]);
                 }
             } else {
-                const int n = 8 * t.g + (arow & 63);
-                const bool live = (arow & 63) < 8 * t.ng && n < p.N;
+                const int half = 64 / tile_boxes(t.ng, XB);          // the gates' rows, then the ups'
+                const int n = kRows * t.g + arow;
+                const bool live = arow < kRows * t.ng && n < p.N;
 #pragma unroll
                 for (int cc = 0; cc < XB; ++cc) {
-                    if (arow >= 64) {
+                    if (arow >= half && arow < 2 * half) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) ex[j * 64 + arow - 64] = acc[16 * cc + j];
+                        for (int j = 0; j < 16; ++j) ex[j * 64 + arow - half] = acc[16 * cc + j];
                     }
                     __syncwarp();
                     named_bar_sync(2, 128);
-                    if (arow < 64 && live && ok) {
+                    if (live && ok) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float g = acc[16 * cc + j];
@@ -353,16 +363,12 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
         };
         Tile t;
         while (walk.next(t)) {
-            for (int m0 = 0; m0 < t.count; m0 += NT) {
-                if constexpr (NT == 16) {
-                    tile(std::integral_constant<int, 1>{}, t, m0);
-                } else {
-                    switch ((min(NT, t.count - m0) + 15) / 16) {
-                        case 1: tile(std::integral_constant<int, 1>{}, t, m0); break;
-                        case 2: tile(std::integral_constant<int, 2>{}, t, m0); break;
-                        case 3: tile(std::integral_constant<int, 3>{}, t, m0); break;
-                        default: tile(std::integral_constant<int, 4>{}, t, m0); break;
-                    }
+            for (int m0 = 0; m0 < t.count; m0 += kNT) {
+                switch (t.xb(m0)) {
+                    case 1: tile(std::integral_constant<int, 1>{}, t, m0); break;
+                    case 2: tile(std::integral_constant<int, 2>{}, t, m0); break;
+                    case 3: tile(std::integral_constant<int, 3>{}, t, m0); break;
+                    default: tile(std::integral_constant<int, 4>{}, t, m0); break;
                 }
             }
         }
@@ -377,8 +383,7 @@ experts_tc_kernel(const __grid_constant__ Maps maps, const Params p)
 }
 
 using Kernel = void (*)(const Maps, const Params);
-const Kernel kKernels[2][2] = {{&experts_tc_kernel<16, false>, &experts_tc_kernel<16, true>},
-                               {&experts_tc_kernel<64, false>, &experts_tc_kernel<64, true>}};
+const Kernel kKernels[2] = {&experts_tc_kernel<false>, &experts_tc_kernel<true>};
 
 }  // namespace
 
@@ -387,9 +392,23 @@ bool experts_tc_supported(const ExpertsArgs &a) {
            a.ldx % 8 == 0 && a.ldw % 8 == 0 && a.ldwe % 8 == 0 && a.ldwe < (1ll << 38);
 }
 
+// The mma.sync kernel reads W at the rate of device memory while an expert has
+// up to 8 rows and reads it again (from L2) for the next 8; this one holds 64
+// rows but needs long lines to fill its tiles.  Measured on GB300, tcgen05
+// against mma.sync (us): 256 experts 2048 x 2048, 1 row each on average 166 and
+// 154, 2 rows 218 and 213; 7168 x 2048, 2 rows, unevenly 423 and 503; 32 experts
+// 2048 x 2048, 16 rows 54 and 83; 8 experts 16 rows, 4096 x 1024 (2048 groups)
+// 21 and 24, 2048 x 2048 (1024 groups) 27 and 24; 1 matrix 24576 x 1536, 64 rows
+// (1536 groups) 28 and 50.
+bool experts_tc_faster(const ExpertsArgs &a, int num_sms) {
+    const int per = a.swiglu ? 8 : 16;
+    const int64_t groups = (int64_t)(a.rows < a.E ? a.rows : a.E) * ((a.N + per - 1) / per), ctas = (int64_t)kCtasPerSm * num_sms;
+    return (a.rows >= 2 * a.E && groups >= kGroups * ctas) || (a.rows >= 8 * a.E && groups >= 5 * ctas);
+}
+
 cudaError_t experts_tc_prepare() {
-    for (int i = 0; i < 4; ++i) {
-        const cudaError_t e = set_max_dyn_smem(kKernels[i >> 1][i & 1]);
+    for (int i = 0; i < 2; ++i) {
+        const cudaError_t e = set_max_dyn_smem(kKernels[i]);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -398,25 +417,25 @@ cudaError_t experts_tc_prepare() {
 cudaError_t launch_experts_tc(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream) {
     Maps maps;
     const int64_t wrows = a.swiglu ? 2ll * a.N : a.N;
-    for (int h = 0; h < kHeights; ++h)
-        if (!encode_bf16_stack(&maps.w[h], a.W, a.K, wrows, a.E, a.ldw, a.ldwe, 128 >> h)) return cudaErrorInvalidValue;
-    if (!encode_bf16_2d(&maps.x, a.X, a.K, a.rows, a.ldx, 16)) return cudaErrorInvalidValue;
+    const int kRows = a.swiglu ? 8 : 16;
+    for (int h = 0; h < kGroups; ++h)
+        if (!encode_bf16_stack(&maps.w[h], a.W, a.K, wrows, a.E, a.ldw, a.ldwe, kRows * (h + 1))) return cudaErrorInvalidValue;
+    for (int h = 0; h < kXBoxes; ++h)
+        if (!encode_bf16_2d(&maps.x[h], a.X, a.K, a.rows, a.ldx, 16 * (h + 1))) return cudaErrorInvalidValue;
     const Params p{a.offsets, a.Y, a.ldy, a.rows, a.E, a.N, a.K, a.out_bf16, c.status, c.budget_ns};
-    // up to 16 rows in all, no expert has more: the shape with the smaller share of X
-    const int big = a.rows > 16;
-    const int64_t groups = (int64_t)(a.rows < a.E ? a.rows : a.E) * ((a.N + 7) / 8);
+    const int64_t groups = (int64_t)(a.rows < a.E ? a.rows : a.E) * ((a.N + kRows - 1) / kRows);
     const int64_t most = (int64_t)kCtasPerSm * c.num_sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(groups < most ? groups : most), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = big ? smem_bytes<64>(a.E) : smem_bytes<16>(a.E);
+    cfg.dynamicSmemBytes = smem_bytes(a.E);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kKernels[big][a.swiglu ? 1 : 0], maps, p);
+    return cudaLaunchKernelEx(&cfg, kKernels[a.swiglu ? 1 : 0], maps, p);
 }
 
 }  // namespace skinny

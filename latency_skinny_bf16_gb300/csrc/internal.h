@@ -153,6 +153,7 @@ struct CallCtx {
     int *status;         // device status word
     uint64_t budget_ns;  // budget of each bounded wait
     bool pdl;            // programmatic dependent launch (SKINNY_OPT_PDL)
+    int force_backend;   // SKINNY_OPT_FORCE_BACKEND
 };
 skinny_status_t call_context(CallCtx *c);   // the current device, set up if need be
 bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1);

@@ -1,244 +1,386 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection:
 //     V[m,r]  = s_a sum_k X[m,k] A[a][r][k]                 a = adapters[m], r < r_a
 //     Y[m,n]  = base[m,n] + sum_{r < r_a} V[m,r] B[a][n][r]  base = X W^T (skinny_gemm_bf16)
-// Three launches: the first (shrink) writes V in fp32, the second is the
-// projection, the third (expand) adds.  Both adapter kernels are bound by the
-// bytes of A and B, read once per adapter that occurs: the CTAs of the first
-// token of an adapter (its leader) serve every token that shares it, the CTAs
-// of the others leave.
+// Three launches: the first (shrink) writes V, the second is the projection,
+// the third (expand) adds.  V keeps the 24 bits of fp32 as three bf16 terms,
+// h = bf16(v), m = bf16(v - h), l = bf16(v - h - m): operands of the third
+// kernel's MMAs as they stand, with zeros from an adapter's rank on.  Both adapter kernels are bound by the
+// bytes of A and B, read once per adapter that occurs and eight (shrink: 32)
+// of its tokens; they take them straight from device memory into mma.sync
+// operands, 16 rows at a time, at any alignment (mma_rows.cuh).
 //
 // With programmatic dependent launch the shrink kernel lets the projection
 // start only after its own wait: what was launched before this call is then
 // complete for all three kernels, so the expand kernel may read the adapters'
-// ids and B before it waits for the projection.
-#include "dotload.cuh"
+// ids and ranks before it waits for the projection.
 #include "experts_gemm.h"
+#include "mma_rows.cuh"
 
 namespace skinny {
 namespace {
 
 constexpr int kMaxM = SKINNY_MAX_M;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 8;              // tokens held at a time
-
-// The tokens that share token m's adapter, if m is the first of them: their
-// number, 0 otherwise.  Tokens without an adapter count as sharing one.  list:
-// kMaxM ints.  Every thread of the CTA takes part.
-__device__ __forceinline__ int adapter_group(const int32_t *adapters, int M, int L, int m, int *list, int *adapter) {
-    __shared__ int s_id[kMaxM];
-    __shared__ int s_count;
-    for (int i = threadIdx.x; i < M; i += blockDim.x) {
-        const int id = __ldcg(adapters + i);
-        s_id[i] = (unsigned)id < (unsigned)L ? id : -1;
-    }
-    __syncthreads();
-    const int a = s_id[m];
-    if (threadIdx.x < 32) {
-        int n = 0;
-        bool first = true;
-        for (int i0 = 0; i0 < M; i0 += 32) {
-            const int i = i0 + threadIdx.x;
-            const unsigned same = __ballot_sync(0xFFFFFFFFu, i < M && s_id[i] == a);
-            if (same && i0 + __ffs(same) - 1 < m) first = false;
-            if (same >> threadIdx.x & 1) list[n + __popc(same & ((1u << threadIdx.x) - 1))] = i;
-            n += __popc(same);
-        }
-        if (threadIdx.x == 0) s_count = first ? n : 0;
-    }
-    __syncthreads();
-    *adapter = a;
-    return s_count;
-}
 
 __device__ __forceinline__ int adapter_rank(const int32_t *ranks, int a, int R) {
     return ranks ? max(0, min(R, __ldcg(ranks + a))) : R;
 }
-
-// Grid (ceil(R / 2), M).  Two rows of A per CTA, four warps along K each: warp
-// q takes the 256-element pieces q, q + 4, ... of its row against eight tokens
-// at a time, and the four sums are added in order.
-constexpr int kShrinkRows = 2;
-constexpr int kShrinkParts = kWarps / kShrinkRows;
-template <int V>
-__global__ void __launch_bounds__(kThreads)
-lora_shrink_kernel(const uint16_t *__restrict__ X, int64_t ldx, const uint16_t *__restrict__ A, int64_t lda,
-                   int64_t ldae, const int32_t *__restrict__ adapters, const int32_t *__restrict__ ranks,
-                   const float *__restrict__ scales, int L, int R, int M, int K, float *__restrict__ Vout)
-{
-    __shared__ int list[kMaxM];
-    __shared__ float part[kShrinkRows][kShrinkParts][kTile];
-    griddep_wait();
-    griddep_launch_dependents();
-    int a;
-    const int count = adapter_group(adapters, M, L, blockIdx.y, list, &a);
-    if (count == 0 || a < 0) return;
-    const int rank = adapter_rank(ranks, a, R);
-    const int r0 = blockIdx.x * kShrinkRows;
-    if (r0 >= rank) return;
-    const float scale = scales ? __ldcg(scales + a) : 1.f;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = warp / kShrinkParts, q = warp % kShrinkParts;
-    const bool live = r0 + row < rank;
-    const uint16_t *ar = A + (int64_t)a * ldae + (int64_t)(live ? r0 + row : r0) * lda;
-    for (int t0 = 0; t0 < count; t0 += kTile) {
-        float acc[kTile];
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) acc[t] = 0.f;
-        if (live) {
-            for (int k0 = q * 256; k0 < K; k0 += kShrinkParts * 256) {
-                float w[8];
-                load8<V, true>(ar, k0, K, lane, w);
-#pragma unroll
-                for (int t = 0; t < kTile; ++t) {
-                    if (t0 + t >= count) break;
-                    float x[8], p = 0.f;
-                    load8<V, false>(X + (int64_t)list[t0 + t] * ldx, k0, K, lane, x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p = fmaf(w[j], x[j], p);
-                    acc[t] += p;
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) {
-            if (t0 + t >= count) break;
-            acc[t] = warp_sum(acc[t]);
-            if (lane == 0) part[row][q][t] = acc[t];
-        }
-        __syncthreads();
-        const int t = threadIdx.x % kTile, rr = threadIdx.x / kTile;
-        if (rr < kShrinkRows && r0 + rr < rank && t0 + t < count) {
-            float s = part[rr][0][t];
-            for (int i = 1; i < kShrinkParts; ++i) s += part[rr][i][t];
-            Vout[(int64_t)list[t0 + t] * R + r0 + rr] = s * scale;
-        }
-        __syncthreads();
-    }
+__device__ __forceinline__ int adapter_id(const int32_t *adapters, int m, int L) {
+    const int id = __ldcg(adapters + m);
+    return (unsigned)id < (unsigned)L ? id : -1;
 }
 
-// Grid (ceil(N / kExpandCols), M).  G lanes share a row of B, eight elements
-// each (G = the power of two covering R / 8), so a warp holds 32 / G outputs at
-// once; a lane's eight V of eight tokens stay in registers while the rows of B
-// stream past.  The sums of a CTA's columns are gathered in shared memory and
-// added to the base in whole rows.
-constexpr int kExpandCols = 128;
-template <int V>
-__global__ void __launch_bounds__(kThreads)
-lora_expand_kernel(const uint16_t *__restrict__ B, int64_t ldb, int64_t ldbe, const int32_t *__restrict__ adapters,
-                   const int32_t *__restrict__ ranks, int L, int R, int G, int M, int N, const float *__restrict__ Vin,
-                   const float *base, int64_t ldbase, void *Y, int64_t ldy, int out_bf16)
+// ------------------------------------------------------------------ shrink
+// Grid (RP / 16, M): the CTAs of the first token of an adapter serve every
+// token that shares it, those of the others leave.  Sixteen rows of A per CTA;
+// its warps split K in pieces of 64 and their sums are added in order.
+constexpr int kShrinkWarps = 16;
+constexpr int kShrinkTT = 4;           // tokens per pass: 8 * 4
+
+struct ShrinkParams {
+    const uint16_t *X;
+    int64_t ldx;
+    const uint16_t *A;
+    int64_t lda, ldae;
+    const int32_t *adapters, *ranks;
+    const float *scales;
+    int L, R, M, K;
+    uint16_t *V;         // [M][3][RP], RP = lora_padded_rank(R)
+    Extent xe, ae;
+};
+
+// The three terms of v: their sum is within 2^-24 |v| of it (exact but for the
+// smallest values).  An infinite or NaN v is its first term alone.
+__device__ __forceinline__ void split3(float v, uint16_t &h, uint16_t &m, uint16_t &l) {
+    h = f32_to_bf16_rn(v);
+    const float r = isfinite(v) ? v - bf16_one(h) : 0.f;
+    m = f32_to_bf16_rn(r);
+    l = f32_to_bf16_rn(r - bf16_one(m));
+}
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(32 * kShrinkWarps)
+lora_shrink_kernel(const ShrinkParams p)
 {
-    __shared__ int list[kMaxM];
-    __shared__ float add[kTile][kExpandCols];
-    griddep_launch_dependents();
-    int a;
-    const int count = adapter_group(adapters, M, L, blockIdx.y, list, &a);
-    const int rank = a >= 0 ? adapter_rank(ranks, a, R) : 0;
+    __shared__ int s_id[kMaxM], list[kMaxM];
+    __shared__ int s_count;
+    __shared__ __align__(16) float part[kShrinkWarps][kShrinkTT][32][4];
     griddep_wait();
-    if (count == 0 || (a < 0 && !out_bf16)) return;   // nothing to add, and fp32: the base is Y
+    griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n0 = blockIdx.x * kExpandCols, cols = min(kExpandCols, N - n0);
-    const int c = lane % G, per = 32 / G;
-    for (int t0 = 0; t0 < count; t0 += kTile) {
-        const int tn = min(kTile, count - t0);
-        if (rank > 0) {
-            float v[kTile][8];
-#pragma unroll
-            for (int t = 0; t < kTile; ++t)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[t][j] = (t < tn && 8 * c + j < rank) ? __ldcg(Vin + (int64_t)list[t0 + t] * R + 8 * c + j) : 0.f;
-            for (int i = warp * per + lane / G; i < kExpandCols; i += kWarps * per) {
-                float b[8];
-                const uint16_t *row = B + (int64_t)a * ldbe + (int64_t)(n0 + min(i, cols - 1)) * ldb + 8 * c;
-                const int len = rank - 8 * c;
-                // a vector never passes the row's R elements; what lies past the rank becomes 0
-#pragma unroll
-                for (int u = 0; u < 8; u += V) {
-                    if (u + V <= len) {
-                        if constexpr (V == 8) {
-                            const uint4 q = ldg_stream_v4(row);
-                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) { b[2 * h] = bf16_lo(w[h]); b[2 * h + 1] = bf16_hi(w[h]); }
-                        } else if constexpr (V == 4) {
-                            const uint2 q = ldg_stream_v2(row + u);
-                            b[u] = bf16_lo(q.x); b[u + 1] = bf16_hi(q.x); b[u + 2] = bf16_lo(q.y); b[u + 3] = bf16_hi(q.y);
-                        } else if constexpr (V == 2) {
-                            const uint32_t q = ldg_stream_u32(row + u);
-                            b[u] = bf16_lo(q); b[u + 1] = bf16_hi(q);
-                        } else {
-                            b[u] = bf16_one(ldg_stream_u16(row + u));
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) b[u + j] = u + j < len ? bf16_one(ldg_stream_u16(row + u + j)) : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < kTile; ++t) {
-                    if (t >= tn) break;
-                    float p = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p = fmaf(b[j], v[t][j], p);
-                    for (int o = G >> 1; o > 0; o >>= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
-                    if (c == 0) add[t][i] = p;
-                }
-            }
-            __syncthreads();
+    const int g = lane >> 2, t = lane & 3;
+    const int m = blockIdx.y, M = p.M, R = p.R, K = p.K;
+    const int a = adapter_id(p.adapters, m, p.L);
+    if (a < 0) return;
+    const int rank = adapter_rank(p.ranks, a, R);
+    const float scale = p.scales ? __ldcg(p.scales + a) : 1.f;
+    if (tid < M) s_id[tid] = adapter_id(p.adapters, tid, p.L);
+    __syncthreads();
+    if (warp == 0) {
+        int n = 0;
+        bool first = true;
+        for (int i0 = 0; i0 < M; i0 += 32) {
+            const int i = i0 + lane;
+            const unsigned same = __ballot_sync(0xFFFFFFFFu, i < M && s_id[i] == a);
+            if (same && i0 + __ffs(same) - 1 < m) first = false;
+            if (same >> lane & 1) list[n + __popc(same & ((1u << lane) - 1))] = i;
+            n += __popc(same);
         }
-        for (int i = tid; i < tn * kExpandCols; i += kThreads) {
-            const int t = i / kExpandCols, n = i % kExpandCols;
-            if (n >= cols) continue;
-            const int64_t m = list[t0 + t];
-            const float y = __ldcg(base + m * ldbase + n0 + n) + (rank > 0 ? add[t][n] : 0.f);
-            store_y(Y, out_bf16, m * ldy + n0 + n, y);
+        if (lane == 0) s_count = first ? n : 0;
+    }
+    __syncthreads();
+    const int count = s_count;
+    const int r0 = blockIdx.x * 16;
+    if (count == 0) return;
+    const int RP = lora_padded_rank(R);
+    if (r0 >= rank) {                  // rows past the rank: zeros
+        for (int o = tid; o < count * 48; o += 32 * kShrinkWarps)
+            p.V[((int64_t)list[o / 48] * 3 + o % 48 / 16) * RP + r0 + o % 16] = 0;
+        return;
+    }
+    // rows past the rank repeat its last one; their sums are not stored
+    const uint16_t *Aa = p.A + (int64_t)a * p.ldae;
+    const uint16_t *al = Aa + (int64_t)min(r0 + g, rank - 1) * p.lda, *ah = Aa + (int64_t)min(r0 + 8 + g, rank - 1) * p.lda;
+    for (int t0 = 0; t0 < count; t0 += 8 * kShrinkTT) {
+        const int nt = min(kShrinkTT, (count - t0 + 7) / 8);
+        const uint16_t *x[kShrinkTT];
+        bool live[kShrinkTT];
+        float acc[kShrinkTT][4];
+#pragma unroll
+        for (int q = 0; q < kShrinkTT; ++q) {
+            live[q] = t0 + 8 * q + g < count;
+            x[q] = p.X + (int64_t)list[live[q] ? t0 + 8 * q + g : t0] * p.ldx;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[q][j] = 0.f;
+        }
+        auto step = [&](int k, int n) {
+            uint4 l[2], h[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                l[s] = load_row8<ALIGNED, true>(al, k + 32 * s + 8 * t, K, p.ae);
+                h[s] = load_row8<ALIGNED, true>(ah, k + 32 * s + 8 * t, K, p.ae);
+            }
+#pragma unroll
+            for (int q = 0; q < kShrinkTT; ++q) {
+                if (q >= n) break;
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    mma_rows32(d, l[s], h[s],
+                               live[q] ? load_row8<ALIGNED, false>(x[q], k + 32 * s + 8 * t, K, p.xe) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[q][j] += d[j];
+            }
+        };
+        if (nt == 1) {                 // the usual case: more steps of K in flight
+#pragma unroll 4
+            for (int k = 64 * warp; k < K; k += 64 * kShrinkWarps) step(k, 1);
+        } else {
+            for (int k = 64 * warp; k < K; k += 64 * kShrinkWarps) step(k, nt);
+        }
+#pragma unroll
+        for (int q = 0; q < kShrinkTT; ++q)
+            if (q < nt) *reinterpret_cast<float4 *>(part[warp][q][lane]) = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+        __syncthreads();
+        for (int o = tid; o < nt * 128; o += 32 * kShrinkWarps) {
+            const int q = o >> 7, sl = (o >> 2) & 31, j = o & 3;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kShrinkWarps; ++w) s += part[w][q][sl][j];
+            const int i = t0 + 8 * q + 2 * (sl & 3) + (j & 1), r = r0 + (sl >> 2) + 8 * (j >> 1);
+            if (i < count) {
+                uint16_t *v = p.V + (int64_t)list[i] * 3 * RP + r;
+                split3(r < rank ? s * scale : 0.f, v[0], v[RP], v[2 * RP]);
+            }
         }
         __syncthreads();
     }
 }
+
+// ------------------------------------------------------------------ expand
+// Persistent CTAs.  Each builds the list of adapters that occur, with their
+// tokens, while the projection still runs; the line of (adapter, block of rows
+// of B) is then dealt to the warps, which do not meet again.  A warp takes up
+// to 4 x 16 rows of B at a time against eight tokens, 32 columns (two k16 MMA
+// steps, three terms of V) at a time: at most six MMAs are summed in the
+// tensor core before a rounded add.
+constexpr int kExpandWarps = 8;
+constexpr int kExpandTiles = 4;
+
+struct ExpandParams {
+    const uint16_t *B;
+    int64_t ldb, ldbe;
+    const int32_t *adapters, *ranks;
+    int L, R, M, N;
+    const uint16_t *V;
+    const float *base;
+    int64_t ldbase;
+    void *Y;
+    int64_t ldy;
+    int out_bf16;
+    Extent be;
+};
+
+// T x 16 rows of one adapter's B from row n0, for its tokens tok[0, cnt).  FULL: all of them below N.
+template <bool ALIGNED, int T, bool FULL>
+__device__ __forceinline__ void expand_piece(const ExpandParams &p, const uint16_t *Ba, int n0, int rank, int RP,
+                                             const int *tok, int cnt, int g, int t) {
+    const int N = p.N;
+    // rows past the end repeat the last one; they are not stored
+    const uint16_t *row[T][2];
+    bool inside = true;
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = n0 + 16 * j + 8 * h + g;
+            row[j][h] = Ba + (int64_t)(FULL ? n : min(n, N - 1)) * p.ldb + 8 * t;
+            if (!ALIGNED) inside = inside && row_inside(row[j][h] - 8 * t, rank, p.be);
+        }
+    if (!ALIGNED) inside = __all_sync(0xFFFFFFFFu, inside);
+    for (int t0 = 0; t0 < cnt; t0 += 8) {
+        // the base of this lane's results, which the products are added to: rows g, g + 8 of each tile, tokens 2t, 2t + 1
+        float acc[T][4];
+        bool mine[2];
+        int64_t m[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            mine[c] = t0 + 2 * t + c < cnt;
+            m[c] = tok[mine[c] ? t0 + 2 * t + c : t0];
+            const float *b = p.base + m[c] * p.ldbase + n0 + g;
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    acc[j][2 * h + c] = 0.f;
+                    if (mine[c] && (FULL || n0 + 16 * j + 8 * h + g < N)) acc[j][2 * h + c] = __ldcg(b + 16 * j + 8 * h);
+                }
+        }
+        const bool live = t0 + g < cnt;
+        const uint16_t *v = p.V + (int64_t)tok[live ? t0 + g : t0] * 3 * RP + 8 * t;
+        auto terms = [&](int r, uint4 (&vt)[3]) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                vt[i] = make_uint4(0, 0, 0, 0);
+                if (live) vt[i] = ldg_v4(v + i * RP + r);
+            }
+        };
+        auto products = [&](int j, const uint4 &lo, const uint4 &hi, const uint4 (&vt)[3]) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_rows32(d, lo, hi, vt[2]);
+            mma_rows32(d, lo, hi, vt[1]);
+            mma_rows32(d, lo, hi, vt[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[j][c] += d[c];
+        };
+        int r = 0;
+        if (inside) {
+            for (; r + 64 <= rank; r += 64) {
+                uint4 w[T][2][2], vt[2][3];
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) w[j][h][s] = load_whole8<ALIGNED, true>(row[j][h], r + 32 * s);
+                terms(r, vt[0]);
+                terms(r + 32, vt[1]);
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) products(j, w[j][0][s], w[j][1][s], vt[s]);
+            }
+            if (r + 32 <= rank) {
+                uint4 w[T][2], vt[3];
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) w[j][h] = load_whole8<ALIGNED, true>(row[j][h], r);
+                terms(r, vt);
+#pragma unroll
+                for (int j = 0; j < T; ++j) products(j, w[j][0], w[j][1], vt);
+                r += 32;
+            }
+        }
+        for (; r < rank; r += 32) {    // the last columns, or rows at an end of B
+            uint4 w[T][2], vt[3];
+            const bool whole = inside && r + 8 * t + 8 <= rank;
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    w[j][h] = make_uint4(0, 0, 0, 0);
+                    if (whole) w[j][h] = load_whole8<ALIGNED, true>(row[j][h], r);
+                }
+            if (!whole && r + 8 * t < rank) {
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) w[j][h] = load_row8<ALIGNED, true>(row[j][h], r, rank - 8 * t, p.be);
+            }
+            terms(r, vt);
+#pragma unroll
+            for (int j = 0; j < T; ++j) products(j, w[j][0], w[j][1], vt);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int64_t at = m[c] * p.ldy + n0 + g;
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (mine[c] && (FULL || n0 + 16 * j + 8 * h + g < N))
+                        store_y(p.Y, p.out_bf16, at + 16 * j + 8 * h, acc[j][2 * h + c]);
+        }
+    }
+}
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(32 * kExpandWarps, 2)
+lora_expand_kernel(const ExpandParams p)
+{
+    __shared__ int s_id[kMaxM], s_lead[kMaxM], list[kMaxM];
+    __shared__ int g_first[kMaxM], g_count[kMaxM], g_adapter[kMaxM], g_rank[kMaxM];
+    __shared__ int s_groups;
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int M = p.M, N = p.N, R = p.R, RP = lora_padded_rank(R);
+    if (tid == 0) s_groups = 0;
+    if (tid < M) s_id[tid] = adapter_id(p.adapters, tid, p.L);
+    __syncthreads();
+    // token i: its adapter's first token, its place among the tokens that share it
+    int lead = 0, among = 0, count = 0;
+    const bool take = tid < M && (s_id[tid] >= 0 || p.out_bf16);   // fp32: the base is Y already
+    if (tid < M) {
+        lead = tid;
+        for (int j = M - 1; j >= 0; --j)
+            if (s_id[j] == s_id[tid]) {
+                lead = j;
+                ++count;
+                among += j < tid ? 1 : 0;
+            }
+        s_lead[tid] = take ? lead : kMaxM;
+    }
+    __syncthreads();
+    if (take) {
+        int before = 0, group = 0;
+        for (int j = 0; j < M; ++j) {
+            before += s_lead[j] < lead ? 1 : 0;
+            group += (s_lead[j] == j && j < lead) ? 1 : 0;
+        }
+        list[before + among] = tid;
+        if (lead == tid) {
+            g_first[group] = before;
+            g_count[group] = count;
+            g_adapter[group] = s_id[tid];
+            g_rank[group] = s_id[tid] >= 0 ? adapter_rank(p.ranks, s_id[tid], R) : 0;
+            atomicMax(&s_groups, group + 1);
+        }
+    }
+    __syncthreads();
+    const int groups = s_groups;
+    const int warps = (int)gridDim.x * kExpandWarps;
+    // rows per piece: 64, or 16 while that leaves warps without work
+    const int tiles = (int64_t)groups * ((N + 16 * kExpandTiles - 1) / (16 * kExpandTiles)) < warps ? 1 : kExpandTiles;
+    const int pieces = (N + 16 * tiles - 1) / (16 * tiles);
+    griddep_wait();
+    for (int64_t u = (int64_t)blockIdx.x + (int64_t)gridDim.x * warp; u < (int64_t)groups * pieces; u += warps) {
+        const int gr = (int)(u / pieces), n0 = (int)(u - (int64_t)gr * pieces) * 16 * tiles;
+        const uint16_t *Ba = p.B + (int64_t)max(0, g_adapter[gr]) * p.ldbe;
+        const int rank = g_rank[gr], cnt = g_count[gr];
+        const int *tok = list + g_first[gr];
+        if (tiles == kExpandTiles && n0 + 16 * kExpandTiles <= N)
+            expand_piece<ALIGNED, kExpandTiles, true>(p, Ba, n0, rank, RP, tok, cnt, g, t);
+        else
+            for (int j = 0; j < tiles && n0 + 16 * j < N; ++j)
+                expand_piece<ALIGNED, 1, false>(p, Ba, n0 + 16 * j, rank, RP, tok, cnt, g, t);
+    }
+}
+
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
 }  // namespace
 
 cudaError_t launch_lora_shrink(const LoraArgs &a, const CallCtx &c, cudaStream_t stream) {
-    const uint16_t *X = a.X, *A = a.A;
-    int64_t ldx = a.ldx, lda = a.lda, ldae = a.ldae;
-    const int32_t *ad = a.adapters, *rk = a.ranks;
-    const float *sc = a.scales;
-    int L = a.L, R = a.R, M = a.M, K = a.K;
-    float *V = a.V;
-    void *args[] = {&X, &ldx, &A, &lda, &ldae, &ad, &rk, &sc, &L, &R, &M, &K, &V};
-    const uintptr_t all = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(A) | (uintptr_t)(2 * ldx) |
-                          (uintptr_t)(2 * lda) | (uintptr_t)(2 * ldae);
-    const void *fn;
-    switch (bf16_vec(all)) {
-        case 8: fn = (const void *)lora_shrink_kernel<8>; break;
-        case 4: fn = (const void *)lora_shrink_kernel<4>; break;
-        case 2: fn = (const void *)lora_shrink_kernel<2>; break;
-        default: fn = (const void *)lora_shrink_kernel<1>; break;
-    }
-    return launch_plain(fn, dim3((R + kShrinkRows - 1) / kShrinkRows, M), kThreads, 0, stream, c.pdl, args);
+    ShrinkParams p{a.X, a.ldx, a.A, a.lda, a.ldae, a.adapters, a.ranks, a.scales, a.L, a.R, a.M, a.K, a.V,
+                   {addr(a.X), addr(a.X) + (uintptr_t)(2 * ((a.M - 1) * a.ldx + a.K))},
+                   {addr(a.A), addr(a.A) + (uintptr_t)(2 * ((a.L - 1) * a.ldae + (a.R - 1) * a.lda + a.K))}};
+    void *args[] = {&p};
+    const bool al = (addr(a.X) | addr(a.A)) % 16 == 0 && (a.ldx | a.lda | a.ldae) % 8 == 0;
+    return launch_plain(al ? (const void *)lora_shrink_kernel<true> : (const void *)lora_shrink_kernel<false>,
+                        dim3(lora_padded_rank(a.R) / 16, a.M), 32 * kShrinkWarps, 0, stream, c.pdl, args);
 }
 
 cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t stream) {
-    const uint16_t *B = a.B;
-    int64_t ldb = a.ldb, ldbe = a.ldbe, ldbase = a.ldbase, ldy = a.ldy;
-    const int32_t *ad = a.adapters, *rk = a.ranks;
-    int L = a.L, R = a.R, M = a.M, N = a.N, ob = a.out_bf16, G = 1;
-    while (8 * G < R) G *= 2;
-    const float *V = a.V, *base = a.base;
-    void *Y = a.Y;
-    void *args[] = {&B, &ldb, &ldbe, &ad, &rk, &L, &R, &G, &M, &N, &V, &base, &ldbase, &Y, &ldy, &ob};
-    const uintptr_t all = reinterpret_cast<uintptr_t>(B) | (uintptr_t)(2 * ldb) | (uintptr_t)(2 * ldbe);
-    const void *fn;
-    switch (bf16_vec(all)) {
-        case 8: fn = (const void *)lora_expand_kernel<8>; break;
-        case 4: fn = (const void *)lora_expand_kernel<4>; break;
-        case 2: fn = (const void *)lora_expand_kernel<2>; break;
-        default: fn = (const void *)lora_expand_kernel<1>; break;
-    }
-    return launch_plain(fn, dim3((N + kExpandCols - 1) / kExpandCols, M), kThreads, 0, stream, c.pdl, args);
+    ExpandParams p{a.B, a.ldb, a.ldbe, a.adapters, a.ranks, a.L, a.R, a.M, a.N, a.V, a.base, a.ldbase, a.Y, a.ldy,
+                   a.out_bf16, {addr(a.B), addr(a.B) + (uintptr_t)(2 * ((a.L - 1) * a.ldbe + (a.N - 1) * a.ldb + a.R))}};
+    void *args[] = {&p};
+    const bool al = addr(a.B) % 16 == 0 && (a.ldb | a.ldbe) % 8 == 0;
+    // two CTAs per SM, or a warp for every 16 rows of every token's adapter when these are fewer
+    const int64_t pieces = (int64_t)a.M * ((a.N + 15) / 16), want = (pieces + kExpandWarps - 1) / kExpandWarps;
+    const int most = 2 * c.num_sms;
+    return launch_plain(al ? (const void *)lora_expand_kernel<true> : (const void *)lora_expand_kernel<false>,
+                        dim3((unsigned)(want < most ? want : most)), 32 * kExpandWarps, 0, stream, c.pdl, args);
 }
 
 }  // namespace skinny

@@ -12,6 +12,11 @@ from __future__ import annotations
 
 import ctypes
 
+try:
+    import torch
+except ImportError:      # the C-named functions need none
+    torch = None
+
 import latency_skinny_bf16_gb300 as _sk
 
 SKINNY_BF16 = 0
@@ -53,19 +58,29 @@ def bind(lib: ctypes.CDLL) -> None:
     lib.skinny_lora_workspace.restype = ll
 
 
+_loaded = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _loaded
+    if _loaded is None:
+        _loaded = _sk.load_library()
+    return _loaded
+
+
 # ---------------------------------------------------------------- C-named wrappers (raw pointers)
 
 def skinny_expert_dispatch(ids: int, ldid: int, X: int, ldx: int, T: int, k: int, E: int, H: int, dtype: int,
                            pos: int, order: int, offsets: int, Xs: int, ldxs: int, stream: int = 0) -> int:
     """Raw C call; returns the skinny_status_t."""
-    return _sk.load_library().skinny_expert_dispatch(ids, ldid, X, ldx, T, k, E, H, dtype, pos, order, offsets, Xs,
+    return _lib().skinny_expert_dispatch(ids, ldid, X, ldx, T, k, E, H, dtype, pos, order, offsets, Xs,
                                                      ldxs, stream)
 
 
 def skinny_expert_combine(Ys: int, ldys: int, rows: int, pos: int, weights: int, ldw: int, T: int, k: int, H: int,
                           in_dtype: int, out_dtype: int, Y: int, ldy: int, stream: int = 0) -> int:
     """Raw C call; returns the skinny_status_t."""
-    return _sk.load_library().skinny_expert_combine(Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype, out_dtype,
+    return _lib().skinny_expert_combine(Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype, out_dtype,
                                                     Y, ldy, stream)
 
 
@@ -73,14 +88,14 @@ def skinny_expert_combine_grad(dY: int, lddy: int, Ys: int, ldys: int, rows: int
                                T: int, k: int, H: int, dtype: int, dYs: int, lddys: int, dweights: int, lddw: int,
                                stream: int = 0) -> int:
     """Raw C call; returns the skinny_status_t."""
-    return _sk.load_library().skinny_expert_combine_grad(dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype,
+    return _lib().skinny_expert_combine_grad(dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype,
                                                          dYs, lddys, dweights, lddw, stream)
 
 
 def skinny_experts_gemm_bf16(Xs: int, ldx: int, rows: int, offsets: int, W: int, ldw: int, ldwe: int, E: int, N: int,
                              K: int, act: int, out_dtype: int, Y: int, ldy: int, stream: int = 0) -> int:
     """Raw C call; returns the skinny_status_t."""
-    return _sk.load_library().skinny_experts_gemm_bf16(Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act, out_dtype,
+    return _lib().skinny_experts_gemm_bf16(Xs, ldx, rows, offsets, W, ldw, ldwe, E, N, K, act, out_dtype,
                                                        Y, ldy, stream)
 
 
@@ -89,78 +104,73 @@ def skinny_lora_gemm_bf16(X: int, ldx: int, W: int, ldw: int, A: int, lda: int, 
                           N: int, K: int, out_dtype: int, workspace: int, workspace_bytes: int,
                           stream: int = 0) -> int:
     """Raw C call; returns the skinny_status_t."""
-    return _sk.load_library().skinny_lora_gemm_bf16(X, ldx, W, ldw, A, lda, ldae, B, ldb, ldbe, adapters, ranks,
+    return _lib().skinny_lora_gemm_bf16(X, ldx, W, ldw, A, lda, ldae, B, ldb, ldbe, adapters, ranks,
                                                     scales, L, R, Y, ldy, M, N, K, out_dtype, workspace,
                                                     workspace_bytes, stream)
 
 
 def skinny_lora_workspace(M: int, N: int, R: int, out_dtype: int) -> int:
     """Bytes of workspace of skinny_lora_gemm_bf16; 0 for sizes it refuses."""
-    return _sk.load_library().skinny_lora_workspace(M, N, R, out_dtype)
+    return _lib().skinny_lora_workspace(M, N, R, out_dtype)
 
 
 # ---------------------------------------------------------------- tensors
 
 def _dtype(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
+    d = t.dtype
+    if d is torch.bfloat16:
         return SKINNY_BF16
-    if t.dtype == torch.float32:
+    if d is torch.float32:
         return SKINNY_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, not {d}")
 
 
 def _rows(t, name, dtype=None):
-    """Row stride of a CUDA matrix with unit column stride."""
+    """(rows, columns, row stride) of a CUDA matrix with unit column stride."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA matrix, not {tuple(t.shape)} on {t.device}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     m, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if n > 1 and one != 1:
         raise ValueError(f"{name} needs unit column stride")
     if m <= 1:
-        return max(n, 1)
-    ld = t.stride(0)
+        return m, n, n or 1
     if ld < n:
         raise ValueError(f"{name} needs rows that do not overlap")
-    return ld
+    return m, n, ld
 
 
 def _flat(t, name, n, dtype):
-    """A contiguous CUDA tensor of n elements."""
-    if t.dtype != dtype:
+    """Address of a contiguous CUDA tensor of n elements."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_cuda or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
-    return t
+    return t.data_ptr()
 
 
-class _On:
-    """The stream a call runs on: torch's current one, or the one that is given.
-    Tensors made inside are made on it, so their memory is not handed to
-    another stream's work while the call may still use it."""
+def _on(stream, device):
+    """The context of a given stream: inside it is torch's current one, so what
+    a call allocates belongs to it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
-    def __init__(self, stream, device):
-        import torch
-        self.guard = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.handle = stream.cuda_stream
-            self.guard = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
+def _current(device):
+    """Handle of torch's current stream."""
+    return torch.cuda.current_stream(device).cuda_stream
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+
+if torch is not None and hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _current(device):  # noqa: F811  (the same handle without a Stream object)
+        return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _refused(st, what):
+    raise _sk.SkinnyError(st, what)
 
 
 def expert_dispatch(ids, num_experts, x=None, xs=None, pos=None, order=None, offsets=None, stream=None):
@@ -170,46 +180,53 @@ def expert_dispatch(ids, num_experts, x=None, xs=None, pos=None, order=None, off
     ``offsets[num_experts]`` on are left as they are; None without ``x``),
     ``pos`` int32 [T, k] (-1: dropped), ``order`` int32 [T*k], ``offsets``
     int32 [num_experts + 1].  See ``skinny_expert_dispatch``."""
-    import torch
-    ldid = _rows(ids, "ids", torch.int32)
-    T, k = ids.shape
-    with _On(stream, ids.device) as s:
-        if pos is None:
-            pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-        if order is None:
-            order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-        if offsets is None:
-            offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
-        _flat(pos, "pos", T * k, torch.int32)
-        _flat(order, "order", T * k, torch.int32)
-        _flat(offsets, "offsets", num_experts + 1, torch.int32)
-        if x is None:
-            st = skinny_expert_dispatch(ids.data_ptr(), ldid, 0, 0, T, k, num_experts, 0, 0, pos.data_ptr(),
-                                        order.data_ptr(), offsets.data_ptr(), 0, 0, s)
-        else:
-            ldx, dt = _rows(x, "x"), _dtype(x, "x")
-            H = x.shape[1]
-            if x.shape[0] != T:
-                raise ValueError(f"x has {x.shape[0]} rows, ids {T}")
-            if xs is None:
-                xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-            ldxs = _rows(xs, "xs", x.dtype)
-            if tuple(xs.shape) != (T * k, H):
-                raise ValueError(f"xs must be {(T * k, H)}, not {tuple(xs.shape)}")
-            st = skinny_expert_dispatch(ids.data_ptr(), ldid, x.data_ptr(), ldx, T, k, num_experts, H, dt,
-                                        pos.data_ptr(), order.data_ptr(), offsets.data_ptr(), xs.data_ptr(), ldxs, s)
-    if st != _sk.SKINNY_OK:
-        raise _sk.SkinnyError(st, "skinny_expert_dispatch")
+    if stream is not None:
+        with _on(stream, ids.device):
+            return expert_dispatch(ids, num_experts, x, xs, pos, order, offsets)
+    T, k, ldid = _rows(ids, "ids", torch.int32)
+    n, dev = T * k, ids.device
+    if pos is None:
+        pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if order is None:
+        order = torch.empty(n, dtype=torch.int32, device=dev)
+    if offsets is None:
+        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    pp, op = _flat(pos, "pos", n, torch.int32), _flat(order, "order", n, torch.int32)
+    fp = _flat(offsets, "offsets", num_experts + 1, torch.int32)
+    if x is None:
+        xp = sp = ldx = ldxs = H = dt = 0
+    else:
+        xrows, H, ldx = _rows(x, "x")
+        dt = _dtype(x, "x")
+        if xrows != T:
+            raise ValueError(f"x has {xrows} rows, ids {T}")
+        if xs is None:
+            xs = torch.empty((n, H), dtype=x.dtype, device=dev)
+        srows, scols, ldxs = _rows(xs, "xs", x.dtype)
+        if srows != n or scols != H:
+            raise ValueError(f"xs must be {(n, H)}, not {tuple(xs.shape)}")
+        xp, sp = x.data_ptr(), xs.data_ptr()
+    st = _lib().skinny_expert_dispatch(ids.data_ptr(), ldid, xp, ldx, T, k, num_experts, H, dt, pp, op, fp, sp, ldxs,
+                                       _current(dev))
+    if st:
+        _refused(st, "skinny_expert_dispatch")
     return xs, pos, order, offsets
 
 
 def _weights(weights, T, k):
-    import torch
     if weights is None:
         return 0, 0
-    if tuple(weights.shape) != (T, k):
-        raise ValueError(f"weights must be {(T, k)}, not {tuple(weights.shape)}")
-    return weights.data_ptr(), _rows(weights, "weights", torch.float32)
+    m, n, ld = _rows(weights, "weights", torch.float32)
+    if m != T or n != k:
+        raise ValueError(f"weights must be {(T, k)}, not {(m, n)}")
+    return weights.data_ptr(), ld
+
+
+def _pos(pos):
+    if pos.dim() != 2:
+        raise ValueError(f"pos must be [T, k], not {tuple(pos.shape)}")
+    T, k = pos.shape
+    return T, k, _flat(pos, "pos", T * k, torch.int32)
 
 
 def expert_combine(ys, pos, weights=None, out=None, stream=None):
@@ -218,24 +235,22 @@ def expert_combine(ys, pos, weights=None, out=None, stream=None):
     H], ``pos`` int32 [T, k] from :func:`expert_dispatch`, ``weights`` fp32
     [T, k] or None (ones: the gradient of dispatch's copies), ``out`` bf16 or
     fp32 [T, H] (default: as ``ys``).  See ``skinny_expert_combine``."""
-    import torch
-    ldys, it = _rows(ys, "ys"), _dtype(ys, "ys")
-    rows, H = ys.shape
-    if pos.dim() != 2:
-        raise ValueError(f"pos must be [T, k], not {tuple(pos.shape)}")
-    T, k = pos.shape
-    _flat(pos, "pos", T * k, torch.int32)
+    if stream is not None:
+        with _on(stream, ys.device):
+            return expert_combine(ys, pos, weights, out)
+    rows, H, ldys = _rows(ys, "ys")
+    it = _dtype(ys, "ys")
+    T, k, pp = _pos(pos)
     wp, ldw = _weights(weights, T, k)
-    with _On(stream, ys.device) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
-        ldy, ot = _rows(out, "out"), _dtype(out, "out")
-        if tuple(out.shape) != (T, H):
-            raise ValueError(f"out must be {(T, H)}, not {tuple(out.shape)}")
-        st = skinny_expert_combine(ys.data_ptr(), ldys, rows, pos.data_ptr(), wp, ldw, T, k, H, it, ot,
-                                   out.data_ptr(), ldy, s)
-    if st != _sk.SKINNY_OK:
-        raise _sk.SkinnyError(st, "skinny_expert_combine")
+    if out is None:
+        out = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+    orows, ocols, ldy = _rows(out, "out")
+    if orows != T or ocols != H:
+        raise ValueError(f"out must be {(T, H)}, not {(orows, ocols)}")
+    st = _lib().skinny_expert_combine(ys.data_ptr(), ldys, rows, pp, wp, ldw, T, k, H, it, _dtype(out, "out"),
+                                      out.data_ptr(), ldy, _current(ys.device))
+    if st:
+        _refused(st, "skinny_expert_combine")
     return out
 
 
@@ -245,42 +260,44 @@ def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stre
     type of ``dy``; rows no entry names are left as they are) and
     ``dweights[t, j] = <dy[t], ys[pos[t, j]]>`` (fp32; 0 for a dropped entry).
     See ``skinny_expert_combine_grad``."""
-    import torch
-    lddy, dt = _rows(dy, "dy"), _dtype(dy, "dy")
-    ldys = _rows(ys, "ys", dy.dtype)
-    T, H = dy.shape
-    rows = ys.shape[0]
-    if pos.dim() != 2 or pos.shape[0] != T or ys.shape[1] != H:
+    if stream is not None:
+        with _on(stream, dy.device):
+            return expert_combine_grad(dy, ys, pos, weights, dys, dweights)
+    T, H, lddy = _rows(dy, "dy")
+    dt = _dtype(dy, "dy")
+    rows, ycols, ldys = _rows(ys, "ys", dy.dtype)
+    prows, k, pp = _pos(pos)
+    if prows != T or ycols != H:
         raise ValueError(f"shape mismatch: dy {tuple(dy.shape)}, ys {tuple(ys.shape)}, pos {tuple(pos.shape)}")
-    k = pos.shape[1]
-    _flat(pos, "pos", T * k, torch.int32)
     wp, ldw = _weights(weights, T, k)
-    with _On(stream, dy.device) as s:
-        if dys is None:
-            dys = torch.empty((rows, H), dtype=dy.dtype, device=dy.device)
-        if dweights is None:
-            dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-        lddys, lddw = _rows(dys, "dys", dy.dtype), _rows(dweights, "dweights", torch.float32)
-        if tuple(dys.shape) != (rows, H) or tuple(dweights.shape) != (T, k):
-            raise ValueError(f"dys must be {(rows, H)} and dweights {(T, k)}")
-        st = skinny_expert_combine_grad(dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, pos.data_ptr(), wp, ldw, T, k,
-                                        H, dt, dys.data_ptr(), lddys, dweights.data_ptr(), lddw, s)
-    if st != _sk.SKINNY_OK:
-        raise _sk.SkinnyError(st, "skinny_expert_combine_grad")
+    if dys is None:
+        dys = torch.empty((rows, H), dtype=dy.dtype, device=dy.device)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    grows, gcols, lddys = _rows(dys, "dys", dy.dtype)
+    wrows, wcols, lddw = _rows(dweights, "dweights", torch.float32)
+    if grows != rows or gcols != H or wrows != T or wcols != k:
+        raise ValueError(f"dys must be {(rows, H)} and dweights {(T, k)}")
+    st = _lib().skinny_expert_combine_grad(dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, pp, wp, ldw, T, k, H, dt,
+                                           dys.data_ptr(), lddys, dweights.data_ptr(), lddw, _current(dy.device))
+    if st:
+        _refused(st, "skinny_expert_combine_grad")
     return dys, dweights
 
 
 def _stack(t, name, rows, cols):
     """(row stride, matrix stride) of a CUDA bf16 stack of matrices [n, rows, cols]."""
-    import torch
-    if t.dim() != 3 or not t.is_cuda or t.dtype != torch.bfloat16:
+    if t.dim() != 3 or not t.is_cuda or t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor of three dimensions")
-    if t.shape[1] != rows or t.shape[2] != cols:
-        raise ValueError(f"{name} must hold {rows} x {cols} matrices, not {tuple(t.shape[1:])}")
-    if cols > 1 and t.stride(2) != 1:
+    n, r, c = t.shape
+    if r != rows or c != cols:
+        raise ValueError(f"{name} must hold {rows} x {cols} matrices, not {r} x {c}")
+    lde, ld, one = t.stride()
+    if c > 1 and one != 1:
         raise ValueError(f"{name} needs unit stride along its last dimension")
-    ld = t.stride(1) if rows > 1 else max(cols, 1)
-    return ld, t.stride(0) if t.shape[0] > 1 else max(rows, 1) * ld
+    if r <= 1:
+        ld = c or 1
+    return ld, lde if n > 1 else (r or 1) * ld
 
 
 def experts_gemm(xs, offsets, w, out=None, activation=None, stream=None):
@@ -291,34 +308,33 @@ def experts_gemm(xs, offsets, w, out=None, activation=None, stream=None):
     times the up product.  ``out`` bf16 or fp32 [rows, N] (default bf16); rows
     from ``offsets[E]`` on are left as they are.  See
     ``skinny_experts_gemm_bf16``."""
-    import torch
-    ldx = _rows(xs, "xs", torch.bfloat16)
-    rows, K = xs.shape
-    if activation not in _ACTS:
+    if stream is not None:
+        with _on(stream, xs.device):
+            return experts_gemm(xs, offsets, w, out, activation)
+    rows, K, ldx = _rows(xs, "xs", torch.bfloat16)
+    act = _ACTS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be 'swiglu' or None, not {activation!r}")
-    act = _ACTS[activation]
     E, wrows = w.shape[0], w.shape[1]
     if act and wrows % 2:
         raise ValueError(f"swiglu needs gate and up rows, not {wrows} rows")
     N = wrows // 2 if act else wrows
     ldw, ldwe = _stack(w, "w", wrows, K)
-    _flat(offsets, "offsets", E + 1, torch.int32)
-    with _On(stream, xs.device) as s:
-        if out is None:
-            out = torch.empty((rows, N), dtype=torch.bfloat16, device=xs.device)
-        ldy, ot = _rows(out, "out"), _dtype(out, "out")
-        if tuple(out.shape) != (rows, N):
-            raise ValueError(f"out must be {(rows, N)}, not {tuple(out.shape)}")
-        st = skinny_experts_gemm_bf16(xs.data_ptr(), ldx, rows, offsets.data_ptr(), w.data_ptr(), ldw, ldwe, E, N, K,
-                                      act, ot, out.data_ptr(), ldy, s)
-    if st != _sk.SKINNY_OK:
-        raise _sk.SkinnyError(st, "skinny_experts_gemm_bf16")
+    fp = _flat(offsets, "offsets", E + 1, torch.int32)
+    if out is None:
+        out = torch.empty((rows, N), dtype=torch.bfloat16, device=xs.device)
+    orows, ocols, ldy = _rows(out, "out")
+    if orows != rows or ocols != N:
+        raise ValueError(f"out must be {(rows, N)}, not {(orows, ocols)}")
+    st = _lib().skinny_experts_gemm_bf16(xs.data_ptr(), ldx, rows, fp, w.data_ptr(), ldw, ldwe, E, N, K, act,
+                                         _dtype(out, "out"), out.data_ptr(), ldy, _current(xs.device))
+    if st:
+        _refused(st, "skinny_experts_gemm_bf16")
     return out
 
 
 def lora_workspace(M, N, R, out_dtype):
     """Bytes of workspace of :func:`lora_gemm` for an ``out`` of ``out_dtype``."""
-    import torch
     return skinny_lora_workspace(M, N, R, SKINNY_BF16 if out_dtype == torch.bfloat16 else SKINNY_F32)
 
 
@@ -329,31 +345,32 @@ def lora_gemm(x, w, a, b, adapters, ranks=None, scales=None, out=None, workspace
     [L, R, K], ``b`` bf16 [L, N, R], ``ranks`` int32 [L] (what lies past an
     adapter's rank is not used), ``scales`` fp32 [L], ``out`` fp32 (default)
     or bf16 [M, N].  See ``skinny_lora_gemm_bf16``."""
-    import torch
-    ldx, ldw = _rows(x, "x", torch.bfloat16), _rows(w, "w", torch.bfloat16)
-    M, K = x.shape
-    N = w.shape[0]
+    if stream is not None:
+        with _on(stream, x.device):
+            return lora_gemm(x, w, a, b, adapters, ranks, scales, out, workspace)
+    M, K, ldx = _rows(x, "x", torch.bfloat16)
+    N, wcols, ldw = _rows(w, "w", torch.bfloat16)
     L, R = a.shape[0], a.shape[1]
-    if w.shape[1] != K or b.shape[0] != L:
+    if wcols != K or b.shape[0] != L:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, a {tuple(a.shape)}, b {tuple(b.shape)}")
     lda, ldae = _stack(a, "a", R, K)
     ldb, ldbe = _stack(b, "b", N, R)
-    _flat(adapters, "adapters", M, torch.int32)
-    rp = 0 if ranks is None else _flat(ranks, "ranks", L, torch.int32).data_ptr()
-    sp = 0 if scales is None else _flat(scales, "scales", L, torch.float32).data_ptr()
-    with _On(stream, x.device) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.float32, device=x.device)
-        ldy, ot = _rows(out, "out"), _dtype(out, "out")
-        if tuple(out.shape) != (M, N):
-            raise ValueError(f"out must be {(M, N)}, not {tuple(out.shape)}")
-        if workspace is None:
-            workspace = torch.empty(skinny_lora_workspace(M, N, R, ot), dtype=torch.uint8, device=x.device)
-        elif not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        st = skinny_lora_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), ldw, a.data_ptr(), lda, ldae, b.data_ptr(), ldb,
-                                   ldbe, adapters.data_ptr(), rp, sp, L, R, out.data_ptr(), ldy, M, N, K, ot,
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
-    if st != _sk.SKINNY_OK:
-        raise _sk.SkinnyError(st, "skinny_lora_gemm_bf16")
+    ip = _flat(adapters, "adapters", M, torch.int32)
+    rp = 0 if ranks is None else _flat(ranks, "ranks", L, torch.int32)
+    sp = 0 if scales is None else _flat(scales, "scales", L, torch.float32)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    orows, ocols, ldy = _rows(out, "out")
+    ot = _dtype(out, "out")
+    if orows != M or ocols != N:
+        raise ValueError(f"out must be {(M, N)}, not {(orows, ocols)}")
+    if workspace is None:
+        workspace = torch.empty(skinny_lora_workspace(M, N, R, ot), dtype=torch.uint8, device=x.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    st = _lib().skinny_lora_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), ldw, a.data_ptr(), lda, ldae, b.data_ptr(), ldb,
+                                      ldbe, ip, rp, sp, L, R, out.data_ptr(), ldy, M, N, K, ot, workspace.data_ptr(),
+                                      workspace.nbytes, _current(x.device))
+    if st:
+        _refused(st, "skinny_lora_gemm_bf16")
     return out

@@ -20,6 +20,18 @@ def _init():
     assert sk.skinny_get_device_status() == 0
 
 
+@pytest.fixture(params=["auto", "tcgen05", "mma"])
+def kernel(request):
+    """Each kernel by force, where it takes the case, and the library's own choice."""
+    force = {"auto": sk.SKINNY_BACKEND_AUTO, "tcgen05": sk.SKINNY_BACKEND_TCGEN05, "mma": sk.SKINNY_BACKEND_DOTPROD}
+    with sk.options(backend=force[request.param]):
+        yield request.param
+
+
+def aligned(K, pad=0, offset=0):
+    return K > 0 and (K + pad) % 8 == 0 and offset % 8 == 0
+
+
 def stack(shape, ld, seed, scale=1.0, offset=0, same_sign=False):
     """A random bf16 CUDA stack [n, rows, cols] with row stride ld, its first element `offset` past an aligned one."""
     g = torch.Generator().manual_seed(seed)
@@ -65,36 +77,42 @@ RAGGED = [0, 1, 16, 17, 0, 33, 64, 65, 2, 0]
 @pytest.mark.parametrize("act", [None, "swiglu"])
 @pytest.mark.parametrize("N,K", [(1, 1), (7, 64), (8, 65), (100, 1000), (130, 1001), (64, 258), (300, 100), (129, 2880),
                                  (16, 7168), (1000, 72)])
-def test_ragged(N, K, act, out):
+def test_ragged(N, K, act, out, kernel):
+    if kernel == "tcgen05" and not aligned(K):
+        pytest.skip("rows not 16-byte aligned")
     run(RAGGED, N, K, act, out, seed=N + K)
 
 
 @pytest.mark.parametrize("act", [None, "swiglu"])
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (4, 4), (2, 0), (1, 0), (0, 1), (3, 5)])
-def test_strides_and_alignment(pad, offset, act):
+def test_strides_and_alignment(pad, offset, act, kernel):
+    if kernel == "tcgen05" and not aligned(136, pad, offset):
+        with pytest.raises(sk.SkinnyError):
+            run([3, 0, 20, 1], 72, 136, act, "bf16", pad=pad, offset=offset, ypad=5)
+        return
     run([3, 0, 20, 1], 72, 136, act, "bf16", pad=pad, offset=offset, ypad=5)
 
 
 @pytest.mark.parametrize("counts", [[0, 0, 0], [1], [0, 0, 1], [130, 0, 300], [8] * 300, [1] * 64 + [0] * 960,
                                     [0] * 1023 + [5], [64, 64], [200]])
 @pytest.mark.parametrize("act", [None, "swiglu"])
-def test_distributions(counts, act):
+def test_distributions(counts, act, kernel):
     run(counts, 40, 192, act, "fp32")
 
 
 @pytest.mark.parametrize("N,K", [(4096, 512), (2112, 1536), (24, 8192), (5000, 128)])
 @pytest.mark.parametrize("act", [None, "swiglu"])
-def test_larger(N, K, act):
+def test_larger(N, K, act, kernel):
     run([2, 0, 9, 1, 0, 40, 3], N, K, act, "bf16", seed=N)
 
 
 @pytest.mark.parametrize("K", [2880, 7168, 14336])
-def test_same_sign_operands(K):
+def test_same_sign_operands(K, kernel):
     """Every product positive: rounding errors do not cancel."""
     run([1, 17, 0, 40], 136, K, None, "fp32", same_sign=True)
 
 
-def test_not_finite_stays_in_its_row():
+def test_not_finite_stays_in_its_row(kernel):
     xs, off, w, _ = run([5, 11, 3], 48, 128, None, "fp32")
     xs[2, 7], xs[9, 100], w[2, 5, 3] = float("nan"), float("inf"), float("nan")
     y = torch.zeros((xs.shape[0], 48), device="cuda")
@@ -106,7 +124,7 @@ def test_not_finite_stays_in_its_row():
     assert np.isfinite(y[rest]).all() and np.isfinite(np.delete(y[16:19], 5, axis=1)).all()
 
 
-def test_swiglu_far_gates():
+def test_swiglu_far_gates(kernel):
     """Gates far from zero: SiLU tends to 0 on the left, to its argument on the right."""
     w = torch.zeros((1, 4, 8), dtype=torch.bfloat16, device="cuda")
     w[0, 0, 0], w[0, 1, 0], w[0, 2, 1], w[0, 3, 1] = -1.0, 1.0, 1.0, 1.0
@@ -120,7 +138,7 @@ def test_swiglu_far_gates():
     assert (np.abs(y[:, 1] - 2 * x0) <= 1e-6 * x0).all()
 
 
-def test_offsets_are_clamped_to_the_rows():
+def test_offsets_are_clamped_to_the_rows(kernel):
     """Offsets past the rows, negative or falling are cut: nothing outside the rows is read or written."""
     xs, w = stack((1, 6, 64), 64, 1)[0], stack((4, 32, 64), 64, 2)
     y = torch.full((8, 32), -7.0, device="cuda")
@@ -145,8 +163,10 @@ def test_empty_calls_and_k_zero():
 
 
 @pytest.mark.parametrize("K", [256, 255])
-def test_graph_streams_and_repeats(K):
+def test_graph_streams_and_repeats(K, kernel):
     """Bits repeat from run to run, under PDL, in a graph whose inputs change, and on a given stream."""
+    if kernel == "tcgen05" and not aligned(K):
+        pytest.skip("rows not 16-byte aligned")
     counts = [[3, 0, 20, 1], [0, 9, 0, 15]]
     xs, w = stack((1, 24, K), K, 1)[0], stack((4, 96, K), K, 2, 0.1)
     off = [torch.tensor([0] + list(np.cumsum(c)), dtype=torch.int32, device="cuda") for c in counts]
@@ -171,7 +191,7 @@ def test_graph_streams_and_repeats(K):
             del g
 
 
-def test_weights_past_32_bits():
+def test_weights_past_32_bits(kernel):
     """Experts whose byte offsets pass 2^32."""
     E, N, K = 40, 8192, 8192                 # 5.4 GB
     w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
@@ -190,14 +210,15 @@ def test_weights_past_32_bits():
 @pytest.mark.parametrize("act", [None, "swiglu"])
 def test_bounded_waits_report_and_recover(act):
     """A wait without any budget gives up at once, the status says so, and the next call is right."""
-    xs, off, w, _ = run([3, 0, 20, 1], 200, 640, act, "fp32")
-    offsets = torch.from_numpy(off).cuda()
-    want = sk.experts_gemm(xs, offsets, w, activation=act)
-    with sk.options(wait_timeout_us=0):
-        sk.experts_gemm(xs, offsets, w, activation=act)
-        torch.cuda.synchronize()
-    assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
-    n = int(off[-1])
-    for _ in range(3):
-        assert torch.equal(sk.experts_gemm(xs, offsets, w, activation=act)[:n], want[:n])
-    assert sk.skinny_get_device_status() == 0
+    with sk.options(backend=sk.SKINNY_BACKEND_TCGEN05):
+        xs, off, w, _ = run([3, 0, 20, 1], 200, 640, act, "fp32")
+        offsets = torch.from_numpy(off).cuda()
+        want = sk.experts_gemm(xs, offsets, w, activation=act)
+        with sk.options(wait_timeout_us=0):
+            sk.experts_gemm(xs, offsets, w, activation=act)
+            torch.cuda.synchronize()
+        assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
+        n = int(off[-1])
+        for _ in range(3):
+            assert torch.equal(sk.experts_gemm(xs, offsets, w, activation=act)[:n], want[:n])
+        assert sk.skinny_get_device_status() == 0

@@ -104,7 +104,7 @@ def lora(X=A, ldx=64, W=B, ldw=64, Aw=C, lda=64, ldae=8 * 64, Bw=D, ldb=8, ldbe=
     (dict(L=-1), INVALID), (dict(R=-1), INVALID), (dict(ot=2), INVALID), (dict(M=-1), INVALID),
     (dict(R=257, ldb=257), UNSUPPORTED), (dict(M=65), UNSUPPORTED),
     (dict(X=0), INVALID), (dict(W=0), INVALID), (dict(Aw=0), INVALID), (dict(Bw=0), INVALID), (dict(ids=0), INVALID),
-    (dict(Y=0), INVALID), (dict(ws=0), INVALID), (dict(ot=1, wsb=5 * 8 * 4 - 1), INVALID), (dict(ot=0, wsb=5 * 8 * 4), INVALID),
+    (dict(Y=0), INVALID), (dict(ws=0), INVALID), (dict(ot=1, wsb=5 * 32 * 6 - 1), INVALID), (dict(ot=0, wsb=5 * 32 * 6), INVALID),
     (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(lda=63), INVALID), (dict(ldb=7), INVALID),
     (dict(ldae=511), INVALID), (dict(ldbe=383), INVALID), (dict(ldy=47), INVALID),
     (dict(X=A + 1), MISALIGNED), (dict(Aw=C + 1), MISALIGNED), (dict(Bw=D + 1), MISALIGNED), (dict(ids=F + 2), MISALIGNED),
@@ -119,7 +119,8 @@ def test_lora_refusals(kw, expect):
 
 
 def test_lora_workspace():
-    assert sk.skinny_lora_workspace(5, 48, 8, sk.SKINNY_F32) == 160
-    assert sk.skinny_lora_workspace(5, 48, 3, sk.SKINNY_BF16) == 64 + 5 * 48 * 4
+    # six bytes for each of the columns of V, in whole steps of 32; bf16: the fp32 projection too
+    assert sk.skinny_lora_workspace(5, 48, 8, sk.SKINNY_F32) == 5 * 32 * 6
+    assert sk.skinny_lora_workspace(5, 48, 33, sk.SKINNY_BF16) == 5 * 64 * 6 + 5 * 48 * 4
     for bad in ((65, 48, 8, 0), (5, -1, 8, 0), (5, 48, 257, 0), (5, 48, 8, 2), (-1, 48, 8, 0)):
         assert sk.skinny_lora_workspace(*bad) == 0
