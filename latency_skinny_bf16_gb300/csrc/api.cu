@@ -639,7 +639,7 @@ skinny_status_t check_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ld
 
 // One call: checks, plan, launch.  out_bf16 selects a bf16 Y (2-byte elements).
 skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, void *Y, int ldy,
-                         int M, int N, int K, void *stream, int out_bf16) {
+                         int M, int N, int K, void *stream, int out_bf16, bool allow_pdl) {
     bool noop = false;
     skinny_status_t st = validate(X, ldx, W, ldw, Y, ldy, M, N, K, &noop, out_bf16 ? 2 : 4);
     if (st != SKINNY_OK || noop) return st;
@@ -658,6 +658,7 @@ skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw,
     skinny_plan_t plan;
     st = make_plan(X, ldx, W, ldw, M, N, K, d.num_sms, &plan);
     if (st != SKINNY_OK) return st;
+    if (!allow_pdl) plan.pdl = 0;
     if (opt_log()) log_plan(M, N, K, ldw, plan);
     GemmArgs a{X, ldx, W, ldw, Y, ldy, M, N, K, out_bf16};
     LaunchCtx c{s, plan.pdl != 0, late_trigger(2.0 * N * K), d.status_word, (uint64_t)g_opt_wait_us.load() * 1000ull};

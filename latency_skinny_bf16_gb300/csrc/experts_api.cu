@@ -218,14 +218,17 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
     const LoraArgs a{X, ldx, A, lda, ldae, B, ldb, ldbe, adapters, ranks, scales, L, R, M, N, K, V, base, ldbase, Y,
                      ldy, ob};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_lora_shrink(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+    // the projection, the shrink beside it, the expand behind both (lora.cu says what may overlap)
     if (rows16) {
-        st = run_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, stream, 0);
+        st = run_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, stream, 0, false);
         if (st != SKINNY_OK) return st;
     } else {
+        CallCtx plain = c;
+        plain.pdl = false;
         const ExpertsArgs b{X, ldx, M, nullptr, W, ldw, (int64_t)N * ldw, 1, N, K, 0, 0, base, ldbase};
-        if (launch_experts_mma(b, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        if (launch_experts_mma(b, plain, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     }
+    if (launch_lora_shrink(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     return launched(launch_lora_expand(a, c, s));
 }
 

@@ -51,18 +51,22 @@ struct LoraArgs {
 cudaError_t launch_lora_shrink(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
 cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t stream);
 
+// cluster_z: CTAs of a cluster along the grid's z
 inline cudaError_t launch_plain(const void *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl,
-                                void **args) {
+                                void **args, int cluster_z = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = cluster_z;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster_z > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

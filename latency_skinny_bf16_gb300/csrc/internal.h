@@ -160,8 +160,9 @@ bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1);
 // skinny_gemm_bf16 / skinny_gemm_bf16_bf16out, and their checks without the launch
 skinny_status_t check_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const void *Y, int ldy, int M,
                            int N, int K, int out_bf16);
+// (allow_pdl false: the launch waits for what precedes it whatever the option says)
 skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, void *Y, int ldy, int M, int N,
-                         int K, void *stream, int out_bf16);
+                         int K, void *stream, int out_bf16, bool allow_pdl = true);
 
 // Allow `fn` the device's opt-in shared memory per block, less its static part.
 template <typename F>

@@ -1,18 +1,21 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection:
 //     V[m,r]  = s_a sum_k X[m,k] A[a][r][k]                 a = adapters[m], r < r_a
 //     Y[m,n]  = base[m,n] + sum_{r < r_a} V[m,r] B[a][n][r]  base = X W^T (skinny_gemm_bf16)
-// Three launches: the first (shrink) writes V, the second is the projection,
-// the third (expand) adds.  V keeps the 24 bits of fp32 as three bf16 terms,
-// h = bf16(v), m = bf16(v - h), l = bf16(v - h - m): operands of the third
-// kernel's MMAs as they stand, with zeros from an adapter's rank on.  Both adapter kernels are bound by the
-// bytes of A and B, read once per adapter that occurs and eight (shrink: 32)
-// of its tokens; they take them straight from device memory into mma.sync
-// operands, 16 rows at a time, at any alignment (mma_rows.cuh).
+// Three launches: the projection, the first product (shrink: V), the second
+// (expand: added to the projection).  V keeps the 24 bits of fp32 as three bf16
+// terms, h = bf16(v), m = bf16(v - h), l = bf16(v - h - m): operands of the
+// expand kernel's MMAs as they stand, with zeros from an adapter's rank on.
+// Both adapter kernels are bound by the bytes of A and B, read once per adapter
+// that occurs and eight (shrink: 16) of its tokens; they take them straight from
+// device memory into mma.sync operands, 16 rows at a time, at any alignment
+// (mma_rows.cuh).
 //
-// With programmatic dependent launch the shrink kernel lets the projection
-// start only after its own wait: what was launched before this call is then
-// complete for all three kernels, so the expand kernel may read the adapters'
-// ids and ranks before it waits for the projection.
+// With programmatic dependent launch the shrink kernel runs beside the
+// projection.  The projection itself is launched without it, so all that
+// precedes this call is complete when the shrink kernel starts: it may read X
+// and write V at once, and waits for the projection only at its end.  The
+// expand kernel, which waits for the shrink kernel, then follows both; before
+// that it may read the adapters' ids, ranks and B.
 #include "experts_gemm.h"
 #include "mma_rows.cuh"
 
@@ -30,11 +33,14 @@ __device__ __forceinline__ int adapter_id(const int32_t *adapters, int m, int L)
 }
 
 // ------------------------------------------------------------------ shrink
-// Grid (RP / 16, M): the CTAs of the first token of an adapter serve every
-// token that shares it, those of the others leave.  Sixteen rows of A per CTA;
-// its warps split K in pieces of 64 and their sums are added in order.
+// Grid (RP / 16, M, S): the CTAs of the first token of an adapter serve every
+// token that shares it, those of the others leave.  Sixteen rows of A per
+// cluster of S CTAs, whose warps split K in pieces of 64; a CTA adds its warps'
+// sums in order, the first CTA of the cluster the CTAs' (distributed shared
+// memory): one CTA alone reads its rows at the rate of one SM.
 constexpr int kShrinkWarps = 16;
-constexpr int kShrinkTT = 4;           // tokens per pass: 8 * 4
+constexpr int kShrinkTT = 2;           // tokens per pass: 8 * 2
+constexpr int kShrinkMaxCluster = 8;
 
 struct ShrinkParams {
     const uint16_t *X;
@@ -45,6 +51,7 @@ struct ShrinkParams {
     const float *scales;
     int L, R, M, K;
     uint16_t *V;         // [M][3][RP], RP = lora_padded_rank(R)
+    int S;               // CTAs of a cluster along K
     Extent xe, ae;
 };
 
@@ -58,14 +65,13 @@ __device__ __forceinline__ void split3(float v, uint16_t &h, uint16_t &m, uint16
 }
 
 template <bool ALIGNED>
-__global__ void __launch_bounds__(32 * kShrinkWarps)
-lora_shrink_kernel(const ShrinkParams p)
+__device__ __forceinline__ void lora_shrink(const ShrinkParams &p)
 {
     __shared__ int s_id[kMaxM], list[kMaxM];
     __shared__ int s_count;
     __shared__ __align__(16) float part[kShrinkWarps][kShrinkTT][32][4];
-    griddep_wait();
-    griddep_launch_dependents();
+    __shared__ float sums[kShrinkMaxCluster][kShrinkTT * 128];      // of the cluster's CTAs, in the first one
+    const int S = p.S, rank_k = S > 1 ? (int)cluster_ctarank() : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int m = blockIdx.y, M = p.M, R = p.R, K = p.K;
@@ -93,13 +99,15 @@ lora_shrink_kernel(const ShrinkParams p)
     if (count == 0) return;
     const int RP = lora_padded_rank(R);
     if (r0 >= rank) {                  // rows past the rank: zeros
-        for (int o = tid; o < count * 48; o += 32 * kShrinkWarps)
+        for (int o = rank_k * 32 * kShrinkWarps + tid; o < count * 48; o += S * 32 * kShrinkWarps)
             p.V[((int64_t)list[o / 48] * 3 + o % 48 / 16) * RP + r0 + o % 16] = 0;
         return;
     }
+    if (S > 1) cluster_arrive_relaxed();               // this CTA runs: its shared memory may be written
     // rows past the rank repeat its last one; their sums are not stored
     const uint16_t *Aa = p.A + (int64_t)a * p.ldae;
     const uint16_t *al = Aa + (int64_t)min(r0 + g, rank - 1) * p.lda, *ah = Aa + (int64_t)min(r0 + 8 + g, rank - 1) * p.lda;
+    const int k0 = 64 * (rank_k * kShrinkWarps + warp), kstep = 64 * kShrinkWarps * S;
     for (int t0 = 0; t0 < count; t0 += 8 * kShrinkTT) {
         const int nt = min(kShrinkTT, (count - t0 + 7) / 8);
         const uint16_t *x[kShrinkTT];
@@ -133,27 +141,56 @@ lora_shrink_kernel(const ShrinkParams p)
         };
         if (nt == 1) {                 // the usual case: more steps of K in flight
 #pragma unroll 4
-            for (int k = 64 * warp; k < K; k += 64 * kShrinkWarps) step(k, 1);
+            for (int k = k0; k < K; k += kstep) step(k, 1);
         } else {
-            for (int k = 64 * warp; k < K; k += 64 * kShrinkWarps) step(k, nt);
+            for (int k = k0; k < K; k += kstep) step(k, nt);
         }
 #pragma unroll
         for (int q = 0; q < kShrinkTT; ++q)
             if (q < nt) *reinterpret_cast<float4 *>(part[warp][q][lane]) = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
         __syncthreads();
+        if (S > 1 && t0 == 0) cluster_wait();
+        const uint32_t slot = smem_u32(&sums[rank_k][0]);
+        const uint32_t first = S > 1 ? mapa_shared(slot, 0) : slot;
         for (int o = tid; o < nt * 128; o += 32 * kShrinkWarps) {
             const int q = o >> 7, sl = (o >> 2) & 31, j = o & 3;
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < kShrinkWarps; ++w) s += part[w][q][sl][j];
-            const int i = t0 + 8 * q + 2 * (sl & 3) + (j & 1), r = r0 + (sl >> 2) + 8 * (j >> 1);
-            if (i < count) {
-                uint16_t *v = p.V + (int64_t)list[i] * 3 * RP + r;
-                split3(r < rank ? s * scale : 0.f, v[0], v[RP], v[2 * RP]);
+            st_shared_cluster_f32(first + 4 * o, s);
+        }
+        auto meet = [&] {
+            if (S > 1) {
+                cluster_arrive_release();
+                cluster_wait_acquire();
+            } else {
+                __syncthreads();
+            }
+        };
+        meet();
+        if (rank_k == 0) {
+            for (int o = tid; o < nt * 128; o += 32 * kShrinkWarps) {
+                const int q = o >> 7, sl = (o >> 2) & 31, j = o & 3;
+                float s = sums[0][o];
+                for (int w = 1; w < S; ++w) s += sums[w][o];
+                const int i = t0 + 8 * q + 2 * (sl & 3) + (j & 1), r = r0 + (sl >> 2) + 8 * (j >> 1);
+                if (i < count) {
+                    uint16_t *v = p.V + (int64_t)list[i] * 3 * RP + r;
+                    split3(r < rank ? s * scale : 0.f, v[0], v[RP], v[2 * RP]);
+                }
             }
         }
-        __syncthreads();
+        meet();                        // the sums are read before the next tokens', and before a CTA leaves
     }
+}
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(32 * kShrinkWarps)
+lora_shrink_kernel(const ShrinkParams p)
+{
+    griddep_launch_dependents();
+    lora_shrink<ALIGNED>(p);
+    griddep_wait();                    // the projection: what follows this kernel follows both
 }
 
 // ------------------------------------------------------------------ expand
@@ -165,6 +202,7 @@ lora_shrink_kernel(const ShrinkParams p)
 // tensor core before a rounded add.
 constexpr int kExpandWarps = 8;
 constexpr int kExpandTiles = 4;
+constexpr int kExpandCtas = 2;         // per SM
 
 struct ExpandParams {
     const uint16_t *B;
@@ -295,7 +333,7 @@ __device__ __forceinline__ void expand_piece(const ExpandParams &p, const uint16
 }
 
 template <bool ALIGNED>
-__global__ void __launch_bounds__(32 * kExpandWarps, 2)
+__global__ void __launch_bounds__(32 * kExpandWarps, kExpandCtas)
 lora_expand_kernel(const ExpandParams p)
 {
     __shared__ int s_id[kMaxM], s_lead[kMaxM], list[kMaxM];
@@ -343,6 +381,16 @@ lora_expand_kernel(const ExpandParams p)
     // rows per piece: 64, or 16 while that leaves warps without work
     const int tiles = (int64_t)groups * ((N + 16 * kExpandTiles - 1) / (16 * kExpandTiles)) < warps ? 1 : kExpandTiles;
     const int pieces = (N + 16 * tiles - 1) / (16 * tiles);
+    const int64_t first = (int64_t)blockIdx.x + (int64_t)gridDim.x * warp;
+    if (first < (int64_t)groups * pieces) {            // the first piece's rows, on their way to L2
+        const int gr = (int)(first / pieces), n0 = (int)(first - (int64_t)gr * pieces) * 16 * tiles;
+        const int bytes = 2 * g_rank[gr];
+        if (bytes > 0)
+            for (int i = lane; i < 16 * tiles && n0 + i < N; i += 32) {
+                const char *row = reinterpret_cast<const char *>(p.B + (int64_t)g_adapter[gr] * p.ldbe + (int64_t)(n0 + i) * p.ldb);
+                for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
+            }
+    }
     griddep_wait();
     for (int64_t u = (int64_t)blockIdx.x + (int64_t)gridDim.x * warp; u < (int64_t)groups * pieces; u += warps) {
         const int gr = (int)(u / pieces), n0 = (int)(u - (int64_t)gr * pieces) * 16 * tiles;
@@ -362,13 +410,18 @@ uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 }  // namespace
 
 cudaError_t launch_lora_shrink(const LoraArgs &a, const CallCtx &c, cudaStream_t stream) {
-    ShrinkParams p{a.X, a.ldx, a.A, a.lda, a.ldae, a.adapters, a.ranks, a.scales, a.L, a.R, a.M, a.K, a.V,
+    // CTAs along K: for long K and few tokens, 512 of K each at least (GB300, one token, 16 x 7168 beside the
+    // 2112 x 7168 projection: the whole call 14.6 us with one CTA, 10.2 with eight)
+    const int tiles = lora_padded_rank(a.R) / 16;
+    int S = 1;
+    while (S < kShrinkMaxCluster && 2 * S * tiles * a.M <= 2 * c.num_sms && a.K >= 2 * S * 512) S *= 2;
+    ShrinkParams p{a.X, a.ldx, a.A, a.lda, a.ldae, a.adapters, a.ranks, a.scales, a.L, a.R, a.M, a.K, a.V, S,
                    {addr(a.X), addr(a.X) + (uintptr_t)(2 * ((a.M - 1) * a.ldx + a.K))},
                    {addr(a.A), addr(a.A) + (uintptr_t)(2 * ((a.L - 1) * a.ldae + (a.R - 1) * a.lda + a.K))}};
     void *args[] = {&p};
     const bool al = (addr(a.X) | addr(a.A)) % 16 == 0 && (a.ldx | a.lda | a.ldae) % 8 == 0;
     return launch_plain(al ? (const void *)lora_shrink_kernel<true> : (const void *)lora_shrink_kernel<false>,
-                        dim3(lora_padded_rank(a.R) / 16, a.M), 32 * kShrinkWarps, 0, stream, c.pdl, args);
+                        dim3(tiles, a.M, S), 32 * kShrinkWarps, 0, stream, c.pdl, args, S);
 }
 
 cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t stream) {
@@ -378,7 +431,7 @@ cudaError_t launch_lora_expand(const LoraArgs &a, const CallCtx &c, cudaStream_t
     const bool al = addr(a.B) % 16 == 0 && (a.ldb | a.ldbe) % 8 == 0;
     // two CTAs per SM, or a warp for every 16 rows of every token's adapter when these are fewer
     const int64_t pieces = (int64_t)a.M * ((a.N + 15) / 16), want = (pieces + kExpandWarps - 1) / kExpandWarps;
-    const int most = 2 * c.num_sms;
+    const int most = kExpandCtas * c.num_sms;
     return launch_plain(al ? (const void *)lora_expand_kernel<true> : (const void *)lora_expand_kernel<false>,
                         dim3((unsigned)(want < most ? want : most)), 32 * kExpandWarps, 0, stream, c.pdl, args);
 }
