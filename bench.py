@@ -61,7 +61,7 @@ WORKLOAD_DESC = {
 # the sources that define each kernel family (a committed DRAM-traffic figure
 # is used only while they are unchanged)
 KERNEL_SOURCES = {"dotprod": ["dotprod.cu"], "dotmma": ["dotmma.cu"], "splitk": ["splitk.cu"],
-                  "stream": ["stream.cu"], "tmem_gemm": ["tmem_gemm.cu", "tma.cuh"]}
+                  "stream": ["stream.cu"], "tmem_gemm": ["tmem_gemm.cu", "tma.cuh", "tcgen05.cuh"]}
 COMMON_SOURCES = ["common.cuh", "internal.h"]
 
 

@@ -18,7 +18,7 @@
 #include <set>
 #include <tuple>
 
-#include "internal.h"
+#include "calls.h"
 #include "dotmma_f32w.h"
 #include "expert_rows.h"
 #include "experts_gemm.h"

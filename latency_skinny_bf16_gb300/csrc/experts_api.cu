@@ -3,6 +3,7 @@
 // launched; no entry point throws, allocates or synchronises.
 #include <initializer_list>
 
+#include "calls.h"
 #include "expert_rows.h"
 #include "experts_gemm.h"
 #include "skinny_experts.h"

@@ -2,7 +2,7 @@
 // adapters beside a projection.
 #pragma once
 
-#include "internal.h"
+#include "calls.h"
 #include "skinny_experts.h"
 
 namespace skinny {

@@ -35,7 +35,7 @@
 #include "common.cuh"
 #include "experts_gemm.h"
 #include "tcgen05.cuh"
-#include "tma.cuh"
+#include "tma_stack.cuh"
 
 namespace skinny {
 namespace {

@@ -147,23 +147,6 @@ cudaError_t launch_router_topk(const float *L, int64_t ldl, int M, int N, int k,
 // bytes opt-in per block, less a margin for the kernels' static shared memory).
 constexpr int kMaxDynSmem = 227 * 1024 - 1024;
 
-// ---- the library's state, for entry points outside api.cu
-struct CallCtx {
-    int num_sms;
-    int *status;         // device status word
-    uint64_t budget_ns;  // budget of each bounded wait
-    bool pdl;            // programmatic dependent launch (SKINNY_OPT_PDL)
-    int force_backend;   // SKINNY_OPT_FORCE_BACKEND
-};
-skinny_status_t call_context(CallCtx *c);   // the current device, set up if need be
-bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1);
-// skinny_gemm_bf16 / skinny_gemm_bf16_bf16out, and their checks without the launch
-skinny_status_t check_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const void *Y, int ldy, int M,
-                           int N, int K, int out_bf16);
-// (allow_pdl false: the launch waits for what precedes it whatever the option says)
-skinny_status_t run_gemm(const uint16_t *X, int ldx, const uint16_t *W, int ldw, void *Y, int ldy, int M, int N,
-                         int K, void *stream, int out_bf16, bool allow_pdl = true);
-
 // Allow `fn` the device's opt-in shared memory per block, less its static part.
 template <typename F>
 inline cudaError_t set_max_dyn_smem(F *fn) {

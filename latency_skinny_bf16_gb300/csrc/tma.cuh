@@ -30,13 +30,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
-// Box at (c0 = K element, c1 = row, c2 = matrix) of a stack of matrices.
-__device__ __forceinline__ void tma_load_stack(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                               uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
-}
 // Byte offset of the 16-byte piece `c` (8 elements; c / 8 selects the 64-element
 // box) of row `r` in a run of boxes of `rows` rows each (rows a multiple of 8).
 __host__ __device__ __forceinline__ uint32_t sw128_offset(int r, int c, int rows) {
@@ -46,9 +39,6 @@ __host__ __device__ __forceinline__ uint32_t sw128_offset(int r, int c, int rows
 // Host side (tmem_gemm.cu).  bf16 [rows, cols] with row stride ld (elements),
 // boxes of 64 columns x box_rows rows; false when the driver refuses the map.
 bool encode_bf16_2d(CUtensorMap *map, const void *ptr, int cols, int rows, int64_t ld, int box_rows);
-// bf16 [n, rows, cols], row stride ld, matrix stride lde (elements), boxes of 64 columns x box_rows rows.
-bool encode_bf16_stack(CUtensorMap *map, const void *ptr, int cols, int64_t rows, int n, int64_t ld, int64_t lde,
-                       int box_rows);
 // A 3-D view [cols / 64][rows][64] (cols a multiple of 64), boxes of
 // kb x box_rows x 64: one copy moves kb consecutive 64-column boxes.
 bool encode_bf16_3d(CUtensorMap *map, const void *ptr, int cols, int rows, int64_t ld, int box_rows, int kb);

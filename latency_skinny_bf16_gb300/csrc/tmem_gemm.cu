@@ -61,7 +61,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
-#include "tma.cuh"
+#include "tma_stack.cuh"
 
 namespace skinny {
 namespace {
