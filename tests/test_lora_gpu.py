@@ -151,3 +151,16 @@ def test_graph_and_streams(out):
                 torch.cuda.synchronize()
                 assert torch.equal(y, v)
             del g
+
+
+def test_infinite_adapter_gives_what_the_definition_gives():
+    """An infinite element of B: its product with V is infinite of V's sign (NaN where V is 0), whatever bits V has."""
+    x, w, a, b, _, _ = inputs(9, 64, 128, 3, 8, seed=6, mixed=False)
+    x[3] = 0.0                                              # V of this token is 0
+    b[:, 7, 1], b[:, 9, 2] = float("inf"), float("-inf")
+    ids = torch.arange(9, dtype=torch.int32, device="cuda") % 3
+    y = sk.lora_gemm(x, w, a, b, ids).double().cpu().numpy()
+    want = np.stack([host(w) @ host(x)[m] + host(b)[m % 3] @ (host(a)[m % 3] @ host(x)[m]) for m in range(9)])
+    assert np.array_equal(np.isnan(y), np.isnan(want)) and np.isnan(want[3, 7])
+    inf = np.isinf(want)
+    assert inf.sum() == 16 and np.array_equal(y[inf], want[inf]) and np.isfinite(y[~inf & ~np.isnan(want)]).all()
