@@ -17,6 +17,9 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kSortCluster = 8;
+constexpr int kBulkThreads = 64;
+constexpr int kBulkBytes = 2048;       // of a row, per chunk
+constexpr uint64_t kBulkDrainNs = 200ull * 1000 * 1000;
 
 // ------------------------------------------------------------------ vectors
 template <int BYTES> struct Vec;
@@ -177,20 +180,24 @@ expert_sort_kernel(const int32_t *__restrict__ ids, int64_t ldid, int k, int n, 
     for (int i = tid; i < W * E; i += blockDim.x) hist[i] = 0;
     griddep_wait();
     __syncthreads();
-    const int seg = ((n + kSortCluster * W - 1) / (kSortCluster * W) + 31) / 32 * 32;
+    const int64_t seg = (((int64_t)n + kSortCluster * W - 1) / (kSortCluster * W) + 31) / 32 * 32;
     const int64_t f0 = (int64_t)(rank * W + warp) * seg;
     const int steps = f0 < n ? (int)((min((int64_t)n, f0 + seg) - f0 + 31) / 32) : 0;
     int *wh = hist + warp * E;
-    constexpr int U = 4;
-    for (int s = 0; s < steps; s += U) {
-        int id[U];
+    constexpr int U = 8;
+    int id[U];
+    auto read = [&](int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
             id[u] = (s + u < steps && f < n) ? load_id(ids, ldid, k, (int)f, E) : -1;
         }
+    };
+    for (int s = 0; s < steps; s += U) {
+        read(s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (s + u >= steps) break;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id[u]);
             if (id[u] >= 0 && lane == __ffs(same) - 1) wh[id[u]] += __popc(same);
             __syncwarp();
@@ -240,21 +247,17 @@ expert_sort_kernel(const int32_t *__restrict__ ids, int64_t ldid, int k, int n, 
         for (int64_t p = (int64_t)total + rank * blockDim.x + tid; p < n; p += kSortCluster * blockDim.x) order[p] = -1;
     __syncthreads();
     for (int s = 0; s < steps; s += U) {
-        int id[U];
+        if (steps > U) read(s);        // else the first pass has left them
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
-            id[u] = (s + u < steps && f < n) ? load_id(ids, ldid, k, (int)f, E) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+            if (s + u >= steps) break;
             const int64_t f = f0 + (int64_t)(s + u) * 32 + lane;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id[u]);
             const int p = id[u] >= 0 ? base[id[u]] + wh[id[u]] + __popc(same & ((1u << lane) - 1)) : -1;
             __syncwarp();
             if (id[u] >= 0 && lane == __ffs(same) - 1) wh[id[u]] += __popc(same);
             __syncwarp();
-            if (s + u < steps && f < n) {
+            if (f < n) {
                 pos[f] = p;
                 if (order && p >= 0) order[p] = (int)f;
             }
@@ -457,6 +460,104 @@ combine_kernel(const char *__restrict__ Ys, int64_t ldys_bytes, int rows, const 
     else combine_piece<IN16, OUT16, VB, 8, IT>(Ys, ldys_bytes, e, n, v0, v1, y, lane);
 }
 
+// Rows that start or end off 8 bytes (bf16: off 4).  Loaded element by element
+// they take a request for every 128 bytes (fp32; 64 for bf16); instead the copy
+// engine brings the whole 16-byte pieces that hold a chunk of each row to shared
+// memory, eight rows at a time, where elements are read at any offset.  Grid
+// (chunks, T).  A token one of whose rows' pieces would reach past Ys (its
+// first and last row may) is read element by element.  GB300, 3001 tokens x 6 x
+// 2881: fp32 51 us element by element, 45 this way (floor 34), bf16 80 and 32
+// (floor 17); chunks of 4 KB and 128 threads 46 and 36, of 1 KB 69 and 45.
+template <bool IN16, bool OUT16>
+__global__ void __launch_bounds__(kBulkThreads)
+combine_bulk_kernel(const char *__restrict__ Ys, int64_t ldys_bytes, int rows, const int32_t *__restrict__ pos,
+                    const float *__restrict__ weights, int64_t ldw, int k, int H, char *__restrict__ Y, int64_t ldy_bytes,
+                    int *status, uint64_t budget_ns)
+{
+    constexpr int ES = IN16 ? 2 : 4, PER = kBulkBytes / ES / kBulkThreads, U = 8;
+    __shared__ __align__(128) char buf[U][kBulkBytes + 16];
+    __shared__ Entries e;
+    __shared__ __align__(8) uint64_t bar_store;
+    __shared__ int s_n;
+    const uint32_t bar = smem_u32(&bar_store);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t t = blockIdx.y;
+    griddep_launch_dependents();
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbarrier_init_cluster();
+    }
+    griddep_wait();
+    if (tid < 32) {
+        const int n = live_entries(e, pos, weights, ldw, t, k, rows, lane);
+        if (lane == 0) s_n = n;
+    }
+    __syncthreads();
+    const int n = s_n;
+    const int first = blockIdx.x * (kBulkBytes / ES), len = min(H - first, kBulkBytes / ES);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(Ys), hi = lo + (uintptr_t)((rows - 1) * ldys_bytes + (int64_t)H * ES);
+    float acc[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) acc[x] = 0.f;
+    int phase = 0;
+    for (int j0 = 0; j0 < n; j0 += U) {
+        const int m = min(U, n - j0);
+        bool inside = true;
+        uint32_t bytes = 0;
+        for (int u = 0; u < m; ++u) {
+            const uintptr_t a = lo + (uintptr_t)((int64_t)e.p[j0 + u] * ldys_bytes + (int64_t)first * ES);
+            const uintptr_t a0 = a & ~(uintptr_t)15, a1 = (a + (uintptr_t)(len * ES) + 15) & ~(uintptr_t)15;
+            inside = inside && a0 >= lo && a1 <= hi;
+            bytes += (uint32_t)(a1 - a0);
+        }
+        if (inside) {                  // the same for every thread
+            if (tid == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(bar, bytes);
+                for (int u = 0; u < m; ++u) {
+                    const uintptr_t a = lo + (uintptr_t)((int64_t)e.p[j0 + u] * ldys_bytes + (int64_t)first * ES);
+                    const uintptr_t a0 = a & ~(uintptr_t)15, a1 = (a + (uintptr_t)(len * ES) + 15) & ~(uintptr_t)15;
+                    bulk_copy_g2s(smem_u32(buf[u]), reinterpret_cast<const void *>(a0), (uint32_t)(a1 - a0), bar);
+                }
+            }
+            const bool got = mbar_wait_bounded(bar, (uint32_t)(phase & 1), budget_ns);
+            if (__syncthreads_or(got ? 0 : 1)) {
+                if (tid == 0) {
+                    report_status(status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitX);
+                    // the copies land before the CTA leaves
+                    if (!mbar_wait_bounded(bar, (uint32_t)(phase & 1), kBulkDrainNs))
+                        report_status(status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+                }
+                __syncthreads();
+                return;
+            }
+            ++phase;
+        }
+        for (int u = 0; u < m; ++u) {
+            const float w = e.w[j0 + u];
+            const char *row = Ys + (int64_t)e.p[j0 + u] * ldys_bytes + (int64_t)first * ES;
+            const char *at = buf[u] + (reinterpret_cast<uintptr_t>(row) & 15);
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                const int i = x * kBulkThreads + tid;
+                if (i >= len) break;
+                float v;
+                if constexpr (IN16) v = bf16_one(inside ? *reinterpret_cast<const uint16_t *>(at + 2 * i) : ldg_u16(row + 2 * i));
+                else v = inside ? *reinterpret_cast<const float *>(at + 4 * i) : __ldcg(reinterpret_cast<const float *>(row + 4 * i));
+                acc[x] = fmaf(w, v, acc[x]);
+            }
+        }
+        __syncthreads();               // the rows are read before the next ones land
+    }
+    char *y = Y + t * ldy_bytes;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+        const int i = x * kBulkThreads + tid;
+        const float v[1] = {acc[x]};
+        if (i < len) store_els<OUT16, 1>(y, first + i, v);
+    }
+}
+
 // ------------------------------------------------------------------ gradient of combine
 // S warps of a CTA share a token (8 / S tokens a CTA), eight entries at a time:
 // dY[t] is read once per eight entries, each Ys row read and each dYs row
@@ -586,8 +687,11 @@ int row_chunks(int64_t T, int nvec, int num_sms) {
     return (int)(want < most ? want : (most > 0 ? most : 1));
 }
 
-// Entries up to which the one-launch form is taken.
-constexpr int kSmallEntries = 1024;
+// Whether the one-launch form is taken: its work grows with the square of the
+// entries, divided by the entries a CTA counts for.  GB300, one launch against
+// sort and copy, us: 192 x 8 entries 5.5 and 8.8, 256 x 8 7.9 and 9.3, 384 x 8
+// 10.8 and 8.8, 2000 x 1 12.5 and 9.5.
+bool few_entries(int n, int k) { return n <= 1024 || (n <= 2048 && k >= 4); }
 
 template <int VB>
 cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStream_t stream, bool pdl) {
@@ -597,7 +701,7 @@ cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStrea
     int T = a.T, k = a.k, E = a.E, n = a.T * a.k;
     const int32_t *ids = a.ids;
     int32_t *pos = a.pos, *order = a.order, *offsets = a.offsets;
-    if (n <= kSmallEntries) {
+    if (few_entries(n, k)) {
         const int smem = 4 * (n > E ? n : E);
         void *args[] = {&ids, &ldid, &X, &ldx, &T, &k, &E, &nvec, &pos, &order, &offsets, &Xs, &ldxs};
         return launch((const void *)dispatch_small_kernel<VB>, dim3(T + 1, T ? row_chunks(T, nvec, num_sms) : 1),
@@ -641,7 +745,33 @@ cudaError_t combine_vec(const CombineArgs &a, int num_sms, cudaStream_t stream, 
                   args);
 }
 template <bool IN16, bool OUT16>
-cudaError_t combine_types(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t combine_bulk(const CombineArgs &a, const CallCtx &c, cudaStream_t stream) {
+    const char *Ys = static_cast<const char *>(a.Ys);
+    char *Y = static_cast<char *>(a.Y);
+    int64_t ldys = a.ldys * (IN16 ? 2 : 4), ldy = a.ldy * (OUT16 ? 2 : 4), ldw = a.ldw;
+    int rows = a.rows, k = a.k, H = a.H;
+    const int32_t *pos = a.pos;
+    const float *w = a.weights;
+    int *status = c.status;
+    uint64_t budget = c.budget_ns;
+    constexpr int per = kBulkBytes / (IN16 ? 2 : 4);
+    // the grid's y holds 65535 tokens
+    for (int t0 = 0; t0 < a.T; t0 += 65535) {
+        const int n = a.T - t0 < 65535 ? a.T - t0 : 65535;
+        void *args[] = {&Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &Y, &ldy, &status, &budget};
+        const cudaError_t e = launch((const void *)combine_bulk_kernel<IN16, OUT16>, dim3((H + per - 1) / per, n),
+                                     kBulkThreads, 0, stream, c.pdl, 1, args);
+        if (e != cudaSuccess) return e;
+        if (pos) pos += (int64_t)n * k;
+        if (w) w += (int64_t)n * ldw;
+        Y += (int64_t)n * ldy;
+    }
+    return cudaSuccess;
+}
+template <bool IN16, bool OUT16>
+cudaError_t combine_types(const CombineArgs &a, const CallCtx &c, cudaStream_t stream) {
+    const int num_sms = c.num_sms;
+    const bool pdl = c.pdl;
     constexpr int ib = IN16 ? 2 : 4, ob = OUT16 ? 2 : 4;
     // the widest load at which every row of Ys starts, ends and is stored aligned
     const uintptr_t in = u(a.Ys) | (uintptr_t)(a.ldys * ib), out = u(a.Y) | (uintptr_t)(a.ldy * ob);
@@ -653,10 +783,8 @@ cudaError_t combine_types(const CombineArgs &a, int num_sms, cudaStream_t stream
     if (fits(8)) return combine_vec<IN16, OUT16, 8>(a, num_sms, stream, pdl);
     if constexpr (IN16) {
         if (fits(4)) return combine_vec<IN16, OUT16, 4>(a, num_sms, stream, pdl);
-        return combine_vec<IN16, OUT16, 2>(a, num_sms, stream, pdl);
-    } else {
-        return combine_vec<IN16, OUT16, 4>(a, num_sms, stream, pdl);
     }
+    return combine_bulk<IN16, OUT16>(a, c, stream);
 }
 
 template <bool B16, int VB, bool DW>
@@ -709,9 +837,9 @@ cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t str
     }
 }
 
-cudaError_t launch_combine(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
-    if (a.in16) return a.out16 ? combine_types<true, true>(a, num_sms, stream, pdl) : combine_types<true, false>(a, num_sms, stream, pdl);
-    return a.out16 ? combine_types<false, true>(a, num_sms, stream, pdl) : combine_types<false, false>(a, num_sms, stream, pdl);
+cudaError_t launch_combine(const CombineArgs &a, const CallCtx &c, cudaStream_t stream) {
+    if (a.in16) return a.out16 ? combine_types<true, true>(a, c, stream) : combine_types<true, false>(a, c, stream);
+    return a.out16 ? combine_types<false, true>(a, c, stream) : combine_types<false, false>(a, c, stream);
 }
 
 cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {

@@ -1,7 +1,7 @@
 // expert_rows.h -- host-side declarations of expert_rows.cu.
 #pragma once
 
-#include "internal.h"
+#include "calls.h"
 #include "skinny_experts.h"
 
 namespace skinny {
@@ -51,7 +51,7 @@ struct CombineGradArgs {
 
 cudaError_t expert_rows_prepare();
 cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t stream, bool pdl);
-cudaError_t launch_combine(const CombineArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_combine(const CombineArgs &a, const CallCtx &c, cudaStream_t stream);
 cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl);
 
 }  // namespace skinny

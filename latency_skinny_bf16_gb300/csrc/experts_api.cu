@@ -104,7 +104,7 @@ skinny_status_t skinny_expert_combine(const void *Ys, int ldys, int rows, const 
     if (st != SKINNY_OK) return st;
     const CombineArgs a{Ys, ldys, rows, pos, weights, ldw, T, k, H, in_dtype == SKINNY_BF16, out_dtype == SKINNY_BF16,
                         Y, ldy};
-    return launched(launch_combine(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
+    return launched(launch_combine(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void *Ys, int ldys, int rows,

@@ -300,3 +300,36 @@ def test_places_past_32_bits():
     assert torch.equal(xs[-1], x[int(order[-1]) // k])
     y = sk.expert_combine(xs, pos, torch.full((T, k), 0.5, device="cuda"))
     assert torch.equal(y, x)
+
+
+@pytest.mark.parametrize("H,dtype", [(1030, "bf16"), (2051, "bf16"), (4097, "fp32"), (1, "fp32"), (3, "bf16")])
+@pytest.mark.parametrize("k", [1, 8, 20])
+def test_combine_rows_of_any_alignment(H, dtype, k):
+    """Rows that start and end off 16 bytes, chunks of them, the first and the last row of a tensor that itself
+    starts off 16 bytes, and rows that lie end to end with a stride above their width."""
+    T, E = 11, 40
+    ids, w = ref.routing(T, k, E, seed=H + k, drop=0.2)
+    pos, _, _ = ref.dispatch(ids, E)
+    pos[0, 0], pos[1, 0] = 0, T * k - 1
+    pt, wt = torch.from_numpy(pos).cuda(), torch.from_numpy(w).cuda()
+    for pad, offset in ((0, 0), (0, 1), (5, 3)):
+        ys = matrix(T * k, H, dtype, seed=H, pad=pad, offset=offset)
+        got = sk.expert_combine(ys, pt, wt)
+        y, mag = ref.combine(host(ys), pos, w)
+        assert (np.abs(host(got) - y) <= ref.rounded(y, 1.01 * k * ref.U32 * mag, dtype)).all()
+        even = torch.zeros((T * k, H + 8 - H % 8), dtype=ys.dtype, device="cuda")[:, :H]
+        even.copy_(ys)
+        assert torch.equal(sk.expert_combine(even, pt, wt, out=torch.empty((T, H + 8 - H % 8), dtype=ys.dtype, device="cuda")[:, :H]), got)
+
+
+def test_combine_bounded_wait_reports_and_recovers():
+    ys = matrix(64, 1001, "fp32", seed=3)
+    pos = torch.arange(64, dtype=torch.int32, device="cuda").reshape(16, 4)
+    want = sk.expert_combine(ys, pos)
+    with sk.options(wait_timeout_us=0):
+        sk.expert_combine(ys, pos)
+        torch.cuda.synchronize()
+    assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
+    for _ in range(3):
+        assert torch.equal(sk.expert_combine(ys, pos), want)
+    assert sk.skinny_get_device_status() == 0
