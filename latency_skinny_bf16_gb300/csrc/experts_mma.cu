@@ -11,8 +11,15 @@
 // K in pieces of 64 (or, in teams, fewer warps a tile), against up to 8 * TT rows
 // of X at once; their sums are added in order through shared memory.  Per warp and step, 2 KB of W are in
 // flight, so four CTAs on an SM cover device memory's latency.
+// Rows of W that are not 16-byte aligned start at the same place within 16 bytes
+// every P rows (P = 2, 4 or 8).  A tile is rows that do (kAlike): W comes in whole
+// pieces as it lies, and X alone is shifted, by as many elements; the shifting is
+// in registers.  (GB300, 16 rows, 60 experts 2816 x 4095: 79 us, 95 with W shifted
+// too; 50 rows, 7 experts 7104 x 6333: 235 and 357.)
 // At most four MMAs (64 elements of K) are summed in the tensor core before a
 // rounded add.
+#include <type_traits>
+
 #include "experts_gemm.h"
 #include "mma_rows.cuh"
 
@@ -21,6 +28,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+
+enum Rows : int {
+    kAny,                // of X and W; every piece of W is shifted too
+    kAligned,            // 16 bytes
+    kAlike,              // of X any, of W alike every P rows
+};
 
 struct Params {
     const uint16_t *X;
@@ -34,13 +47,15 @@ struct Params {
     void *Y;
     int64_t ldy;
     int kw;              // warps of a CTA along K: 1, 2, 4 or 8; its 8 / kw teams take tiles of their own
+    int P;               // kAlike
     Extent xe, we;
 };
 
-template <bool ALIGNED, bool SWIGLU, int TT>
+template <Rows ROWS, bool SWIGLU, int TT>
 __global__ void __launch_bounds__(kThreads, TT == 1 ? 4 : 2)
 experts_mma_kernel(const Params p)
 {
+    constexpr bool ALIGNED = ROWS == kAligned;
     extern __shared__ int smem[];
     __shared__ __align__(16) float part[kWarps][TT][32][4];
     __shared__ int s_warp[kWarps];
@@ -48,7 +63,7 @@ experts_mma_kernel(const Params p)
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int E = p.E, N = p.N, K = p.K;
+    const int E = p.E, N = p.N;
     int *row = smem;                                  // clamped offsets [E + 1]
     int *active = smem + E + 1;                       // the experts that have rows
     for (int e = tid; e <= E; e += kThreads)
@@ -70,7 +85,8 @@ experts_mma_kernel(const Params p)
         __syncthreads();
     }
     constexpr int kTileN = SWIGLU ? 8 : 16;
-    const int tiles = (N + kTileN - 1) / kTileN;
+    const int P = ROWS == kAlike ? p.P : 1;
+    const int tiles = P * (((N + P - 1) / P + kTileN - 1) / kTileN);
     const int64_t line = (int64_t)found * tiles;
     const int KW = p.kw, kw = warp % KW, team = warp / KW, teams = kWarps / KW;
     auto meet = [&] {                                 // the warps of a team
@@ -79,22 +95,31 @@ experts_mma_kernel(const Params p)
     };
     for (int64_t i = (int64_t)blockIdx.x * teams + team; i < line; i += (int64_t)gridDim.x * teams) {
         const int a = (int)(i / tiles);
-        const int e = active[a], n0 = (int)(i - (int64_t)a * tiles) * kTileN;
+        const int in = (int)(i - (int64_t)a * tiles);
+        const int e = active[a], c0 = in % P, j0 = in / P * kTileN;      // rows c0 + P j, j from j0 on
+        const int J = (N - c0 + P - 1) / P;
+        if (J <= 0) continue;
         const int r0 = row[e], r1 = row[e + 1];
         const uint16_t *We = p.W + (int64_t)e * p.ldwe;
         // rows past the end repeat the last one; they are not stored
-        const int nl = min(n0 + g, N - 1), nh = SWIGLU ? N + nl : min(n0 + 8 + g, N - 1);
+        const int nl = c0 + P * min(j0 + g, J - 1), nh = SWIGLU ? N + nl : c0 + P * min(j0 + 8 + g, J - 1);
         const uint16_t *wl = We + (int64_t)nl * p.ldw, *wh = We + (int64_t)nh * p.ldw;
+        // kAlike: the row's elements are o behind the piece it starts in
+        const int o = ROWS == kAlike && p.K > 0 ? (int)(reinterpret_cast<uintptr_t>(wl) & 15) / 2 : 0;
+        wl -= o;
+        wh -= o;
+        const int K = p.K + o;
         for (int rb = r0; rb < r1; rb += 8 * TT) {
             const int nt = min(TT, (r1 - rb + 7) / 8);
             const uint16_t *x[TT];
             bool live[TT];
-            bool inside = ALIGNED || (row_inside(wl, K, p.we) && row_inside(wh, K, p.we));
+            bool inside = ROWS != kAny || (row_inside(wl, K, p.we) && row_inside(wh, K, p.we));
 #pragma unroll
             for (int q = 0; q < TT; ++q) {
                 live[q] = rb + 8 * q + g < r1;
                 x[q] = p.X + (int64_t)(live[q] ? rb + 8 * q + g : rb) * p.ldx;
-                if (!ALIGNED) inside = inside && row_inside(x[q], K, p.xe);
+                if (!ALIGNED) inside = inside && row_inside(x[q], p.K, p.xe);
+                x[q] -= o;
             }
             if (!ALIGNED) inside = __all_sync(0xFFFFFFFFu, inside);
             float acc[TT][4];
@@ -102,60 +127,81 @@ experts_mma_kernel(const Params p)
             for (int q = 0; q < TT; ++q)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[q][j] = 0.f;
-            auto products = [&](const uint4 (&l)[2], const uint4 (&h)[2], const uint4 (&v)[TT][2]) {
-#pragma unroll
-                for (int q = 0; q < TT; ++q) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_rows32(d, l[0], h[0], v[q][0]);
-                    mma_rows32(d, l[1], h[1], v[q][1]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[q][j] += d[j];
-                }
+            auto piece = [](const uint16_t *w) {
+                if constexpr (ROWS == kAny) return load_whole8<false, true>(w, 0);
+                // neighbours share sectors: through L1 where X leaves it room (GB300, 16 rows, 60 experts
+                // 2816 x 4095: 79 us with, 82 without; 354 rows, 86 experts 318 x 6727: 282 and 190)
+                if constexpr (ROWS == kAlike && TT == 1) return ldg16<true>(w);
+                return ldg_stream_v4(w);
             };
-            int k = 64 * kw;
-            if (inside) {
-#pragma unroll 2
-                for (; k + 64 <= K; k += 64 * KW) {
-                    uint4 l[2], h[2], v[TT][2];
+            // the sums of the first NT token tiles
+            auto sums = [&](auto NTc) {
+                constexpr int NT = decltype(NTc)::value;
+                auto products = [&](const uint4 (&l)[2], const uint4 (&h)[2], const uint4 (&v)[NT][2]) {
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_rows32(d, l[0], h[0], v[q][0]);
+                        mma_rows32(d, l[1], h[1], v[q][1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[q][j] += d[j];
+                    }
+                };
+                // the ends of the rows, or rows at an end of W or X
+                auto ends = [&](int k) {
+                    uint4 l[2], h[2], v[NT][2];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        l[s] = load_whole8<ALIGNED, true>(wl, k + 32 * s + 8 * t);
-                        h[s] = load_whole8<ALIGNED, true>(wh, k + 32 * s + 8 * t);
+                        const int k8 = k + 32 * s + 8 * t;
+                        l[s] = load_row8<ROWS != kAny, true>(wl, k8, K, p.we, o);
+                        h[s] = load_row8<ROWS != kAny, true>(wh, k8, K, p.we, o);
 #pragma unroll
-                        for (int q = 0; q < TT; ++q) {
+                        for (int q = 0; q < NT; ++q) {
                             v[q][s] = make_uint4(0, 0, 0, 0);
-                            if (live[q]) v[q][s] = load_whole8<ALIGNED, false>(x[q], k + 32 * s + 8 * t);
+                            if (live[q]) v[q][s] = load_row8<ALIGNED, false>(x[q], k8, K, p.xe, o);
                         }
                     }
                     products(l, h, v);
+                };
+                int k = 64 * kw;
+                if (ROWS == kAlike && k < o) {
+                    ends(k);
+                    k += 64 * KW;
                 }
-            }
-            for (; k < K; k += 64 * KW) {             // the end of the rows, or rows at an end of W or X
-                uint4 l[2], h[2], v[TT][2];
+                if (inside) {
+#pragma unroll 2
+                    for (; k + 64 <= K; k += 64 * KW) {
+                        uint4 l[2], h[2], v[NT][2];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    l[s] = load_row8<ALIGNED, true>(wl, k + 32 * s + 8 * t, K, p.we);
-                    h[s] = load_row8<ALIGNED, true>(wh, k + 32 * s + 8 * t, K, p.we);
+                        for (int s = 0; s < 2; ++s) {
+                            l[s] = piece(wl + k + 32 * s + 8 * t);
+                            h[s] = piece(wh + k + 32 * s + 8 * t);
 #pragma unroll
-                    for (int q = 0; q < TT; ++q) {
-                        v[q][s] = make_uint4(0, 0, 0, 0);
-                        if (live[q]) v[q][s] = load_row8<ALIGNED, false>(x[q], k + 32 * s + 8 * t, K, p.xe);
+                            for (int q = 0; q < NT; ++q) {
+                                v[q][s] = make_uint4(0, 0, 0, 0);
+                                if (live[q]) v[q][s] = load_whole8<ALIGNED, false>(x[q], k + 32 * s + 8 * t);
+                            }
+                        }
+                        products(l, h, v);
                     }
                 }
-                products(l, h, v);
-            }
+                for (; k < K; k += 64 * KW) ends(k);
+            };
+            if (TT == 1 || nt == 1) sums(std::integral_constant<int, 1>{});
+            else if (nt == 2) sums(std::integral_constant<int, TT < 2 ? TT : 2>{});
+            else sums(std::integral_constant<int, TT>{});
             // the results of token tile q from lane sl, its two rows of X
             auto result = [&](int q, int sl, const float (&c)[4]) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int r = rb + 8 * q + 2 * (sl & 3) + j, n = n0 + (sl >> 2);
+                    const int r = rb + 8 * q + 2 * (sl & 3) + j, nj = j0 + (sl >> 2);
                     if (r >= r1) continue;
-                    const int64_t y = (int64_t)r * p.ldy + n;
+                    const int64_t y = (int64_t)r * p.ldy + c0 + P * nj;
                     if constexpr (SWIGLU) {
-                        if (n < N) store_y(p.Y, p.out_bf16, y, c[j] / (1.f + expf(-c[j])) * c[2 + j]);
+                        if (nj < J) store_y(p.Y, p.out_bf16, y, c[j] / (1.f + expf(-c[j])) * c[2 + j]);
                     } else {
-                        if (n < N) store_y(p.Y, p.out_bf16, y, c[j]);
-                        if (n + 8 < N) store_y(p.Y, p.out_bf16, y + 8, c[2 + j]);
+                        if (nj < J) store_y(p.Y, p.out_bf16, y, c[j]);
+                        if (nj + 8 < J) store_y(p.Y, p.out_bf16, y + 8 * P, c[2 + j]);
                     }
                 }
             };
@@ -184,20 +230,20 @@ experts_mma_kernel(const Params p)
     }
 }
 
-template <bool ALIGNED, bool SWIGLU, int TT>
+template <Rows ROWS, bool SWIGLU, int TT>
 cudaError_t launch_tt(const Params &p, int64_t tiles, const CallCtx &c, cudaStream_t stream) {
     Params q = p;
     void *args[] = {&q};
     const int64_t most = (TT == 1 ? 4 : 2) * (int64_t)c.num_sms, per = kWarps / p.kw, ctas = (tiles + per - 1) / per;
-    return launch_plain((const void *)experts_mma_kernel<ALIGNED, SWIGLU, TT>, dim3((unsigned)(ctas < most ? ctas : most)),
+    return launch_plain((const void *)experts_mma_kernel<ROWS, SWIGLU, TT>, dim3((unsigned)(ctas < most ? ctas : most)),
                         kThreads, 4 * (2 * p.E + 1), stream, c.pdl, args);
 }
-template <bool ALIGNED, bool SWIGLU>
+template <Rows ROWS, bool SWIGLU>
 cudaError_t launch_as(const Params &p, int64_t tiles, const CallCtx &c, cudaStream_t stream) {
     // rows of X held at once: 8, or 32 where the experts have more than 4 on average (GB300, TT 1 and 4, us:
     // 256 experts 2048 x 2048, 1 row each 154 and 242; 8 experts 2048 x 2048, 16 rows each 34 and 24)
-    if (p.rows <= 4 * p.E) return launch_tt<ALIGNED, SWIGLU, 1>(p, tiles, c, stream);
-    return launch_tt<ALIGNED, SWIGLU, 4>(p, tiles, c, stream);
+    if (p.rows <= 4 * p.E) return launch_tt<ROWS, SWIGLU, 1>(p, tiles, c, stream);
+    return launch_tt<ROWS, SWIGLU, 4>(p, tiles, c, stream);
 }
 
 }  // namespace
@@ -205,8 +251,11 @@ cudaError_t launch_as(const Params &p, int64_t tiles, const CallCtx &c, cudaStre
 cudaError_t launch_experts_mma(const ExpertsArgs &a, const CallCtx &c, cudaStream_t stream) {
     const uintptr_t xl = reinterpret_cast<uintptr_t>(a.X), wl = reinterpret_cast<uintptr_t>(a.W);
     const int64_t wrows = a.swiglu ? 2ll * a.N : a.N;
-    const int per = a.swiglu ? 8 : 16;
-    const int64_t tiles = (int64_t)(a.rows < a.E ? a.rows : a.E) * ((a.N + per - 1) / per);
+    const bool al = (xl | wl) % 16 == 0 && (a.ldx | a.ldw | a.ldwe) % 8 == 0;
+    const int P = a.ldw % 8 == 0 ? 1 : a.ldw % 4 == 0 ? 2 : a.ldw % 2 == 0 ? 4 : 8;
+    const bool alike = !al && (!a.swiglu || a.N % P == 0);   // an up lies as its gate
+    const int per = a.swiglu ? 8 : 16, apart = alike ? P : 1;
+    const int64_t tiles = (int64_t)(a.rows < a.E ? a.rows : a.E) * apart * (((a.N + apart - 1) / apart + per - 1) / per);
     // Warps per tile: as many as K has pieces for on a long line; on a short one
     // the number with the least steps of K one after the other, rounds of tiles
     // times pieces of K per warp (the smaller number when equal: fewer sums to
@@ -221,11 +270,11 @@ cudaError_t launch_experts_mma(const ExpertsArgs &a, const CallCtx &c, cudaStrea
         if (best < 0 || steps < best || tiles >= slots) { best = steps; kw = w; }
     }
     const Params p{a.X, a.ldx, a.rows, a.offsets, a.W, a.ldw, a.ldwe, a.E, a.N, a.K, a.out_bf16, a.Y, a.ldy,
-                   kw, {xl, xl + (uintptr_t)(2 * ((a.rows - 1) * a.ldx + a.K))},
+                   kw, P, {xl, xl + (uintptr_t)(2 * ((a.rows - 1) * a.ldx + a.K))},
                    {wl, wl + (uintptr_t)(2 * ((a.E - 1) * a.ldwe + (wrows - 1) * a.ldw + a.K))}};
-    const bool al = (xl | wl) % 16 == 0 && (a.ldx | a.ldw | a.ldwe) % 8 == 0;
-    if (al) return a.swiglu ? launch_as<true, true>(p, tiles, c, stream) : launch_as<true, false>(p, tiles, c, stream);
-    return a.swiglu ? launch_as<false, true>(p, tiles, c, stream) : launch_as<false, false>(p, tiles, c, stream);
+    if (al) return a.swiglu ? launch_as<kAligned, true>(p, tiles, c, stream) : launch_as<kAligned, false>(p, tiles, c, stream);
+    if (!a.swiglu) return launch_as<kAlike, false>(p, tiles, c, stream);
+    return alike ? launch_as<kAlike, true>(p, tiles, c, stream) : launch_as<kAny, true>(p, tiles, c, stream);
 }
 
 }  // namespace skinny

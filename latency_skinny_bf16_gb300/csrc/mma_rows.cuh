@@ -68,22 +68,23 @@ __device__ __forceinline__ uint4 load_whole8(const uint16_t *row, int k) {
     }
 }
 
-// Eight bf16 elements from element k of `row`, those from `len` on zero: ends
-// of rows, and rows at the ends of their extent.
+// Eight bf16 elements from element k of `row`, those before `first` and from
+// `len` on zero: ends of rows, and rows at the ends of their extent.
 template <bool ALIGNED, bool STREAM>
-__device__ __forceinline__ uint4 load_row8(const uint16_t *row, int k, int len, const Extent &ext) {
+__device__ __forceinline__ uint4 load_row8(const uint16_t *row, int k, int len, const Extent &ext, int first = 0) {
     const uint16_t *at = row + k;
     if constexpr (ALIGNED) {
-        if (k + 8 <= len) return STREAM ? ldg_stream_v4(at) : ldg_v4(at);
+        if (k >= first && k + 8 <= len) return STREAM ? ldg_stream_v4(at) : ldg_v4(at);
     } else {
         const uintptr_t a = reinterpret_cast<uintptr_t>(at), a0 = a & ~(uintptr_t)15;
         const int off = (int)(a - a0);
-        if (k + 8 <= len && a0 >= ext.lo && a0 + (off ? 32 : 16) <= ext.hi) return load_whole8<ALIGNED, STREAM>(row, k);
+        if (k >= first && k + 8 <= len && a0 >= ext.lo && a0 + (off ? 32 : 16) <= ext.hi)
+            return load_whole8<ALIGNED, STREAM>(row, k);
     }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (k + e < len) w[e >> 1] |= (uint32_t)ldg_u16(at + e) << (16 * (e & 1));
+        if (k + e >= first && k + e < len) w[e >> 1] |= (uint32_t)ldg_u16(at + e) << (16 * (e & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

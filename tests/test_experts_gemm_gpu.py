@@ -222,3 +222,37 @@ def test_bounded_waits_report_and_recover(act):
         for _ in range(3):
             assert torch.equal(sk.experts_gemm(xs, offsets, w, activation=act)[:n], want[:n])
         assert sk.skinny_get_device_status() == 0
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("N,K", [(5, 63), (3, 7), (2, 9), (8, 1), (8, 3), (77, 130), (77, 129), (104, 777), (264, 57),
+                                 (136, 1001), (40, 514), (40, 2052), (300, 6121)])
+@pytest.mark.parametrize("counts", [[1, 0, 2], [0, 1, 16, 17, 33, 65]])
+def test_rows_that_lie_alike(N, K, counts, act):
+    """Odd lengths: rows of W that start alike within 16 bytes share a tile, also where N is no multiple of
+    their distance, or less than it."""
+    run(counts, N, K, act, "fp32", seed=N * K)
+
+
+@pytest.mark.parametrize("K,ld", [(129, 129), (130, 130), (132, 140), (250, 251)])
+def test_infinities_of_neighbouring_rows_and_padding(K, ld):
+    """What lies before and behind a row of W or X, within the 16 bytes of its ends, does not reach its sums."""
+    E, N, rows = 2, 48, 7
+    w, xs = stack((E, N, K), ld, 1), stack((1, rows, K), ld, 2)[0]
+    off = torch.tensor([0, 4, rows], dtype=torch.int32, device="cuda")
+    want = sk.experts_gemm(xs, off, w, out=torch.empty((rows, N), device="cuda")).clone()
+    bad = [(0, 5), (0, 11), (1, 0), (1, N - 1)]
+    for e, n in bad:
+        w[e, n, 0], w[e, n, K - 1] = float("inf"), float("nan")
+    xs[2, 0], xs[2, K - 1] = float("nan"), float("inf")
+    if ld > K:
+        torch.as_strided(w, (E * N - 1, ld - K), (ld, 1), w.storage_offset() + K).fill_(float("nan"))
+        torch.as_strided(xs, (rows - 1, ld - K), (ld, 1), xs.storage_offset() + K).fill_(float("inf"))
+    got = sk.experts_gemm(xs, off, w, out=torch.empty((rows, N), device="cuda"))
+    hit = torch.zeros((rows, N), dtype=torch.bool, device="cuda")
+    for e, n in bad:
+        hit[:4, n] |= e == 0
+        hit[4:, n] |= e == 1
+    hit[2] = True
+    assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[~hit], want[~hit])
