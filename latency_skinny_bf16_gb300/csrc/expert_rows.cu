@@ -11,6 +11,7 @@
 // written once each), and at decode sizes by launch latency.
 #include "common.cuh"
 #include "expert_rows.h"
+#include "mma_rows.cuh"
 
 namespace skinny {
 namespace {
@@ -650,6 +651,181 @@ combine_grad_kernel(const char *__restrict__ dY, int64_t lddy_bytes, const char 
     }
 }
 
+// ------------------------------------------------------------------ rows off 8 bytes, one to many
+// out[pos_f] = G[t] (kCopy: dispatch) or w_f G[t], with dw_f = <G[t], Ys[pos_f]>
+// (kScaleDot), for rows that start or end off 8 bytes, where loads and stores of
+// elements would bound it.  The copy engine brings a chunk of G[t] and of its
+// rows of Ys to shared memory in whole 16-byte pieces; a warp per row of out
+// writes whole pieces as they lie there, each from two of the chunk's shifted,
+// and single elements at the chunk's ends, where a piece belongs to other rows
+// too.  Grid (T, chunks; kScaleDot: 1, the dot products stay in registers).
+enum Spread : int { kCopy, kScale, kScaleDot };
+constexpr int kSpreadThreads = 128;
+constexpr int kSpreadBytes = 2032;     // of a row per chunk: 128 pieces wherever they start
+constexpr int kSpreadPitch = 2112;     // 16 bytes before the first piece and 32 behind the last are read, not used
+
+template <bool B16, Spread MODE>
+__global__ void __launch_bounds__(kSpreadThreads)
+spread_bulk_kernel(const char *__restrict__ G, int64_t ldg_bytes, int T, const char *__restrict__ Ys, int64_t ldys_bytes,
+                   int rows, const int32_t *__restrict__ pos, const float *__restrict__ weights, int64_t ldw, int k, int H,
+                   char *__restrict__ out, int64_t ldo_bytes, float *__restrict__ dw, int64_t lddw, int *status,
+                   uint64_t budget_ns)
+{
+    constexpr bool DOT = MODE == kScaleDot;
+    constexpr int ES = B16 ? 2 : 4, NE = 16 / ES, PER = kSpreadBytes / ES, WARPS = kSpreadThreads / 32;
+    constexpr int U = DOT ? 8 : kMaxTopk;              // entries at a time
+    __shared__ __align__(128) char buf[DOT ? 1 + U : 1][kSpreadPitch];
+    __shared__ Entries e;
+    __shared__ float part[WARPS][kMaxTopk];
+    __shared__ __align__(8) uint64_t bar_store;
+    __shared__ int s_n;
+    const uint32_t bar = smem_u32(&bar_store);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t = blockIdx.x;
+    griddep_launch_dependents();
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbarrier_init_cluster();
+    }
+    griddep_wait();
+    if (warp == 0) {
+        const int n = live_entries(e, pos, weights, ldw, t, k, rows, lane);
+        if (lane == 0) s_n = n;
+    }
+    if constexpr (DOT)
+        for (int i = tid; i < WARPS * kMaxTopk; i += kSpreadThreads) part[0][i] = 0.f;
+    __syncthreads();
+    const int n = s_n, chunks = (H + PER - 1) / PER;
+    const uintptr_t glo = reinterpret_cast<uintptr_t>(G), ghi = glo + (uintptr_t)((T - 1) * ldg_bytes + (int64_t)H * ES);
+    const uintptr_t ylo = reinterpret_cast<uintptr_t>(Ys), yhi = ylo + (uintptr_t)((rows - 1) * ldys_bytes + (int64_t)H * ES);
+    int phase = 0;
+    for (int j0 = 0; j0 < n; j0 += U) {
+        const int m = min(U, n - j0);
+        const int share = m >= WARPS ? 1 : m >= 2 ? 2 : WARPS, at_once = WARPS / share;    // warps per row, rows at once
+        float dot[2] = {0.f, 0.f};
+        for (int c = blockIdx.y; c < chunks; c += gridDim.y) {
+            const int first = c * PER, len = min(H - first, PER);
+            const int sources = DOT ? 1 + m : 1;
+            // row s of the sources, from `first` on
+            auto source = [&](int s) {
+                return s == 0 ? glo + (uintptr_t)(t * ldg_bytes + (int64_t)first * ES)
+                              : ylo + (uintptr_t)((int64_t)e.p[j0 + s - 1] * ldys_bytes + (int64_t)first * ES);
+            };
+            bool inside = true;        // whole pieces lie inside G and Ys; the same for every thread
+            uint32_t bytes = 0;
+            for (int s = 0; s < sources; ++s) {
+                const uintptr_t a = source(s), a0 = a & ~(uintptr_t)15, a1 = (a + (uintptr_t)(len * ES) + 15) & ~(uintptr_t)15;
+                inside = inside && a0 >= (s ? ylo : glo) && a1 <= (s ? yhi : ghi);
+                bytes += (uint32_t)(a1 - a0);
+            }
+            if (inside) {
+                if (tid == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar, bytes);
+                    for (int s = 0; s < sources; ++s) {
+                        const uintptr_t a = source(s), a0 = a & ~(uintptr_t)15, a1 = (a + (uintptr_t)(len * ES) + 15) & ~(uintptr_t)15;
+                        bulk_copy_g2s(smem_u32(buf[s] + 16), reinterpret_cast<const void *>(a0), (uint32_t)(a1 - a0), bar);
+                    }
+                }
+                const bool got = mbar_wait_bounded(bar, (uint32_t)(phase & 1), budget_ns);
+                if (__syncthreads_or(got ? 0 : 1)) {
+                    if (tid == 0) {
+                        report_status(status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitX);
+                        // the copies land before the CTA leaves
+                        if (!mbar_wait_bounded(bar, (uint32_t)(phase & 1), kBulkDrainNs))
+                            report_status(status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+                    }
+                    __syncthreads();
+                    return;
+                }
+                ++phase;
+            } else {
+                for (int s = 0; s < sources; ++s) {
+                    const uintptr_t a = source(s);
+                    char *to = buf[s] + 16 + (a & 15);
+                    for (int i = tid; i < len; i += kSpreadThreads) {
+                        if constexpr (B16) *reinterpret_cast<uint16_t *>(to + 2 * i) = ldg_u16(reinterpret_cast<const char *>(a) + 2 * i);
+                        else *reinterpret_cast<float *>(to + 4 * i) = __ldcg(reinterpret_cast<const float *>(a) + i);
+                    }
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int h = 0; h < (DOT ? U / WARPS : 1); ++h) {
+                for (int q = at_once * h + warp / share; q < m; q += DOT ? U : at_once) {
+                    const float w = e.w[j0 + q];
+                    char *d = out + (int64_t)e.p[j0 + q] * ldo_bytes + (int64_t)first * ES;
+                    const int off = (int)(reinterpret_cast<uintptr_t>(d) & 15);
+                    const int pieces = (off + len * ES + 15) / 16;
+                    const char *g = buf[0] + 16 + (source(0) & 15) - off;
+                    const char *y = DOT ? buf[1 + (DOT ? q : 0)] + 16 + (source(1 + q) & 15) - off : g;
+                    const int gs = (int)(smem_u32(g) & 15), ys = (int)(smem_u32(y) & 15);
+                    d -= off;
+                    g -= gs;
+                    y -= ys;
+#pragma unroll 2
+                    for (int i = lane + 32 * (warp % share); i < pieces; i += 32 * share) {
+                        const uint4 gv = shifted16(*reinterpret_cast<const uint4 *>(g + 16 * i),
+                                                   *reinterpret_cast<const uint4 *>(g + 16 * i + 16), gs);
+                        const int el = (16 * i - off) / ES;            // of the chunk; exact: off is whole elements
+                        const bool whole = el >= 0 && el + NE <= len;
+                        Raw<16> r, o;
+                        r.w[0] = gv.x; r.w[1] = gv.y; r.w[2] = gv.z; r.w[3] = gv.w;
+                        o = r;
+                        if constexpr (MODE != kCopy) {
+                            float v[NE];
+#pragma unroll
+                            for (int x = 0; x < NE; ++x) v[x] = w * raw_el<B16, 16>(r, x);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if constexpr (B16) o.w[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
+                                else o.w[x] = __float_as_uint(v[x]);
+                            }
+                        }
+                        if constexpr (DOT) {
+                            const uint4 yv = shifted16(*reinterpret_cast<const uint4 *>(y + 16 * i),
+                                                       *reinterpret_cast<const uint4 *>(y + 16 * i + 16), ys);
+                            Raw<16> z;
+                            z.w[0] = yv.x; z.w[1] = yv.y; z.w[2] = yv.z; z.w[3] = yv.w;
+#pragma unroll
+                            for (int x = 0; x < NE; ++x)
+                                if (whole || (unsigned)(el + x) < (unsigned)len)
+                                    dot[h] = fmaf(raw_el<B16, 16>(r, x), raw_el<B16, 16>(z, x), dot[h]);
+                        }
+                        if (whole) {
+                            *reinterpret_cast<uint4 *>(d + 16 * i) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < NE; ++x)
+                                if ((unsigned)(el + x) < (unsigned)len) {
+                                    if constexpr (B16) *reinterpret_cast<uint16_t *>(d + 16 * i + 2 * x) = (uint16_t)(o.w[x >> 1] >> (16 * (x & 1)));
+                                    else *reinterpret_cast<uint32_t *>(d + 16 * i + 4 * x) = o.w[x];
+                                }
+                        }
+                    }
+                }
+            }
+            __syncthreads();           // the chunk is read before the next one lands
+        }
+        if constexpr (DOT) {
+#pragma unroll
+            for (int h = 0; h < U / WARPS; ++h) {
+                const int q = at_once * h + warp / share;
+                const float s = warp_sum(dot[h]);
+                if (q < m && lane == 0) part[warp % share][e.j[j0 + q]] = s;
+            }
+        }
+    }
+    if constexpr (DOT) {
+        __syncthreads();
+        if (tid < k) {
+            float s = part[0][tid];
+            for (int i = 1; i < WARPS; ++i) s += part[i][tid];
+            dw[t * lddw + tid] = s;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ launches
 uintptr_t u(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
@@ -693,8 +869,27 @@ int row_chunks(int64_t T, int nvec, int num_sms) {
 // 10.8 and 8.8, 2000 x 1 12.5 and 9.5.
 bool few_entries(int n, int k) { return n <= 1024 || (n <= 2048 && k >= 4); }
 
+template <bool B16, Spread MODE>
+cudaError_t spread_bulk(const CombineGradArgs &a, const CallCtx &c, cudaStream_t stream) {
+    const int b = B16 ? 2 : 4;
+    const char *G = static_cast<const char *>(a.dY), *Ys = static_cast<const char *>(a.Ys);
+    char *out = static_cast<char *>(a.dYs);
+    int64_t ldg = a.lddy * b, ldys = a.ldys * b, ldo = a.lddys * b, ldw = a.ldw, lddw = a.lddw;
+    int rows = a.rows, T = a.T, k = a.k, H = a.H;
+    const int32_t *pos = a.pos;
+    const float *w = a.weights;
+    float *dw = a.dweights;
+    int *status = c.status;
+    uint64_t budget = c.budget_ns;
+    void *args[] = {&G, &ldg, &T, &Ys, &ldys, &rows, &pos, &w, &ldw, &k, &H, &out, &ldo, &dw, &lddw, &status, &budget};
+    const int chunks = MODE == kScaleDot ? 1 : (H + kSpreadBytes / b - 1) / (kSpreadBytes / b);
+    return launch((const void *)spread_bulk_kernel<B16, MODE>, dim3(T, chunks), kSpreadThreads, 0, stream, c.pdl, 1, args);
+}
+
 template <int VB>
-cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, const CallCtx &c, cudaStream_t stream) {
+    const int num_sms = c.num_sms;
+    const bool pdl = c.pdl;
     const char *X = static_cast<const char *>(a.X);
     char *Xs = static_cast<char *>(a.Xs);
     int64_t ldx = a.ldx * a.el_bytes, ldxs = a.ldxs * a.el_bytes, ldid = a.ldid;
@@ -713,6 +908,14 @@ cudaError_t dispatch_vec(const DispatchArgs &a, int nvec, int num_sms, cudaStrea
     cudaError_t e = launch((const void *)expert_sort_kernel, dim3(kSortCluster), 32 * W, 4 * (W + 2) * E, stream, pdl,
                            kSortCluster, args);
     if (e != cudaSuccess || nvec == 0) return e;
+    if constexpr (VB < 8) {
+        // a chunk brought to shared memory pays where it is stored more than a few times.  GB300, us by elements
+        // and this way: 3001 x 6 x 2881 bf16 40 and 33, fp32 63 and 50; 2500 x 3 x 2001 bf16 15.0 and 17.7
+        if (k >= 4) {
+            const CombineGradArgs g{X, a.ldx, nullptr, 0, n, pos, nullptr, 0, T, k, a.H, a.el_bytes == 2, Xs, a.ldxs, nullptr, 0};
+            return g.b16 ? spread_bulk<true, kCopy>(g, c, stream) : spread_bulk<false, kCopy>(g, c, stream);
+        }
+    }
     const int32_t *cpos = pos;
     void *cargs[] = {&cpos, &X, &ldx, &k, &nvec, &Xs, &ldxs};
     return launch((const void *)dispatch_copy_kernel<VB>, dim3(T, row_chunks(T, nvec, num_sms)), kRowThreads, 0,
@@ -806,11 +1009,17 @@ cudaError_t grad_as(const CombineGradArgs &a, int num_sms, cudaStream_t stream, 
                   1, args);
 }
 template <bool B16, bool DW>
-cudaError_t grad_types(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t grad_types(const CombineGradArgs &a, const CallCtx &c, cudaStream_t stream) {
+    const int num_sms = c.num_sms;
+    const bool pdl = c.pdl;
     constexpr int b = B16 ? 2 : 4;
     const uintptr_t all = u(a.dY) | u(a.dYs) | (uintptr_t)(a.lddy * b) | (uintptr_t)(a.lddys * b) |
                           (DW ? u(a.Ys) | (uintptr_t)(a.ldys * b) : 0);
-    switch (vec_bytes((int64_t)a.H * b, b, all)) {
+    const int vb = vec_bytes((int64_t)a.H * b, b, all);
+    // GB300, us by elements and this way: 3001 x 6 x 2881 bf16 250 and 70, fp32 88 and 80; one token x 8 x 501
+    // bf16 5.0 and 8.6, 40 x 8 x 7001 29 and 23
+    if (vb == b && a.T >= (B16 ? 32 : 2 * num_sms)) return spread_bulk<B16, DW ? kScaleDot : kScale>(a, c, stream);
+    switch (vb) {
         case 16: return grad_as<B16, 16, DW>(a, num_sms, stream, pdl);
         case 8: return grad_as<B16, 8, DW>(a, num_sms, stream, pdl);
         case 4: return grad_as<B16, 4, DW>(a, num_sms, stream, pdl);
@@ -822,7 +1031,7 @@ cudaError_t grad_types(const CombineGradArgs &a, int num_sms, cudaStream_t strea
 
 cudaError_t expert_rows_prepare() { return set_max_dyn_smem(&expert_sort_kernel); }
 
-cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
+cudaError_t launch_dispatch(const DispatchArgs &a, const CallCtx &c, cudaStream_t stream) {
     const int64_t row = (int64_t)a.H * a.el_bytes;
     const bool rows = a.X != nullptr && row > 0;
     const int vb = rows ? vec_bytes(row, a.el_bytes,
@@ -830,10 +1039,10 @@ cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t str
                         : 16;
     const int nvec = rows ? (int)(row / vb) : 0;
     switch (vb) {
-        case 16: return dispatch_vec<16>(a, nvec, num_sms, stream, pdl);
-        case 8: return dispatch_vec<8>(a, nvec, num_sms, stream, pdl);
-        case 4: return dispatch_vec<4>(a, nvec, num_sms, stream, pdl);
-        default: return dispatch_vec<2>(a, nvec, num_sms, stream, pdl);
+        case 16: return dispatch_vec<16>(a, nvec, c, stream);
+        case 8: return dispatch_vec<8>(a, nvec, c, stream);
+        case 4: return dispatch_vec<4>(a, nvec, c, stream);
+        default: return dispatch_vec<2>(a, nvec, c, stream);
     }
 }
 
@@ -842,9 +1051,9 @@ cudaError_t launch_combine(const CombineArgs &a, const CallCtx &c, cudaStream_t 
     return a.out16 ? combine_types<false, true>(a, c, stream) : combine_types<false, false>(a, c, stream);
 }
 
-cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl) {
-    if (a.b16) return a.dweights ? grad_types<true, true>(a, num_sms, stream, pdl) : grad_types<true, false>(a, num_sms, stream, pdl);
-    return a.dweights ? grad_types<false, true>(a, num_sms, stream, pdl) : grad_types<false, false>(a, num_sms, stream, pdl);
+cudaError_t launch_combine_grad(const CombineGradArgs &a, const CallCtx &c, cudaStream_t stream) {
+    if (a.b16) return a.dweights ? grad_types<true, true>(a, c, stream) : grad_types<true, false>(a, c, stream);
+    return a.dweights ? grad_types<false, true>(a, c, stream) : grad_types<false, false>(a, c, stream);
 }
 
 }  // namespace skinny

@@ -50,8 +50,8 @@ struct CombineGradArgs {
 };
 
 cudaError_t expert_rows_prepare();
-cudaError_t launch_dispatch(const DispatchArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_dispatch(const DispatchArgs &a, const CallCtx &c, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs &a, const CallCtx &c, cudaStream_t stream);
-cudaError_t launch_combine_grad(const CombineGradArgs &a, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_combine_grad(const CombineGradArgs &a, const CallCtx &c, cudaStream_t stream);
 
 }  // namespace skinny

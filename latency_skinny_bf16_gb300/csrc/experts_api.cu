@@ -79,7 +79,7 @@ skinny_status_t skinny_expert_dispatch(const int32_t *ids, int ldid, const void 
     CallCtx c;
     st = call_context(&c);
     if (st != SKINNY_OK) return st;
-    return launched(launch_dispatch(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
+    return launched(launch_dispatch(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 skinny_status_t skinny_expert_combine(const void *Ys, int ldys, int rows, const int32_t *pos, const float *weights,
@@ -131,7 +131,7 @@ skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, const void 
     if (st != SKINNY_OK) return st;
     const CombineGradArgs a{dY, lddy, Ys, ldys, rows, pos, weights, ldw, T, k, H, dtype == SKINNY_BF16, dYs, lddys,
                             dweights, lddw};
-    return launched(launch_combine_grad(a, c.num_sms, static_cast<cudaStream_t>(stream), c.pdl));
+    return launched(launch_combine_grad(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, const int32_t *offsets,

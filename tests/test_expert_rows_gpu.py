@@ -333,3 +333,82 @@ def test_combine_bounded_wait_reports_and_recovers():
     for _ in range(3):
         assert torch.equal(sk.expert_combine(ys, pos), want)
     assert sk.skinny_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T,k,H,dtype", [(40, 8, 2881, "bf16"), (33, 1, 1, "bf16"), (64, 3, 7, "bf16"), (40, 20, 1017, "bf16"),
+                                         (50, 2, 1016, "bf16"), (700, 2, 2051, "fp32"), (700, 6, 509, "fp32"), (640, 1, 1, "fp32"),
+                                         (640, 9, 34, "fp32")])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (5, 3)])
+def test_combine_grad_rows_of_any_alignment(T, k, H, dtype, pad, offset):
+    """Rows off 8 bytes: whole pieces and their ends; rows no entry names and the gaps between rows stay."""
+    ids, w = ref.routing(T, k, max(40, k), seed=H + k, drop=0.2)
+    pos, _, _ = ref.dispatch(ids, max(40, k))
+    n = int((pos >= 0).sum())
+    pos[pos == n - 1] = T * k - 1             # the last row of all, and one that no entry names
+    ys, dy = matrix(T * k, H, dtype, H + 1, pad=pad, offset=offset), matrix(T, H, dtype, H + 2, pad=pad, offset=offset)
+    pt, wt = torch.from_numpy(pos).cuda(), torch.from_numpy(w).cuda()
+    ld = H + pad
+    buf = torch.full((T * k * ld + offset + 16,), -5.0, dtype=DT[dtype], device="cuda")
+    dys = torch.as_strided(buf, (T * k, H), (ld, 1), offset + 1)
+    _, dw = sk.expert_combine_grad(dy, ys, pt, wt, dys=dys)
+    rys, rw, mag = ref.combine_grad(host(dy), host(ys), pos, w)
+    named = ~np.isnan(rys[:, 0])
+    got = host(dys)
+    assert (got[~named] == -5.0).all()
+    assert (np.abs(got[named] - rys[named]) <= ref.rounded(rys[named], ref.U32 * np.abs(rys[named]), dtype)).all()
+    # a lane adds four pieces of every 2032 bytes, a warp its lanes, four warps theirs
+    el = 2 if dtype == "bf16" else 4
+    chain = 4 * (16 // el) * ((H * el + 2031) // 2032) + 5 + 4
+    chain = max(chain, H // 256 + 1 + 13)
+    assert (np.abs(host(dw) - rw) <= 1.01 * chain * ref.U32 * mag + ref.TINY["fp32"]).all()
+    dys.fill_(-5.0)
+    assert (buf == -5.0).all()
+    # without the weights' gradient the rows are the same
+    sk.expert_combine_grad(dy, ys, pt, wt, dys=dys)
+    want = dys.clone()
+    dys.fill_(-5.0)
+    assert sk.skinny_expert_combine_grad(dy.data_ptr(), dy.stride(0), 0, 0, T * k, pt.data_ptr(), wt.data_ptr(), k, T, k, H,
+                                         sk.SKINNY_BF16 if dtype == "bf16" else sk.SKINNY_F32, dys.data_ptr(), ld, 0, 0,
+                                         torch.cuda.current_stream().cuda_stream) == sk.SKINNY_OK
+    assert torch.equal(dys, want)
+
+
+@pytest.mark.parametrize("H,dtype", [(2047, "bf16"), (1, "bf16"), (9, "bf16"), (1018, "bf16"), (509, "fp32"), (1, "fp32"), (1027, "fp32")])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (5, 3)])
+def test_dispatch_copies_bits_at_any_alignment(H, dtype, pad, offset):
+    """Every pattern of bits, NaN of any payload too, arrives as it is; the gaps between rows stay."""
+    T, k, E = 700, 5, 37
+    ids, _ = ref.routing(T, k, E, seed=H, drop=0.2)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    ld = H + pad
+    g = torch.Generator().manual_seed(H)
+    lo, hi = torch.iinfo(bits).min, torch.iinfo(bits).max
+    x = torch.as_strided(torch.randint(lo, hi, (T * ld + offset + 8,), generator=g, dtype=bits).cuda().view(DT[dtype]), (T, H),
+                         (ld, 1), offset)
+    buf = torch.full((T * k * ld + offset + 16,), 77, dtype=bits, device="cuda")
+    xs = torch.as_strided(buf.view(DT[dtype]), (T * k, H), (ld, 1), offset + 1)
+    _, pos, order, off = sk.expert_dispatch(torch.from_numpy(ids).cuda(), E, x=x, xs=xs)
+    rpos, rorder, roff = ref.dispatch(ids, E)
+    n = int(roff[-1])
+    assert np.array_equal(pos.cpu().numpy(), rpos)
+    assert torch.equal(xs.view(bits)[:n], x.view(bits)[torch.from_numpy(rorder[:n].astype(np.int64)).cuda() // k])
+    xs.view(bits)[:n] = 77
+    assert (buf == 77).all()
+
+
+def test_spread_bounded_wait_reports_and_recovers():
+    T, k, H = 640, 4, 1001                    # more entries than one launch sorts
+    pos = torch.arange(T * k, dtype=torch.int32, device="cuda").reshape(T, k)
+    ids, _ = ref.routing(T, k, 16, seed=1)
+    it = torch.from_numpy(ids).cuda()
+    for dtype in ("bf16", "fp32"):
+        x, ys = matrix(T, H, dtype, 1), matrix(T * k, H, dtype, 2)
+        for call in (lambda: sk.expert_dispatch(it, 16, x=x)[0], lambda: sk.expert_combine_grad(x, ys, pos)[0]):
+            want = call()
+            with sk.options(wait_timeout_us=0):
+                call()
+                torch.cuda.synchronize()
+            assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
+            for _ in range(2):
+                assert torch.equal(call(), want)
+            assert sk.skinny_get_device_status() == 0
