@@ -256,3 +256,9 @@ def test_infinities_of_neighbouring_rows_and_padding(K, ld):
     hit[2] = True
     assert not torch.isfinite(got[hit]).any()
     assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("N,K,act", [(6000, 1001, None), (6008, 1001, "swiglu"), (6007, 1001, None), (9001, 130, None), (9002, 258, "swiglu")])
+def test_long_lines_of_unaligned_rows(N, K, act):
+    """Tens of rows an expert and long lines of odd rows, whose last tiles are in part empty."""
+    run([33, 0, 9, 64, 40], N, K, act, "bf16", seed=N)
