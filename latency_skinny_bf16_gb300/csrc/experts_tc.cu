@@ -399,10 +399,14 @@ bool experts_tc_supported(const ExpertsArgs &a) {
 // 154, 2 rows 218 and 213; 7168 x 2048, 2 rows, unevenly 423 and 503; 32 experts
 // 2048 x 2048, 16 rows 54 and 83; 8 experts 16 rows, 4096 x 1024 (2048 groups)
 // 21 and 24, 2048 x 2048 (1024 groups) 27 and 24; 1 matrix 24576 x 1536, 64 rows
-// (1536 groups) 28 and 50.
+// (1536 groups) 28 and 50.  A tile's fill and its epilogue cost as much as about
+// 256 elements of K: 19 experts, SwiGLU, 1242 x 64, 19 rows each 21.6 and 6.8, 18
+// experts 3392 x 128, 7 rows 12.9 and 7.7, 10 experts 4000 x 192, 5 rows 12.1 and
+// 6.7, 29 experts 6568 x 256, 5 rows 25.7 and 33.3.
 bool experts_tc_faster(const ExpertsArgs &a, int num_sms) {
     const int per = a.swiglu ? 8 : 16;
     const int64_t groups = (int64_t)(a.rows < a.E ? a.rows : a.E) * ((a.N + per - 1) / per), ctas = (int64_t)kCtasPerSm * num_sms;
+    if (a.K <= 192) return false;
     return (a.rows >= 2 * a.E && groups >= kGroups * ctas) || (a.rows >= 8 * a.E && groups >= 5 * ctas);
 }
 
