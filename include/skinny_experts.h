@@ -6,7 +6,10 @@
  * 16-bit patterns, streams as `void*`, every call asynchronous on `stream`,
  * no allocation, no synchronisation (graph-capturable), every argument error
  * found on the host before anything is launched, results bit-identical from
- * run to run.
+ * run to run on buffers that lie alike within 16 bytes (the dot products of
+ * skinny_expert_combine_grad are added in the order of the pieces it stores).
+ * Waits inside the kernels are bounded: one that gives up leaves the output
+ * unwritten and reports SKINNY_ERR_DEVICE_TIMEOUT to skinny_get_device_status.
  *
  * The framework's router gives ids[t][j] (skinny_router_topk).  An entry
  * f = t * k + j is live when 0 <= ids[t][j] < E; any other id (-1, say) drops
