@@ -119,8 +119,11 @@ SKINNY_API skinny_status_t skinny_expert_combine_grad(const void *dY, int lddy, 
  *   1 <= E <= 1024; rows, N, K >= 0 (rows or N 0: no-op; K 0: zeros).
  *
  * With 16-byte aligned rows (pointers, ldx, ldw and ldwe multiples of 8
- * elements) the tcgen05 kernel runs, else a CUDA-core kernel.  Both take any
+ * elements), more than two rows an expert and enough of N and K the tcgen05
+ * kernel runs, else an mma.sync kernel that takes any alignment.  Both take any
  * number of rows for an expert; they are built for decode (up to 64).
+ * SKINNY_OPT_FORCE_BACKEND: SKINNY_BACKEND_TCGEN05 is the first (UNSUPPORTED
+ * where rows are not aligned), SKINNY_BACKEND_DOTPROD the second.
  */
 SKINNY_API skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx, int rows, const int32_t *offsets,
                                                     const uint16_t *W, int ldw, int64_t ldwe, int E, int N, int K,
