@@ -12,11 +12,6 @@ from __future__ import annotations
 
 import ctypes
 
-try:
-    import torch
-except ImportError:      # the C-named functions need none
-    torch = None
-
 import latency_skinny_bf16_gb300 as _sk
 
 SKINNY_BF16 = 0
@@ -116,6 +111,18 @@ def skinny_lora_workspace(M: int, N: int, R: int, out_dtype: int) -> int:
 
 # ---------------------------------------------------------------- tensors
 
+torch = None    # imported by the first call that takes tensors: the C-named functions need none
+
+
+def _import_torch():
+    global torch, _current
+    import torch
+    if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        # the same handle without a Stream object
+        def _current(device):
+            return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _dtype(t, name):
     d = t.dtype
     if d is torch.bfloat16:
@@ -164,11 +171,6 @@ def _current(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-if torch is not None and hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    def _current(device):  # noqa: F811  (the same handle without a Stream object)
-        return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _refused(st, what):
     raise _sk.SkinnyError(st, what)
 
@@ -180,6 +182,8 @@ def expert_dispatch(ids, num_experts, x=None, xs=None, pos=None, order=None, off
     ``offsets[num_experts]`` on are left as they are; None without ``x``),
     ``pos`` int32 [T, k] (-1: dropped), ``order`` int32 [T*k], ``offsets``
     int32 [num_experts + 1].  See ``skinny_expert_dispatch``."""
+    if torch is None:
+        _import_torch()
     if stream is not None:
         with _on(stream, ids.device):
             return expert_dispatch(ids, num_experts, x, xs, pos, order, offsets)
@@ -235,6 +239,8 @@ def expert_combine(ys, pos, weights=None, out=None, stream=None):
     H], ``pos`` int32 [T, k] from :func:`expert_dispatch`, ``weights`` fp32
     [T, k] or None (ones: the gradient of dispatch's copies), ``out`` bf16 or
     fp32 [T, H] (default: as ``ys``).  See ``skinny_expert_combine``."""
+    if torch is None:
+        _import_torch()
     if stream is not None:
         with _on(stream, ys.device):
             return expert_combine(ys, pos, weights, out)
@@ -260,6 +266,8 @@ def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stre
     type of ``dy``; rows no entry names are left as they are) and
     ``dweights[t, j] = <dy[t], ys[pos[t, j]]>`` (fp32; 0 for a dropped entry).
     See ``skinny_expert_combine_grad``."""
+    if torch is None:
+        _import_torch()
     if stream is not None:
         with _on(stream, dy.device):
             return expert_combine_grad(dy, ys, pos, weights, dys, dweights)
@@ -308,6 +316,8 @@ def experts_gemm(xs, offsets, w, out=None, activation=None, stream=None):
     times the up product.  ``out`` bf16 or fp32 [rows, N] (default bf16); rows
     from ``offsets[E]`` on are left as they are.  See
     ``skinny_experts_gemm_bf16``."""
+    if torch is None:
+        _import_torch()
     if stream is not None:
         with _on(stream, xs.device):
             return experts_gemm(xs, offsets, w, out, activation)
@@ -335,6 +345,8 @@ def experts_gemm(xs, offsets, w, out=None, activation=None, stream=None):
 
 def lora_workspace(M, N, R, out_dtype):
     """Bytes of workspace of :func:`lora_gemm` for an ``out`` of ``out_dtype``."""
+    if torch is None:
+        _import_torch()
     return skinny_lora_workspace(M, N, R, SKINNY_BF16 if out_dtype == torch.bfloat16 else SKINNY_F32)
 
 
@@ -345,6 +357,8 @@ def lora_gemm(x, w, a, b, adapters, ranks=None, scales=None, out=None, workspace
     [L, R, K], ``b`` bf16 [L, N, R], ``ranks`` int32 [L] (what lies past an
     adapter's rank is not used), ``scales`` fp32 [L], ``out`` fp32 (default)
     or bf16 [M, N].  See ``skinny_lora_gemm_bf16``."""
+    if torch is None:
+        _import_torch()
     if stream is not None:
         with _on(stream, x.device):
             return lora_gemm(x, w, a, b, adapters, ranks, scales, out, workspace)
