@@ -284,6 +284,15 @@ class options:
 
 # ---------------------------------------------------------------- tensor convenience
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fits_int(name, *values):
+    """The C ABI's sizes and row strides are ints, and ctypes cuts a larger one to its low 32 bits without a word."""
+    if max(values) > _INT_MAX:
+        raise ValueError(f"{name}: a size or row stride of {max(values)} elements is past {_INT_MAX}")
+
+
 def gemm(x, w, out=None, stream=None):
     """``out[:M, :N] = x . w^T`` for CUDA tensors: x bf16 [M, K], w bf16 [N, K]
     (unit stride along K), out fp32 or bf16 [M, N] (any row stride >= N, unit
@@ -311,6 +320,8 @@ def gemm(x, w, out=None, stream=None):
     ldx = x.stride(0) if M > 1 else max(K, 1)
     ldw = w.stride(0) if N > 1 else max(K, 1)
     ldy = out.stride(0) if M > 1 else max(N, 1)
+    if (M | N | K | ldx | ldw | ldy) >> 31:
+        _fits_int("gemm", M, N, K, ldx, ldw, ldy)
     if w.dtype == torch.float32:
         if out.dtype != torch.float32:
             raise TypeError("fp32 weights give an fp32 output")
@@ -341,9 +352,12 @@ def router_topk(logits, k, renormalize=False, weights=None, ids=None, stream=Non
         stream = torch.cuda.current_stream(logits.device)
     s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     ldl = logits.stride(0) if M > 1 else max(N, 1)
-    st = skinny_router_topk(logits.data_ptr(), ldl, M, N, k, 1 if renormalize else 0,
-                            weights.data_ptr(), weights.stride(0) if M > 1 else max(k, 1),
-                            ids.data_ptr(), ids.stride(0) if M > 1 else max(k, 1), s)
+    ldwt = weights.stride(0) if M > 1 else max(k, 1)
+    ldid = ids.stride(0) if M > 1 else max(k, 1)
+    if (M | N | k | ldl | ldwt | ldid) >> 31:
+        _fits_int("router_topk", M, N, k, ldl, ldwt, ldid)
+    st = skinny_router_topk(logits.data_ptr(), ldl, M, N, k, 1 if renormalize else 0, weights.data_ptr(), ldwt,
+                            ids.data_ptr(), ldid, s)
     if st != SKINNY_OK:
         raise SkinnyError(st, "skinny_router_topk")
     return weights, ids
@@ -365,10 +379,12 @@ def rmsnorm_gemm(x, gamma, eps, w, out=None, xn=None, stream=None):
     if stream is None:
         stream = torch.cuda.current_stream(x.device)
     s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    st = skinny_rmsnorm_gemm_bf16(x.data_ptr(), x.stride(0) if M > 1 else max(K, 1), gamma.data_ptr(), eps,
-                                  xn.data_ptr(), xn.stride(0) if M > 1 else max(K, 1),
-                                  w.data_ptr(), w.stride(0) if N > 1 else max(K, 1),
-                                  out.data_ptr(), out.stride(0) if M > 1 else max(N, 1), M, N, K, s)
+    ldx, ldxn, ldy = ((x.stride(0), xn.stride(0), out.stride(0)) if M > 1 else (max(K, 1), max(K, 1), max(N, 1)))
+    ldw = w.stride(0) if N > 1 else max(K, 1)
+    if (M | N | K | ldx | ldxn | ldw | ldy) >> 31:
+        _fits_int("rmsnorm_gemm", M, N, K, ldx, ldxn, ldw, ldy)
+    st = skinny_rmsnorm_gemm_bf16(x.data_ptr(), ldx, gamma.data_ptr(), eps, xn.data_ptr(), ldxn, w.data_ptr(), ldw,
+                                  out.data_ptr(), ldy, M, N, K, s)
     if st != SKINNY_OK:
         raise SkinnyError(st, "skinny_rmsnorm_gemm_bf16")
     return out, xn

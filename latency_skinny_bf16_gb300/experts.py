@@ -32,6 +32,7 @@ __all__ = [
     "expert_dispatch", "expert_combine", "expert_combine_grad", "experts_gemm", "lora_gemm", "lora_workspace",
 ]
 
+_fits_int = _sk._fits_int
 _ACTS = {"none": SKINNY_ACT_NONE, None: SKINNY_ACT_NONE, "swiglu": SKINNY_ACT_SWIGLU}
 
 SYMBOLS = ("skinny_expert_dispatch", "skinny_expert_combine", "skinny_expert_combine_grad", "skinny_experts_gemm_bf16",
@@ -143,9 +144,11 @@ def _rows(t, name, dtype=None):
     if n > 1 and one != 1:
         raise ValueError(f"{name} needs unit column stride")
     if m <= 1:
-        return m, n, n or 1
-    if ld < n:
+        ld = n or 1
+    elif ld < n:
         raise ValueError(f"{name} needs rows that do not overlap")
+    if (m | ld) >> 31:          # n <= ld
+        _fits_int(name, m, ld)
     return m, n, ld
 
 
@@ -188,6 +191,8 @@ def expert_dispatch(ids, num_experts, x=None, xs=None, pos=None, order=None, off
         with _on(stream, ids.device):
             return expert_dispatch(ids, num_experts, x, xs, pos, order, offsets)
     T, k, ldid = _rows(ids, "ids", torch.int32)
+    if num_experts >> 31:
+        _fits_int("num_experts", num_experts)
     n, dev = T * k, ids.device
     if pos is None:
         pos = torch.empty((T, k), dtype=torch.int32, device=dev)
@@ -230,6 +235,8 @@ def _pos(pos):
     if pos.dim() != 2:
         raise ValueError(f"pos must be [T, k], not {tuple(pos.shape)}")
     T, k = pos.shape
+    if (T | k) >> 31:
+        _fits_int("pos", T, k)
     return T, k, _flat(pos, "pos", T * k, torch.int32)
 
 
@@ -305,6 +312,8 @@ def _stack(t, name, rows, cols):
         raise ValueError(f"{name} needs unit stride along its last dimension")
     if r <= 1:
         ld = c or 1
+    if (n | r | ld) >> 31:
+        _fits_int(name, n, r, ld)
     return ld, lde if n > 1 else (r or 1) * ld
 
 
@@ -347,6 +356,7 @@ def lora_workspace(M, N, R, out_dtype):
     """Bytes of workspace of :func:`lora_gemm` for an ``out`` of ``out_dtype``."""
     if torch is None:
         _import_torch()
+    _fits_int("M, N and R", M, N, R)
     return skinny_lora_workspace(M, N, R, SKINNY_BF16 if out_dtype == torch.bfloat16 else SKINNY_F32)
 
 
