@@ -8,8 +8,11 @@
  * found on the host before anything is launched, results bit-identical from
  * run to run on buffers that lie alike within 16 bytes (the dot products of
  * skinny_expert_combine_grad are added in the order of the pieces it stores).
- * Waits inside the kernels are bounded: one that gives up leaves the output
- * unwritten and reports SKINNY_ERR_DEVICE_TIMEOUT to skinny_get_device_status.
+ * Waits inside the kernels are bounded: one that gives up reports
+ * SKINNY_ERR_DEVICE_TIMEOUT to skinny_get_device_status.  What its call was to
+ * write is then not a result: parts may be written, parts be left as they
+ * were, and skinny_lora_gemm_bf16 adds the adapters to what its projection has
+ * left.  Nothing else is written, and later calls are not affected.
  *
  * The framework's router gives ids[t][j] (skinny_router_topk).  An entry
  * f = t * k + j is live when 0 <= ids[t][j] < E; any other id (-1, say) drops

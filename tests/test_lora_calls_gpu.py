@@ -1,0 +1,64 @@
+"""The three kernels of a projection with adapters as one call: what follows a
+projection that gave up, and calls one behind the other."""
+import numpy as np
+import pytest
+import torch
+
+import latency_skinny_bf16_gb300 as sk
+from test_experts_gemm_gpu import DT
+from test_lora_gpu import check, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _init():
+    assert sk.skinny_init(0) == sk.SKINNY_OK
+    yield
+    assert sk.skinny_get_device_status() == 0
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M", [1, 16, 40])
+@pytest.mark.parametrize("backend", [sk.SKINNY_BACKEND_TCGEN05, sk.SKINNY_BACKEND_AUTO])
+def test_projection_that_gives_up(M, out, backend):
+    """Without any budget the projection's waits give up, and the two kernels behind it run all the same: the status
+    says so, only Y is written, and the calls after it, eager and captured, are right."""
+    N = 640
+    x, w, a, b, ranks, scales = inputs(M, N, 1024, 6, 32, seed=M)
+    ids = np.random.default_rng(M).integers(-1, 6, M).astype(np.int32)
+    dev = [torch.from_numpy(v).cuda() for v in (ids, ranks, scales)]
+    nbytes = sk.lora_workspace(M, N, 32, DT[out])
+    ws = torch.full((nbytes + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    with sk.options(backend=backend):
+        want = check(x, w, a, b, ids, ranks, scales, out)
+        y = torch.full((M, N + 5), -7.0, dtype=DT[out], device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+
+        def call():
+            sk.lora_gemm(x, w, a, b, *dev, out=y[:, :N], workspace=ws[:nbytes])
+
+        def captured():
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                call()
+            return g
+
+        good = captured()
+        for pdl in (0, 1):
+            with sk.options(wait_timeout_us=0, pdl=pdl):
+                bad = captured()
+                for run in (call, bad.replay, bad.replay):
+                    run()
+                    torch.cuda.synchronize()
+                    assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
+                    assert (y[:, N:] == -7.0).all() and (ws[nbytes:] == 0x5A).all()
+                    with sk.options(wait_timeout_us=500000):
+                        for again in (call, good.replay):
+                            y[:, :N] = float("nan")
+                            again()
+                            assert torch.equal(y[:, :N], want)
+                    assert sk.skinny_get_device_status() == 0
+                del bad
+        del good
