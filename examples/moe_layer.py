@@ -134,6 +134,10 @@ def main(argv=None):
         with torch.cuda.graph(graph, stream=s):
             layer.step(x, adapter_ids)
     y0 = y.clone()
+    for t in (layer.h, layer.logits, layer.weights, layer.hs, layer.act, layer.d, layer.out):
+        t.fill_(float("nan"))                          # nothing of the eager step is left to the captured one
+    for t in (layer.ids, layer.pos, layer.order, layer.offsets):
+        t.fill_(-1)
     graph.replay()
     torch.cuda.synchronize()
     if not torch.equal(layer.out, y0):

@@ -62,3 +62,39 @@ def test_projection_that_gives_up(M, out, backend):
                     assert sk.skinny_get_device_status() == 0
                 del bad
         del good
+
+
+@pytest.mark.parametrize("pdl", [0, 1, 2])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(16, 640, 1024), (3, 200, 777), (64, 2048, 512), (1, 2112, 7168)])
+def test_calls_one_behind_the_other(M, N, K, out, pdl):
+    """Calls with inputs, ids and outputs of their own share one workspace: what a call writes there must not reach the
+    one before it, nor what that left the call itself. Buffers are filled before every replay."""
+    calls = []
+    for s in range(4):
+        x, w, a, b, ranks, scales = inputs(M, N, K, 5, 48, seed=10 * s + M)
+        ids = np.random.default_rng(s).integers(-1, 5, M).astype(np.int32)
+        want = check(x, w, a, b, ids, ranks, scales, out)
+        calls.append((x, w, a, b, *[torch.from_numpy(v).cuda() for v in (ids, ranks, scales)], torch.empty_like(want), want))
+    ws = torch.empty(sk.lora_workspace(M, N, 48, DT[out]), dtype=torch.uint8, device="cuda")
+
+    def all_calls():
+        for _ in range(2):
+            for c in calls:
+                sk.lora_gemm(*c[:7], out=c[7], workspace=ws)
+
+    with sk.options(pdl=pdl):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            all_calls()
+        for run in (all_calls, g.replay, g.replay):
+            ws.fill_(0xFF)
+            for c in calls:
+                c[7].fill_(float("nan"))
+            run()
+            torch.cuda.synchronize()
+            for c in calls:
+                assert torch.equal(c[7], c[8])
+        del g
