@@ -142,7 +142,8 @@ SKINNY_API skinny_status_t skinny_experts_gemm_bf16(const uint16_t *Xs, int ldx,
  * in fp32; Y is rounded once to out_dtype.  What A and B hold past r_a is not
  * used.  ranks are clamped to [0, R]; scales == NULL takes 1.
  *
- *   X, W     as in skinny_gemm_bf16 (M <= 64, and its rules for M > 16)
+ *   X, W     as in skinny_gemm_bf16, M <= 64; 16-byte aligned rows (pointers, ldx and ldw multiples of 8
+ *            elements) give its results, and rows of any other alignment are taken for every M
  *   A        device, bf16 [L, R, K], row stride lda >= K, adapter stride ldae
  *   B        device, bf16 [L, N, R], row stride ldb >= R, adapter stride ldbe
  *   adapters device, int32 [M];  ranks device, int32 [L] or NULL;  scales device, fp32 [L] or NULL

@@ -98,3 +98,13 @@ def test_calls_one_behind_the_other(M, N, K, out, pdl):
             for c in calls:
                 assert torch.equal(c[7], c[8])
         del g
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M", [17, 33, 64])
+@pytest.mark.parametrize("K,pad,offset", [(777, 0, 0), (520, 0, 1), (520, 3, 5), (130, 2, 2), (1001, 7, 4)])
+def test_many_tokens_unaligned(M, K, pad, offset, out):
+    """Rows off 16 bytes are served at every number of tokens, several of them to an adapter."""
+    x, w, a, b, ranks, scales = inputs(M, 333, K, 7, 40, seed=M + K, pad=pad, offset=offset)
+    ids = np.random.default_rng(M).integers(-1, 7, M).astype(np.int32)
+    check(x, w, a, b, ids, ranks, scales, out, ypad=1)
