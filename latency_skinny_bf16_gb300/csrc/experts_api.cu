@@ -184,7 +184,22 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
     const int ob = out_dtype == SKINNY_BF16;
     const bool none = L == 0 || R == 0 || M <= 0 || N <= 0 || K <= 0;
     skinny_status_t st = SKINNY_OK;
-    if (none) return run_gemm(X, ldx, W, ldw, Y, ldy, M, N, K, stream, ob);
+    // The projection: skinny_gemm_bf16 where its rows are 16-byte aligned; else the experts' mma.sync
+    // kernel on the one matrix, which reads whole 16-byte pieces at any alignment and takes every M.  GB300,
+    // us, skinny_gemm_bf16 and this kernel: 896 x 2645, 1, 2, 8 and 16 tokens 10.7 and 11.1, 14.0 and 11.6,
+    // 58.9 and 11.1, 102 and 15.3; 15936 x 4083, 1 and 8 tokens 107 and 38, 1500 and 40; short and long the
+    // other way round for few tokens, 512 x 7169, 1, 2 and 4 tokens 12.0 and 21.9, 17.6 and 22.9, 53 and 23.
+    const bool rows16 = ((addr(X) | addr(W)) % 16 | (ldx | ldw) % 8) == 0;
+    if (none) {
+        st = run_gemm(X, ldx, W, ldw, Y, ldy, M, N, K, stream, ob);
+        // what it refuses of checked arguments: unaligned rows with more than 16 tokens
+        if (st != SKINNY_ERR_UNSUPPORTED || M > SKINNY_MAX_M || rows16) return st;
+        CallCtx c;
+        st = call_context(&c);
+        if (st != SKINNY_OK) return st;
+        const ExpertsArgs b{X, ldx, M, nullptr, W, ldw, (int64_t)N * ldw, 1, N, K, 0, ob, Y, ldy};
+        return launched(launch_experts_mma(b, c, static_cast<cudaStream_t>(stream)));
+    }
     if (M > SKINNY_MAX_M) return SKINNY_ERR_UNSUPPORTED;
     if (!Y || ldy < N || !A || !B || !adapters || !workspace || lda < K || ldb < R ||
         (L > 1 && (ldae < (int64_t)R * lda || ldbe < (int64_t)N * ldb)) ||
@@ -205,12 +220,6 @@ skinny_status_t skinny_lora_gemm_bf16(const uint16_t *X, int ldx, const uint16_t
         return SKINNY_ERR_INVALID_VALUE;
     if (!X || !W || ldx < K || ldw < K) return SKINNY_ERR_INVALID_VALUE;
     if (!aligned(X, 2) || !aligned(W, 2)) return SKINNY_ERR_MISALIGNED;
-    // The projection: skinny_gemm_bf16 where its rows are 16-byte aligned; else the experts' mma.sync
-    // kernel on the one matrix, which reads whole 16-byte pieces at any alignment and takes every M.  GB300,
-    // us, skinny_gemm_bf16 and this kernel: 896 x 2645, 1, 2, 8 and 16 tokens 10.7 and 11.1, 14.0 and 11.6,
-    // 58.9 and 11.1, 102 and 15.3; 15936 x 4083, 1 and 8 tokens 107 and 38, 1500 and 40; short and long the
-    // other way round for few tokens, 512 x 7169, 1, 2 and 4 tokens 12.0 and 21.9, 17.6 and 22.9, 53 and 23.
-    const bool rows16 = ((addr(X) | addr(W)) % 16 | (ldx | ldw) % 8) == 0;
     if (rows16) {
         st = check_gemm(X, ldx, W, ldw, base, ldbase, M, N, K, 0);
         if (st != SKINNY_OK) return st;

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import experts_ref as ref
 import latency_skinny_bf16_gb300 as sk
-from test_experts_gemm_gpu import DT
+from test_experts_gemm_gpu import DT, host
 from test_lora_gpu import check, inputs
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +109,17 @@ def test_many_tokens_unaligned(M, K, pad, offset, out):
     x, w, a, b, ranks, scales = inputs(M, 333, K, 7, 40, seed=M + K, pad=pad, offset=offset)
     ids = np.random.default_rng(M).integers(-1, 7, M).astype(np.int32)
     check(x, w, a, b, ids, ranks, scales, out, ypad=1)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("L,R", [(0, 8), (4, 0)])
+@pytest.mark.parametrize("M,K,pad,offset", [(17, 777, 0, 0), (64, 520, 0, 1), (40, 520, 3, 5), (16, 777, 0, 0), (40, 520, 0, 0)])
+def test_no_adapters_at_any_alignment(M, K, pad, offset, L, R, out):
+    """The projection alone takes what the call with adapters takes."""
+    x, w, *_ = inputs(M, 333, K, 1, 8, seed=M + K, pad=pad, offset=offset)
+    a, b = torch.zeros((L, R, K), dtype=torch.bfloat16, device="cuda"), torch.zeros((L, 333, R), dtype=torch.bfloat16, device="cuda")
+    y = sk.lora_gemm(x, w, a, b, torch.zeros(M, dtype=torch.int32, device="cuda"),
+                     out=torch.full((M, 334), -7.0, dtype=DT[out], device="cuda")[:, :333])
+    want = host(x) @ host(w).T
+    err = 1e-5 * (np.abs(host(x)) @ np.abs(host(w)).T)
+    assert (np.abs(host(y) - want) <= ref.rounded(want, err, out) + 1e-6).all()
