@@ -267,17 +267,19 @@ def expert_combine(ys, pos, weights=None, out=None, stream=None):
     return out
 
 
-def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stream=None):
+def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stream=None, weight_grad=True):
     """The gradient of :func:`expert_combine` for ``dy`` [T, H]: returns
     ``(dys, dweights)`` with ``dys[pos[t, j]] = weights[t, j] * dy[t]`` (the
     type of ``dy``; rows no entry names are left as they are) and
     ``dweights[t, j] = <dy[t], ys[pos[t, j]]>`` (fp32; 0 for a dropped entry).
-    See ``skinny_expert_combine_grad``."""
+    ``weight_grad=False`` (a router that is not trained) leaves dweights out
+    and reads nothing of ``ys``, which then only gives the number of rows.  See
+    ``skinny_expert_combine_grad``."""
     if torch is None:
         _import_torch()
     if stream is not None:
         with _on(stream, dy.device):
-            return expert_combine_grad(dy, ys, pos, weights, dys, dweights)
+            return expert_combine_grad(dy, ys, pos, weights, dys, dweights, None, weight_grad)
     T, H, lddy = _rows(dy, "dy")
     dt = _dtype(dy, "dy")
     rows, ycols, ldys = _rows(ys, "ys", dy.dtype)
@@ -287,14 +289,19 @@ def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stre
     wp, ldw = _weights(weights, T, k)
     if dys is None:
         dys = torch.empty((rows, H), dtype=dy.dtype, device=dy.device)
-    if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     grows, gcols, lddys = _rows(dys, "dys", dy.dtype)
-    wrows, wcols, lddw = _rows(dweights, "dweights", torch.float32)
+    dwp, wrows, wcols, lddw = 0, T, k, 0
+    if weight_grad:
+        if dweights is None:
+            dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        wrows, wcols, lddw = _rows(dweights, "dweights", torch.float32)
+        dwp = dweights.data_ptr()
+    elif dweights is not None:
+        raise ValueError("dweights is given, and weight_grad is False")
     if grows != rows or gcols != H or wrows != T or wcols != k:
         raise ValueError(f"dys must be {(rows, H)} and dweights {(T, k)}")
     st = _lib().skinny_expert_combine_grad(dy.data_ptr(), lddy, ys.data_ptr(), ldys, rows, pp, wp, ldw, T, k, H, dt,
-                                           dys.data_ptr(), lddys, dweights.data_ptr(), lddw, _current(dy.device))
+                                           dys.data_ptr(), lddys, dwp, lddw, _current(dy.device))
     if st:
         _refused(st, "skinny_expert_combine_grad")
     return dys, dweights
