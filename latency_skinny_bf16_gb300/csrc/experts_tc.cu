@@ -86,6 +86,11 @@ int smem_bytes(int E) {
     if (tail < 12 * 1024) tail = 12 * 1024;
     return 1024 + kStages * kStage + tail;             // 110 KB: two CTAs on an SM, as tensor memory holds
 }
+// Tensor memory is allocated behind griddep_wait, when CTAs of the next kernel may be on the SM and hold theirs.  An
+// SM always has columns for its CTAs, since those of every kernel that takes some (here and tmem_gemm.cu) take 256 and
+// ask for so much shared memory that no three fit (with the 1 KB that each CTA is charged beside it).
+static_assert(1024 + kStages * kStage + 12 * 1024 >= kTcMinSmem && 3 * (kTcMinSmem + 1024) > 228 * 1024,
+              "at most two CTAs with tensor memory on an SM");
 
 // Groups [g, g + ng) of expert e.
 struct Tile {
