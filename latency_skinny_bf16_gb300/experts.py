@@ -135,11 +135,12 @@ def _dtype(t, name):
 
 def _rows(t, name, dtype=None):
     """(rows, columns, row stride) of a CUDA matrix with unit column stride."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA matrix, not {tuple(t.shape)} on {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA matrix, not {tuple(shape)} on {t.device}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    m, n = t.shape
+    m, n = shape
     ld, one = t.stride()
     if n > 1 and one != 1:
         raise ValueError(f"{name} needs unit column stride")
@@ -232,9 +233,10 @@ def _weights(weights, T, k):
 
 
 def _pos(pos):
-    if pos.dim() != 2:
-        raise ValueError(f"pos must be [T, k], not {tuple(pos.shape)}")
-    T, k = pos.shape
+    shape = pos.shape
+    if len(shape) != 2:
+        raise ValueError(f"pos must be [T, k], not {tuple(shape)}")
+    T, k = shape
     if (T | k) >> 31:
         _fits_int("pos", T, k)
     return T, k, _flat(pos, "pos", T * k, torch.int32)
@@ -309,9 +311,10 @@ def expert_combine_grad(dy, ys, pos, weights=None, dys=None, dweights=None, stre
 
 def _stack(t, name, rows, cols):
     """(row stride, matrix stride) of a CUDA bf16 stack of matrices [n, rows, cols]."""
-    if t.dim() != 3 or not t.is_cuda or t.dtype is not torch.bfloat16:
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda or t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor of three dimensions")
-    n, r, c = t.shape
+    n, r, c = shape
     if r != rows or c != cols:
         raise ValueError(f"{name} must hold {rows} x {cols} matrices, not {r} x {c}")
     lde, ld, one = t.stride()
