@@ -27,7 +27,7 @@
 //     as many rows behind them; at its end the ups go through shared memory to
 //     the gates' threads.
 // Every wait is bounded.  A wait that gives up records an error and the CTA
-// winds down without storing: copies in flight and issued MMAs are waited for
+// winds down, storing no tile from there on: copies in flight and issued MMAs are waited for
 // (bounded) and the draining warps still meet at every barrier.
 #include <cuda.h>
 #include <type_traits>
