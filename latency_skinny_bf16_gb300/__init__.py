@@ -134,6 +134,7 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.skinny_version.argtypes = []
     lib.skinny_version.restype = i
     experts.bind(lib)
+    layer.bind(lib)
     return lib
 
 
@@ -390,8 +391,9 @@ def rmsnorm_gemm(x, gamma, eps, w, out=None, xn=None, stream=None):
     return out, xn
 
 
-from . import experts  # noqa: E402  (its functions call back into this module)
+from . import experts, layer  # noqa: E402  (their functions call back into this module)
 from .experts import *  # noqa: E402,F401,F403
+from .layer import *  # noqa: E402,F401,F403
 
-__all__ += experts.__all__
-EXPORTED_SYMBOLS += experts.SYMBOLS
+__all__ += experts.__all__ + layer.__all__
+EXPORTED_SYMBOLS += experts.SYMBOLS + layer.SYMBOLS

@@ -1,0 +1,78 @@
+// layer.h -- host-side declarations of a dense layer's operators: products with
+// an epilogue and their gradients, heads' norms with rotation and theirs.
+#pragma once
+
+#include "calls.h"
+#include "skinny_layer.h"
+
+namespace skinny {
+
+// An operand of a product over a depth c: element (i, c) at p[i * ld + c], or,
+// crossed, at p[c * ld + i].
+struct Operand {
+    const uint16_t *p;
+    int64_t ld;
+    bool crossed;
+};
+
+// Y[r][n] = epilogue(sum_c B(r, c) A(n, c)), r < rows, n < cols.  A gated
+// activation takes A(cols + n, c) beside it.
+struct ProductArgs {
+    Operand A, B;
+    int64_t rows;
+    int cols, depth;
+    int act;
+    const uint16_t *bias;    // NULL: none
+    const void *R;           // out's type; NULL: none
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+    uint16_t *Z;             // NULL: not kept
+    int64_t ldz;
+    int out_bf16;
+};
+cudaError_t launch_product_any(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
+
+// dZ (bf16, row stride lddz) and, into `partial` [parts][rows of W], the sums of dZ over the tokens of a part
+struct LinearDzArgs {
+    const uint16_t *dY;
+    int64_t lddy;
+    const uint16_t *Z;
+    int64_t ldz;
+    uint16_t *dZ;            // NULL: sums only
+    int64_t lddz;
+    float *dbias;            // NULL: not computed
+    float *partial;          // kDbiasParts rows
+    int64_t M;
+    int N, act;
+};
+constexpr int kDbiasParts = 64;
+cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream_t stream);
+
+// Heads of queries (side 0) and keys (side 1).
+struct HeadsSide {
+    const void *x;
+    int64_t st, sh;
+    const void *w;
+    const void *d;           // gradients: of the outputs
+    int64_t dst, dsh;
+    void *y;                 // outputs; gradients: of the inputs
+    int64_t yst, ysh;
+    float *dw;               // gradients of the weights, or NULL
+    int H;
+};
+struct HeadsArgs {
+    HeadsSide side[2];
+    const float *table;
+    int64_t P;
+    const int32_t *positions, *pair_axis;
+    int axes, R, interleaved;
+    int T, D, norm;
+    float eps;
+    bool b16, grad;
+    float *partial;          // gradients of the weights: [parts][2][D]
+};
+constexpr int kHeadsParts = 608;
+cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stream);
+
+}  // namespace skinny
