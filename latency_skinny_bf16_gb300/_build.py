@@ -22,9 +22,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "dotprod.cu", "dotprod_f32w.cu", "dotmma.cu", "dotmma_f32w.cu", "splitk.cu", "stream.cu",
            "topk.cu", "rmsnorm.cu", "tmem_gemm.cu", "expert_rows.cu", "experts_api.cu",
-           "experts_mma.cu", "experts_tc.cu", "lora.cu", "layer_api.cu", "linear_any.cu", "linear_dz.cu", "heads.cu"]
+           "experts_mma.cu", "experts_tc.cu", "lora.cu", "layer_api.cu", "linear_any.cu", "linear_dz.cu", "linear_tc.cu", "rows_pack.cu", "heads.cu"]
 HEADERS = ["common.cuh", "internal.h", "tuning_table.inc", "tma.cuh", "dotmma_f32w.h", "expert_rows.h", "experts_gemm.h",
-           "mma_rows.cuh", "tcgen05.cuh", "tma_stack.cuh", "calls.h", "ranges.h", "layer.h", "act.cuh"]
+           "mma_rows.cuh", "tcgen05.cuh", "tma_stack.cuh", "calls.h", "ranges.h", "layer.h", "act.cuh", "product.cuh"]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -169,13 +169,14 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                 }
             }
             for (int b = b0; b < b1; b += kAhead) {
-                Piece<E, V> x[kAhead][NC][2], d[GRAD ? kAhead : 1][NC][2];
+                Piece<E, V> x[kAhead][NC][2];
+                [[maybe_unused]] Piece<E, V> d[GRAD ? kAhead : 1][NC][2];
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q) {
                     const int h = (b + q) * HP + hs;
                     const bool live = b + q < b1 && h < s.H;
                     const E *xp = static_cast<const E *>(s.x) + (int64_t)t * s.st + (int64_t)h * s.sh;
-                    const E *dp = static_cast<const E *>(s.d) + (int64_t)t * s.dst + (int64_t)h * s.dsh;
+                    [[maybe_unused]] const E *dp = static_cast<const E *>(s.d) + (int64_t)t * s.dst + (int64_t)h * s.dsh;
 #pragma unroll
                     for (int j = 0; j < NC; ++j) {
                         x[q][j][0].zero();

@@ -30,8 +30,24 @@ struct ProductArgs {
     uint16_t *Z;             // NULL: not kept
     int64_t ldz;
     int out_bf16;
+    bool early;              // A is a weight that no preceding kernel of the stream writes
 };
+// CUDA cores, operands of any strides and alignment (linear_any.cu)
 cudaError_t launch_product_any(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
+
+// tcgen05 (linear_tc.cu): 16-byte aligned rows, a depth of 1 at least
+bool linear_tc_supported(const ProductArgs &a);
+cudaError_t linear_tc_prepare();
+cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
+
+// Rows laid out from `to` on, whole 16-byte pieces each; from NULL: none.
+struct PackArgs {
+    const uint16_t *from;
+    int64_t ldfrom, rows;
+    int cols;
+    uint16_t *to;
+};
+cudaError_t launch_rows_pack(const PackArgs &a, const PackArgs &b, const CallCtx &c, cudaStream_t stream);
 
 // dZ (bf16, row stride lddz) and, into `partial` [parts][rows of W], the sums of dZ over the tokens of a part
 struct LinearDzArgs {

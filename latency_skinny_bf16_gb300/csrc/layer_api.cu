@@ -18,16 +18,33 @@ skinny_status_t check_product(int M, int N, int K, int act) {
     return SKINNY_OK;
 }
 
-// Where the pieces of a backward pass lie in its workspace.
-struct GradSpace {
-    int64_t dz, partial, bytes;
+bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+constexpr int kPackedM = 64;      // rows above which unaligned operands are laid out first
+
+// Where the pieces of a call lie in its workspace (-1: not used).
+struct Space {
+    int64_t x = -1, w = -1, dz = -1, partial = -1, bytes = 0;
+    int64_t take(int64_t n) {
+        const int64_t at = bytes;
+        bytes += pad16(n);
+        return at;
+    }
 };
-GradSpace grad_space(int M, int rows, int act) {
-    GradSpace g{};
-    g.dz = 0;
-    g.partial = act == SKINNY_ACT_NONE ? 0 : pad16((int64_t)M * pad8(rows) * 2);
-    g.bytes = g.partial + (int64_t)kDbiasParts * rows * 4;
-    return g;
+Space linear_space(const void *X, int ldx, const void *W, int ldw, int M, int K, int rows) {
+    Space s;
+    if (M <= kPackedM || K == 0) return s;
+    if (!rows16(X, ldx)) s.x = s.take((int64_t)M * pad8(K) * 2);
+    if (!rows16(W, ldw)) s.w = s.take((int64_t)rows * pad8(K) * 2);
+    return s;
+}
+// dZ (or dY on 16-byte boundaries), X and W likewise, the parts of the bias gradient
+Space grad_space(const void *dY, int lddy, const void *X, int ldx, const void *W, int ldw, int M, int K, int rows, int act) {
+    Space s;
+    if (act != SKINNY_ACT_NONE || !rows16(dY, lddy)) s.dz = s.take((int64_t)M * pad8(rows) * 2);
+    if (!rows16(X, ldx)) s.x = s.take((int64_t)M * pad8(K) * 2);
+    if (!rows16(W, ldw)) s.w = s.take((int64_t)rows * pad8(K) * 2);
+    s.partial = s.take((int64_t)kDbiasParts * rows * 4);
+    return s;
 }
 
 // [T, H] rows of D elements, strides st and sh.
@@ -109,8 +126,8 @@ using namespace skinny;
 extern "C" {
 
 int64_t skinny_linear_workspace(const uint16_t *X, int ldx, const uint16_t *W, int ldw, int M, int N, int K, int act) {
-    (void)X; (void)ldx; (void)W; (void)ldw; (void)M; (void)N; (void)K; (void)act;
-    return 0;
+    if (check_product(M, N, K, act) != SKINNY_OK || M == 0 || N == 0) return 0;
+    return linear_space(X, ldx, W, ldw, M, K, act_gated(act) ? 2 * N : N).bytes;
 }
 
 skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W, int ldw, const uint16_t *bias,
@@ -138,16 +155,31 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
     CallCtx c;
     st = call_context(&c);
     if (st != SKINNY_OK) return st;
-    const ProductArgs a{{W, ldw, false}, {X, ldx, false}, M, N, K, act, bias, R, ldr, Y, ldy, Z, ldz,
-                        out_dtype == SKINNY_BF16};
-    return launched(launch_product_any(a, c, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProductArgs a{{W, ldw, false}, {X, ldx, false}, M, N, K, act, bias, R, ldr, Y, ldy, Z, ldz, out_dtype == SKINNY_BF16,
+                  true};
+    const Space sp = linear_space(X, ldx, W, ldw, M, K, rows);
+    if (sp.bytes > 0) {
+        uint8_t *space = static_cast<uint8_t *>(workspace);
+        PackArgs px{}, pw{};
+        if (sp.x >= 0) {
+            px = {X, ldx, M, K, reinterpret_cast<uint16_t *>(space + sp.x)};
+            a.B = {px.to, pad8(K), false};
+        }
+        if (sp.w >= 0) {
+            pw = {W, ldw, rows, K, reinterpret_cast<uint16_t *>(space + sp.w)};
+            a.A = {pw.to, pad8(K), false};
+            a.early = false;
+        }
+        if (launch_rows_pack(px, pw, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+    }
+    return launched(linear_tc_supported(a) ? launch_linear_tc(a, c, s) : launch_product_any(a, c, s));
 }
 
 int64_t skinny_linear_grad_workspace(const uint16_t *dY, int lddy, const uint16_t *X, int ldx, const uint16_t *W, int ldw,
                                      int M, int N, int K, int act) {
-    (void)dY; (void)lddy; (void)X; (void)ldx; (void)W; (void)ldw;
     if (check_product(M, N, K, act) != SKINNY_OK || M == 0 || N == 0) return 0;
-    return grad_space(M, act_gated(act) ? 2 * N : N, act).bytes;
+    return grad_space(dY, lddy, X, ldx, W, ldw, M, K, act_gated(act) ? 2 * N : N, act).bytes;
 }
 
 skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint16_t *X, int ldx, const uint16_t *W,
@@ -190,24 +222,36 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
         return SKINNY_ERR_INVALID_VALUE;
     st = call_context(&c);
     if (st != SKINNY_OK) return st;
-    const GradSpace g = grad_space(M, rows, act);
+    const Space sp = grad_space(dY, lddy, X, ldx, W, ldw, M, K, rows, act);
     uint8_t *space = static_cast<uint8_t *>(workspace);
-    Operand dz{dY, lddy, false};
-    if (!act_none || dbias) {
-        uint16_t *to = act_none || (!dX && !dW) ? nullptr : reinterpret_cast<uint16_t *>(space + g.dz);
+    Operand dz{dY, lddy, false}, xo{X, ldx, true}, wo{W, ldw, true};
+    if (dX || dW) {
+        PackArgs px{}, pw{};
+        if (dW && sp.x >= 0) {
+            px = {X, ldx, M, K, reinterpret_cast<uint16_t *>(space + sp.x)};
+            xo = {px.to, pad8(K), true};
+        }
+        if (dX && sp.w >= 0) {
+            pw = {W, ldw, rows, K, reinterpret_cast<uint16_t *>(space + sp.w)};
+            wo = {pw.to, pad8(K), true};
+        }
+        if (launch_rows_pack(px, pw, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+    }
+    if (dbias || ((dX || dW) && sp.dz >= 0)) {
+        uint16_t *to = sp.dz >= 0 && (dX || dW) ? reinterpret_cast<uint16_t *>(space + sp.dz) : nullptr;
         const LinearDzArgs d{dY, lddy, act_none ? nullptr : Z, ldz, to, pad8(rows), dbias,
-                             reinterpret_cast<float *>(space + g.partial), M, N, act};
+                             reinterpret_cast<float *>(space + sp.partial), M, N, act};
         if (launch_linear_dz(d, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
         if (to) dz = {to, pad8(rows), false};
     }
     if (dX) {
-        const ProductArgs a{{W, ldw, true}, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1};
-        if (launch_product_any(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        const ProductArgs a{wo, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1, false};
+        if (launch_linear_tc(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     }
     if (dW) {
-        const ProductArgs a{{X, ldx, true}, {dz.p, dz.ld, true}, rows, K, M, SKINNY_ACT_NONE, nullptr, nullptr, 0, dW, lddw,
-                            nullptr, 0, 1};
-        if (launch_product_any(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        const ProductArgs a{xo, {dz.p, dz.ld, true}, rows, K, M, SKINNY_ACT_NONE, nullptr, nullptr, 0, dW, lddw, nullptr, 0,
+                            1, false};
+        if (launch_linear_tc(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     }
     return SKINNY_OK;
 }

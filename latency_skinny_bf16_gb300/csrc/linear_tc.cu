@@ -1,0 +1,359 @@
+// linear_tc.cu -- products with an epilogue on the fifth-generation tensor
+// cores, for few rows: Y[r][n] = epilogue(sum_c B(r, c) A(n, c)).
+//
+// A's index is the MMA's M side (128 of a weight's rows; with a gated activation
+// 64 gates and their 64 ups), up to BN rows of B its N side, so that the
+// outputs' contiguous index lies along the lanes of tensor memory and A, the
+// weight, is read once whatever the number of rows.
+//   * A CTA has one tile and a slice of the depth: the S CTAs of a cluster split
+//     it, so that small weights fill the GPU as well.  Two CTAs fit on an SM.
+//   * Thread 0 moves 64-deep boxes of A and B by tensor-map TMA into a ring
+//     (zeros outside), thread 32 issues tcgen05.mma into sets of tensor-memory
+//     accumulators in rotation, at most 16 MMAs a set; warps 2 to 5 add each set
+//     into fp32 registers.
+//   * Both operands may lie crossed (the depth along the rows of memory), as the
+//     backward pass needs them: the MMA reads either order.
+//   * At the end every CTA sends row r's partial sums to CTA r % S of its
+//     cluster, which adds them in the order of the CTAs and runs the epilogue,
+//     neighbouring threads on neighbouring outputs.
+// Every wait is bounded; a CTA whose wait gave up reports it and stores nothing.
+#include <cuda.h>
+
+#include "experts_gemm.h"
+#include "product.cuh"
+#include "tma.cuh"
+
+namespace skinny {
+namespace {
+
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+enum : int { kWaitAcc = 5, kWaitAccEmpty = 6 };
+constexpr int kThreads = 192;          // TMA warp, MMA warp, four draining warps
+constexpr int kTmemCols = 256;
+constexpr int kABytes = 128 * 128;     // 128 indexes of A, 64 steps of the depth
+
+__host__ __device__ constexpr int stage_bytes(int BN) { return kABytes + BN * 128; }
+__host__ __device__ constexpr int ring_stages(int BN) { return BN <= 32 ? 5 : BN <= 64 ? 4 : 3; }
+__host__ __device__ constexpr int acc_sets(int BN) { return BN <= 64 ? 4 : 2; }
+__host__ __device__ constexpr int set_cols(int BN) { return BN <= 64 ? 64 : BN; }
+constexpr int kTail = 256;             // barriers, tensor-memory address, flags
+__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + ring_stages(BN) * stage_bytes(BN) + kTail; }
+// tensor memory for two CTAs on an SM, as for every kernel that takes 256 columns of it
+static_assert(smem_bytes(16) >= kTcMinSmem && smem_bytes(32) >= kTcMinSmem && smem_bytes(64) >= kTcMinSmem &&
+              smem_bytes(128) >= kTcMinSmem && 2 * (smem_bytes(32) + 1024) <= 228 * 1024, "two CTAs on an SM");
+
+struct Maps {
+    CUtensorMap a, b;
+};
+struct Params {
+    Epilogue e;
+    int64_t mt;          // tiles along the rows of B
+    int boxes;           // 64-step boxes of the depth
+    int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
+    int early;           // A may be read before the preceding kernel is done
+    int *status;
+    uint64_t budget_ns;
+};
+
+template <int BN, bool GATED, bool AX, bool BX>
+__global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_constant__ Maps maps, const Params p)
+{
+    constexpr int kStages = ring_stages(BN), kStage = stage_bytes(BN), kSets = acc_sets(BN), kCols = set_cols(BN);
+    constexpr int P = kCols / BN;                    // accumulators of a set, taken in turn
+    constexpr int TA = GATED ? 64 : 128;             // outputs of a tile
+    static_assert(!BX || BN >= 64, "crossed boxes hold 64 indexes");
+    extern __shared__ uint8_t smem_raw[];
+    griddep_launch_dependents();
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t bars = base + kStages * kStage;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+    auto accf = [&](int b) { return bars + 8u * (2 * kStages + b); };
+    auto acce = [&](int b) { return bars + 8u * (2 * kStages + kSets + b); };
+    const uint32_t done = bars + 8u * (2 * kStages + 2 * kSets);
+    static_assert(8 * (2 * kStages + 2 * kSets + 1) + 16 <= kTail, "tail");
+    uint8_t *tail = smem + kStages * kStage + 8 * (2 * kStages + 2 * kSets + 1);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
+    volatile int *mma_ok = reinterpret_cast<volatile int *>(tail + 4);
+    volatile int *failed = reinterpret_cast<volatile int *>(tail + 8);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = p.split, rank = S == 1 ? 0 : (int)cluster_ctarank();
+    const int64_t tile = blockIdx.x / S;
+    const int n0 = (int)(tile / p.mt) * TA;
+    const int64_t r0 = tile % p.mt * BN;
+    const int live = (int)min((int64_t)BN, p.e.rows - r0);
+    const int b0 = (int)((int64_t)p.boxes * rank / S), nb = (int)((int64_t)p.boxes * (rank + 1) / S) - b0;
+    if (tid == 0) {
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.b);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < kSets; ++b) {
+            mbar_init(accf(b), 1);
+            mbar_init(acce(b), 4);
+        }
+        mbar_init(done, 1);
+        *mma_ok = 0;
+        *failed = 0;
+        fence_mbarrier_init_cluster();
+    }
+    __syncthreads();
+
+    float acc[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) acc[j] = 0.f;
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- TMA producer
+            auto load_a = [&](int i, int s) {
+                const uint32_t st = base + s * kStage;
+                const int c = (b0 + i) * 64;
+                if constexpr (AX) {
+                    tma_load_2d(st, &maps.a, n0, c, full(s));
+                    tma_load_2d(st + kBox, &maps.a, n0 + 64, c, full(s));
+                } else {
+                    tma_load_2d(st, &maps.a, c, n0, full(s));
+                    if (GATED) tma_load_2d(st + 64 * 128, &maps.a, c, p.e.cols + n0, full(s));
+                }
+            };
+            auto load_b = [&](int i, int s) {
+                const uint32_t st = base + s * kStage + kABytes;
+                const int c = (b0 + i) * 64;
+                if constexpr (BX) {
+#pragma unroll
+                    for (int j = 0; j < BN / 64; ++j) tma_load_2d(st + j * kBox, &maps.b, (int)r0 + 64 * j, c, full(s));
+                } else {
+                    tma_load_2d(st, &maps.b, c, (int)r0, full(s));
+                }
+            };
+            const int pre = min(nb, kStages);
+            if (!p.early) griddep_wait();
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(full(i), (uint32_t)kStage);
+                load_a(i, i);
+            }
+            if (p.early) griddep_wait();
+            for (int i = 0; i < pre; ++i) load_b(i, i);
+            int issued = pre;
+            for (int i = pre; i < nb; ++i) {
+                const int s = i % kStages;
+                if (!mbar_wait_bounded(empty(s), (uint32_t)((i / kStages - 1) & 1), p.budget_ns)) {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitProducerEmpty);
+                    break;
+                }
+                mbar_arrive_expect_tx(full(s), (uint32_t)kStage);
+                load_a(i, s);
+                load_b(i, s);
+                issued = i + 1;
+            }
+            // every copy issued has landed before the ring is used again or the CTA exits
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                if (!mbar_wait_bounded(full(i % kStages), (uint32_t)((i / kStages) & 1), kDrainNs)) {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+                    *failed = 1;
+                }
+        }
+        __syncwarp();
+        griddep_wait();
+    } else if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
+        tc_fence_before();
+        named_bar_sync(1, kThreads - 32);
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
+        griddep_wait();
+        if (lane == 0) {
+            // ---- MMA issuer
+            constexpr uint32_t idesc = product_idesc<BN, 128, AX, BX>();
+            for (int i = 0; i < nb; ++i) {
+                const int s = i % kStages, c = i / 4, b = c % kSets;
+                if (i % 4 == 0 && c >= kSets && !mbar_wait_bounded(acce(b), (uint32_t)((c / kSets - 1) & 1), p.budget_ns)) {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
+                    break;
+                }
+                if (!mbar_wait_bounded(full(s), (uint32_t)((i / kStages) & 1), p.budget_ns)) {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = base + s * kStage;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int q = i % 4 * 4 + j;     // of the set's 16
+                    umma_bf16(tmem + (uint32_t)(b * kCols + q % P * BN), operand_desc<AX>(st, j), operand_desc<BX>(st + kABytes, j),
+                              idesc, q < P ? 0u : 1u);
+                }
+                umma_commit(empty(s));
+                if (i % 4 == 3 || i == nb - 1) umma_commit(accf(b));
+            }
+            umma_commit(done);
+            if (mbar_wait_bounded(done, 0, kDrainNs)) *mma_ok = 1;
+            else report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+        }
+        __syncwarp();
+    } else {
+        // ---- draining warps: lane quarter warp % 4 of tensor memory
+        named_bar_sync(1, kThreads - 32);
+        tc_fence_after();
+        griddep_wait();
+        const uint32_t lanes = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int chunks = (nb + 3) / 4;
+        for (int c = 0; c < chunks; ++c) {
+            const int b = c % kSets;
+            int got = 1;
+            if (lane == 0) got = mbar_wait_bounded(accf(b), (uint32_t)((c / kSets) & 1), p.budget_ns);
+            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
+                if (lane == 0) {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAcc);
+                    *failed = 1;
+                }
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+#pragma unroll
+                for (int j = 0; j < BN; j += 16) {
+                    uint32_t r[16];
+                    tmem_ld16_nowait(lanes + (uint32_t)(b * kCols + q * BN + j), r);
+                    tmem_ld_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[j + i] += __uint_as_float(r[i]);
+                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce(b));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if (*mma_ok) tmem_dealloc(*tmem_slot, kTmemCols);
+        // else an issued MMA may still write it: it stays allocated until the CTA exits
+    }
+
+    // ---- partial sums to the rows' owners, through the ring
+    if (S > 1) {
+        cluster_arrive_release();                    // every CTA's ring has been read
+        cluster_wait_acquire();
+    }
+    const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = (BN + S - 1) >> shift;
+    const bool ok = *failed == 0 && *mma_ok != 0;
+    if (warp >= 2 && ok) {
+        const uint32_t at = base + 4u * (uint32_t)(rank * per * 128 + 32 * (warp & 3) + lane);
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+            const uint32_t to = at + 512u * (uint32_t)(j >> shift);
+            if (j >= live) continue;
+            if (S == 1) *reinterpret_cast<float *>(smem + (to - base)) = acc[j];
+            else st_shared_cluster_f32(mapa_shared(to, (uint32_t)(j & (S - 1))), acc[j]);
+        }
+    }
+    if (S > 1) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    if (!ok) return;
+    const float *slots = reinterpret_cast<const float *>(smem);
+    const int mine = (live - rank + S - 1) >> shift;
+    for (int i = tid; i < mine * TA; i += kThreads) {
+        const int ci = i / TA, nl = i % TA, n = n0 + nl;
+        if (n >= p.e.cols) continue;
+        float z = 0.f, up = 0.f;
+        for (int s = 0; s < S; ++s) {
+            const float *slot = slots + (s * per + ci) * 128 + nl;
+            z += slot[0];
+            if (GATED) up += slot[64];
+        }
+        finish<GATED>(p.e, r0 + (int64_t)ci * S + rank, n, z, up);
+    }
+}
+
+template <int BN, bool GATED, bool AX, bool BX>
+cudaError_t launch_as(const Maps &maps, const Params &p, int64_t ctas, const CallCtx &c, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes(BN);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN, GATED, AX, BX>, maps, p);
+}
+
+template <int BN>
+cudaError_t prepare_bn() {
+    cudaError_t e = set_max_dyn_smem(&linear_tc_kernel<BN, false, false, false>);
+    if (e == cudaSuccess) e = set_max_dyn_smem(&linear_tc_kernel<BN, true, false, false>);
+    if (e == cudaSuccess) e = set_max_dyn_smem(&linear_tc_kernel<BN, false, true, false>);
+    return e;
+}
+
+bool rows16(const Operand &o) { return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0; }
+
+}  // namespace
+
+bool linear_tc_supported(const ProductArgs &a) { return a.depth >= 1 && rows16(a.A) && rows16(a.B); }
+
+cudaError_t linear_tc_prepare() {
+    cudaError_t e = prepare_bn<16>();
+    if (e == cudaSuccess) e = prepare_bn<32>();
+    if (e == cudaSuccess) e = prepare_bn<64>();
+    if (e == cudaSuccess) e = prepare_bn<128>();
+    if (e == cudaSuccess) e = set_max_dyn_smem(&linear_tc_kernel<128, false, true, true>);
+    return e;
+}
+
+cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream) {
+    const bool gated = act_gated(a.act), ax = a.A.crossed, bx = a.B.crossed;
+    const int BN = bx || a.rows > 64 ? 128 : a.rows > 32 ? 64 : a.rows > 16 ? 32 : 16;
+    const int TA = gated ? 64 : 128;
+    Maps maps;
+    const int arows = gated ? 2 * a.cols : a.cols;
+    if (!(ax ? encode_bf16_2d(&maps.a, a.A.p, a.cols, a.depth, a.A.ld, 64)
+             : encode_bf16_2d(&maps.a, a.A.p, a.depth, arows, a.A.ld, TA)) ||
+        !(bx ? encode_bf16_2d(&maps.b, a.B.p, (int)a.rows, a.depth, a.B.ld, 64)
+             : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, BN)))
+        return cudaErrorInvalidValue;
+    Params p{};
+    p.e = epilogue_of(a);
+    p.mt = (a.rows + BN - 1) / BN;
+    p.boxes = (a.depth + 63) / 64;
+    p.early = a.early;
+    p.status = c.status;
+    p.budget_ns = c.budget_ns;
+    const int64_t tiles = p.mt * ((a.cols + TA - 1) / TA);
+    for (p.split = 1; p.split < 8 && tiles * p.split * 2 <= 2 * c.num_sms && p.boxes >= 4 * p.split;) p.split *= 2;
+    const int64_t ctas = tiles * p.split;
+    if (ctas >= 1ll << 31) return cudaErrorInvalidValue;
+#define SKINNY_TC(BNv)                                                              \
+    case BNv:                                                                       \
+        if (ax) return launch_as<BNv, false, true, false>(maps, p, ctas, c, stream); \
+        return gated ? launch_as<BNv, true, false, false>(maps, p, ctas, c, stream) \
+                     : launch_as<BNv, false, false, false>(maps, p, ctas, c, stream);
+    if (bx) return launch_as<128, false, true, true>(maps, p, ctas, c, stream);
+    switch (BN) {
+        SKINNY_TC(16)
+        SKINNY_TC(32)
+        SKINNY_TC(64)
+        SKINNY_TC(128)
+    }
+#undef SKINNY_TC
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace skinny

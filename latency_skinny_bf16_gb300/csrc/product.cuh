@@ -1,0 +1,69 @@
+// product.cuh -- what the products with an epilogue share on the fifth-
+// generation tensor cores: operands of either order in shared memory, and the
+// epilogue of one output.
+#pragma once
+
+#include "act.cuh"
+#include "common.cuh"
+#include "layer.h"
+#include "tcgen05.cuh"
+
+namespace skinny {
+
+// A stage of an operand holds 64 steps of the depth in 128-byte swizzle atoms.
+// Plain (depth along the 128-byte rows, sw128_desc): 16 steps further is 32
+// bytes.  Crossed (the operand's index along the 128-byte rows): boxes of 64
+// indexes x 64 steps, 8 KB each, one behind the other along the index; groups of
+// 8 steps lie 1024 bytes apart, 16 steps further is 2048 bytes.
+constexpr uint32_t kBox = 64 * 128;
+__device__ __forceinline__ uint64_t crossed_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <bool CROSSED>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t stage, int step) {
+    return CROSSED ? crossed_desc(stage + 2048u * step) : sw128_desc(stage + 32u * step);
+}
+// kind::f16 with operands of either order: bits 15 and 16 for a crossed A and B.
+template <int N, int M, bool AX, bool BX>
+__host__ __device__ constexpr uint32_t product_idesc() {
+    return idesc_bf16<N, M>() | ((uint32_t)AX << 15) | ((uint32_t)BX << 16);
+}
+
+struct Epilogue {
+    const uint16_t *bias;
+    const void *R;
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+    uint16_t *Z;
+    int64_t ldz;
+    int64_t rows;
+    int cols, act, out_bf16;
+};
+inline Epilogue epilogue_of(const ProductArgs &a) {
+    return {a.bias, a.R, a.ldr, a.Y, a.ldy, a.Z, a.ldz, a.rows, a.cols, a.act, a.out_bf16};
+}
+
+__device__ __forceinline__ float residual_at(const Epilogue &e, int64_t r, int n) {
+    return e.out_bf16 ? bf16_one(ldg_u16(static_cast<const uint16_t *>(e.R) + r * e.ldr + n))
+                      : __ldcg(static_cast<const float *>(e.R) + r * e.ldr + n);
+}
+// Output n of row r from its sum (gated: with the sum of its up).
+template <bool GATED>
+__device__ __forceinline__ void finish(const Epilogue &e, int64_t r, int n, float z, float up) {
+    if (e.bias) {
+        z += bf16_one(ldg_u16(e.bias + n));
+        if (GATED) up += bf16_one(ldg_u16(e.bias + e.cols + n));
+    }
+    if (e.Z) {
+        e.Z[r * e.ldz + n] = f32_to_bf16_rn(z);
+        if (GATED) e.Z[r * e.ldz + e.cols + n] = f32_to_bf16_rn(up);
+    }
+    float y = act_value(e.act, z);
+    if (GATED) y *= up;
+    if (e.R) y += residual_at(e, r, n);
+    store_y(e.Y, e.out_bf16, r * e.ldy + n, y);
+}
+
+}  // namespace skinny
