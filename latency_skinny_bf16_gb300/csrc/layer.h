@@ -40,6 +40,11 @@ bool linear_tc_supported(const ProductArgs &a);
 cudaError_t linear_tc_prepare();
 cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
 
+// tcgen05 by pairs of SMs (linear_pair.cu), as above
+cudaError_t linear_pair_prepare();
+bool linear_pair_faster(const ProductArgs &a, int num_sms);   // than linear_tc.cu
+cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
+
 // Rows laid out from `to` on, whole 16-byte pieces each; from NULL: none.
 struct PackArgs {
     const uint16_t *from;

@@ -47,6 +47,14 @@ Space grad_space(const void *dY, int lddy, const void *X, int ldx, const void *W
     return s;
 }
 
+skinny_status_t launch_product(const ProductArgs &a, const CallCtx &c, cudaStream_t s) {
+    const bool tc = linear_tc_supported(a);
+    if (c.force_backend == SKINNY_BACKEND_TCGEN05) return tc ? launched(launch_linear_pair(a, c, s)) : SKINNY_ERR_UNSUPPORTED;
+    if (c.force_backend == SKINNY_BACKEND_SPLITK) return tc ? launched(launch_linear_tc(a, c, s)) : SKINNY_ERR_UNSUPPORTED;
+    if (c.force_backend == SKINNY_BACKEND_DOTPROD || !tc) return launched(launch_product_any(a, c, s));
+    return launched(linear_pair_faster(a, c.num_sms) ? launch_linear_pair(a, c, s) : launch_linear_tc(a, c, s));
+}
+
 // [T, H] rows of D elements, strides st and sh.
 struct View {
     const void *p;
@@ -173,7 +181,7 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
         }
         if (launch_rows_pack(px, pw, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     }
-    return launched(linear_tc_supported(a) ? launch_linear_tc(a, c, s) : launch_product_any(a, c, s));
+    return launch_product(a, c, s);
 }
 
 int64_t skinny_linear_grad_workspace(const uint16_t *dY, int lddy, const uint16_t *X, int ldx, const uint16_t *W, int ldw,
@@ -246,12 +254,14 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
     }
     if (dX) {
         const ProductArgs a{wo, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1, false};
-        if (launch_linear_tc(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        st = launch_product(a, c, s);
+        if (st != SKINNY_OK) return st;
     }
     if (dW) {
         const ProductArgs a{xo, {dz.p, dz.ld, true}, rows, K, M, SKINNY_ACT_NONE, nullptr, nullptr, 0, dW, lddw, nullptr, 0,
                             1, false};
-        if (launch_linear_tc(a, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        st = launch_product(a, c, s);
+        if (st != SKINNY_OK) return st;
     }
     return SKINNY_OK;
 }

@@ -49,6 +49,66 @@ __device__ __forceinline__ float residual_at(const Epilogue &e, int64_t r, int n
     return e.out_bf16 ? bf16_one(ldg_u16(static_cast<const uint16_t *>(e.R) + r * e.ldr + n))
                       : __ldcg(static_cast<const float *>(e.R) + r * e.ldr + n);
 }
+// ---- the epilogue of N rows of one output, from registers.  Each step by itself, its types and pointers
+// settled outside its loop, so that loads go out together and a row costs a step of a pointer.
+template <typename T>
+__device__ __forceinline__ uint32_t load_cg(const T *p) {     // a register each: halves of one would wait for each other
+    if constexpr (sizeof(T) == 2) return ldg_u16(p);
+    else return __float_as_uint(__ldcg(p));
+}
+// v[j] += R[j * ld], j < live
+template <int N, typename T>
+__device__ __forceinline__ void add_rows(float (&v)[N], const T *R, int64_t ld, int live) {
+    if (live <= 0) return;
+    constexpr int kBatch = N < 32 ? N : 32;
+    const T *last = R + (live - 1) * ld;             // no branch around a load, so that they go out together
+#pragma unroll
+    for (int j = 0; j < N; j += kBatch) {
+        uint32_t raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            raw[i] = load_cg(j + i < live ? R : last);
+            R += ld;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[j + i] += __uint_as_float(sizeof(T) == 2 ? raw[i] << 16 : raw[i]);
+    }
+}
+// Y[j * ld] = v[j], j < live
+template <int N, typename T>
+__device__ __forceinline__ void store_rows(const float (&v)[N], T *Y, int64_t ld, int live) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (j < live) {
+            if constexpr (sizeof(T) == 2) *Y = f32_to_bf16_rn(v[j]);
+            else *Y = v[j];
+        }
+        Y += ld;
+    }
+}
+template <int N>
+__device__ __forceinline__ void act_rows(float (&v)[N], int act) {
+    if (act == SKINNY_ACT_NONE) return;
+    if (act_gelu(act)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(SKINNY_ACT_GELU, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_value(SKINNY_ACT_SILU, v[j]);
+    }
+}
+// Residual and store of rows r .. r + live - 1 of output n.
+template <int N>
+__device__ __forceinline__ void out_rows(const Epilogue &e, float (&v)[N], int64_t r, int n, int live) {
+    if (e.out_bf16) {
+        if (e.R) add_rows(v, static_cast<const uint16_t *>(e.R) + r * e.ldr + n, e.ldr, live);
+        store_rows(v, static_cast<uint16_t *>(e.Y) + r * e.ldy + n, e.ldy, live);
+    } else {
+        if (e.R) add_rows(v, static_cast<const float *>(e.R) + r * e.ldr + n, e.ldr, live);
+        store_rows(v, static_cast<float *>(e.Y) + r * e.ldy + n, e.ldy, live);
+    }
+}
+
 // Output n of row r from its sum (gated: with the sum of its up).
 template <bool GATED>
 __device__ __forceinline__ void finish(const Epilogue &e, int64_t r, int n, float z, float up) {

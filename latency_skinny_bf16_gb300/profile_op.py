@@ -2,7 +2,9 @@
 
     python -m latency_skinny_bf16_gb300.profile_op --op experts --T 16 --k 8 --E 64 --N 2048 --K 7168 --act swiglu
 
-``--op`` is dispatch, combine, combine_grad, experts or lora; ``--calls`` calls
+``--op`` is dispatch, combine, combine_grad, experts or lora, or, of a dense
+layer, linear, linear_grad, heads or heads_grad (T tokens, E heads of queries
+and k of keys, K elements a head); ``--calls`` calls
 run, alternating between two sets of inputs (together larger than L2 at sizes
 worth profiling).  Prints the algorithmic bytes of a call: each input read
 once, each output written once, the weights of the experts or adapters that
@@ -37,10 +39,32 @@ def prepare(a, seed):
         used = min(a.T, a.E)
         return (lambda: sk.lora_gemm(x, w, la, lb, ids),
                 2 * (a.N * a.K + used * a.R * (a.N + a.K) + a.T * a.K) + 4 * a.T * a.N)
+    act = None if a.act == "none" else a.act
+    wrows = 2 * a.N if act in ("swiglu", "geglu") else a.N
+    if a.op in ("linear", "linear_grad"):
+        x, w = rand(a.T, a.K), rand(wrows, a.K, scale=a.K ** -0.5)
+        y, pre = rand(a.T, a.N), rand(a.T, wrows) if act else None
+        if a.op == "linear":
+            return (lambda: sk.linear(x, w, activation=act, out=y, residual=None if act else y, pre=pre),
+                    2 * (wrows * a.K + a.T * a.K + a.T * a.N * (1 if act else 2) + (a.T * wrows if act else 0)))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        return (lambda: sk.linear_grad(y, x, w, pre=pre, activation=act, dx=dx, dw=dw),
+                2 * (2 * wrows * a.K + 2 * a.T * a.K + a.T * a.N + (a.T * wrows if act else 0)))
+    if a.op in ("heads", "heads_grad"):
+        q, k = rand(a.T, a.E + 2 * a.k, a.K).split([a.E, 2 * a.k], dim=1)
+        k = k[:, :a.k]
+        qw, kw = rand(a.K), rand(a.K)
+        angle = torch.arange(4096, device="cuda")[:, None] * 1e4 ** (-torch.arange(0, a.K, 2, device="cuda") / a.K)
+        table = torch.cat([angle.cos(), angle.sin()], dim=1)
+        at = torch.arange(a.T, dtype=torch.int32, device="cuda") % 4096
+        dq, dk = rand(a.T, a.E, a.K), rand(a.T, a.k, a.K)
+        size = 2 * a.T * (a.E + a.k) * a.K
+        if a.op == "heads":
+            return lambda: sk.qk_norm_rope(q, k, qw, kw, table, at, q_out=dq, k_out=dk), 2 * size
+        return lambda: sk.qk_norm_rope_grad(dq, dk, q, k, qw, kw, table, at), 3 * size
     ids, (_, pos, _, offsets) = routing(a, seed)
     rows = a.T * a.k
     if a.op == "experts":
-        wrows = 2 * a.N if a.act == "swiglu" else a.N
         xs, w = rand(rows, a.K), rand(a.E, wrows, a.K, scale=a.K ** -0.5)
         out = torch.empty((rows, a.N), dtype=torch.bfloat16, device="cuda")
         touched = int((offsets[1:] > offsets[:-1]).sum())
@@ -58,17 +82,20 @@ def prepare(a, seed):
 
 def main(argv=None):
     p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
-    p.add_argument("--op", choices=["dispatch", "combine", "combine_grad", "experts", "lora"], required=True)
+    p.add_argument("--op", choices=["dispatch", "combine", "combine_grad", "experts", "lora", "linear", "linear_grad", "heads",
+                                      "heads_grad"], required=True)
     p.add_argument("--T", type=int, default=16, help="tokens")
     p.add_argument("--k", type=int, default=8, help="experts per token")
     p.add_argument("--E", type=int, default=64, help="experts, or adapters")
     p.add_argument("--N", type=int, default=2048, help="outputs; the rows' width for dispatch and combine")
     p.add_argument("--K", type=int, default=7168)
     p.add_argument("--R", type=int, default=16, help="rank of the adapters")
-    p.add_argument("--act", choices=["none", "swiglu"], default="none")
+    p.add_argument("--act", choices=["none", "silu", "gelu", "swiglu", "geglu"], default="none")
     p.add_argument("--calls", type=int, default=6)
+    p.add_argument("--backend", type=int, default=0, help="SKINNY_OPT_FORCE_BACKEND")
     a = p.parse_args(argv)
     assert sk.skinny_init(0) == sk.SKINNY_OK
+    sk.skinny_set_option(sk.SKINNY_OPT_FORCE_BACKEND, a.backend)
     calls = [prepare(a, seed) for seed in (1, 2)]
     for i in range(a.calls):
         calls[i % 2][0]()

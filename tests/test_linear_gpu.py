@@ -270,6 +270,42 @@ def test_grad_far_values(act):
     assert torch.allclose(db[at], want[at], atol=1e-30)
 
 
+# ------------------------------------------------------------------ each kernel
+
+KERNELS = {"pair": sk.SKINNY_BACKEND_TCGEN05, "split": sk.SKINNY_BACKEND_SPLITK, "any": sk.SKINNY_BACKEND_DOTPROD}
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (130, 72, 64), (256, 256, 256), (257, 264, 320), (600, 520, 1096), (1, 700, 4104),
+                                   (2305, 136, 72)])
+def test_kernels_agree_with_64_bits(M, N, K, act, kernel):
+    with sk.options(backend=KERNELS[kernel]):
+        forward(M, N, K, act)
+        forward(M, N, K, act, out=torch.float32, bias=False, residual=False, pre=False)
+        backward(M, N, K, act)
+
+
+@pytest.mark.parametrize("act", [None, "geglu"])
+def test_pair_walks_many_tiles(act):
+    """More tiles than pairs of SMs, the last band of rows short."""
+    with sk.options(backend=sk.SKINNY_BACKEND_TCGEN05):
+        forward(2700, 2312, 200, act)
+        backward(2700, 2312, 328, act)
+
+
+@pytest.mark.parametrize("kernel", ["pair", "split"])
+def test_same_sign_sums_each_kernel(kernel):
+    g = gen(6)
+    for M in (16, 300):
+        x, w = rand(g, M, 14336).abs(), rand(g, 256, 14336).abs()
+        y = torch.empty((M, 256), dtype=torch.float32, device="cuda")
+        with sk.options(backend=KERNELS[kernel]):
+            sk.linear(x, w, out=y)
+        want, _, size = ref.linear(x, w, None, None, None)
+        ref.check(y, want, 1e-5 * size, kernel)
+
+
 # ------------------------------------------------------------------ calls
 
 def calls(M):
