@@ -14,8 +14,8 @@
 //     landed: 4864 x 4096 x 8192 at 1244 TFLOP/s.)  At most 64 MMAs are summed in tensor memory: two sets of 256 columns
 //     in rotation, eight warps add each set into fp32 registers (128 rows of one
 //     output each) while the tensor cores work on the other.  Reading a set holds
-//     the tensor cores up by 0.23 us, whatever it overlaps (4864 x 4096 x 8192:
-//     243 us with 16 MMAs a set, 229 with 32, 222 with 64); 64 keep the bound of
+//     the tensor cores up, whatever it overlaps (4864 x 4096 x 8192:
+//     197 us with 16 MMAs a set, 189 with 32, 185 with 64); 64 keep the bound of
 //     the products, 64 * 2 * 2^-24 = 7.6e-6 of the terms' sum (measured: a third).
 //   * At a tile's end these warps run the epilogue from their registers, and the
 //     MMAs of the next tile go on for two sets.  With a gated activation a CTA's
@@ -200,46 +200,61 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---- MMA issuer
+        if (rank == 0) {
+            // ---- MMA issuer: the warp stays together, so that what the MMAs take is uniform, and the ring's
+            // place is counted, not divided for (4864 x 4096 x 8192: 223 us by one lane with divisions)
             constexpr uint32_t idesc = product_idesc<256, 256, AX, BX>();
-            int64_t i = 0, c = 0;
+            constexpr uint64_t kStepA = AX ? 2048 >> 4 : 32 >> 4, kStepB = BX ? 2048 >> 4 : 32 >> 4;
+            const uint64_t da = operand_desc<AX>(base, 0), db = operand_desc<BX>(base + kHalf, 0);
+            const bool one = elect_one();
+            int s = 0, b = 0;
+            uint32_t phase = 0, free_phase = 1;      // of the ring's place and of the set; the sets are free at first
             bool go = true;
             for (int64_t t = first; go && t < tiles; t += pairs) {
-                for (int k = 0; k < p.boxes; ++k, ++i) {
-                    const int s = (int)(i % kStages), b = (int)(c % kSets);
-                    const uint32_t phase = (uint32_t)((i / kStages) & 1);
-                    if (k % kChunk == 0 && c >= kSets && !mbar_wait_bounded(acce(b), (uint32_t)((c / kSets - 1) & 1), p.budget_ns)) {
-                        report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
+                for (int k = 0; k < p.boxes; ++k) {
+                    const bool starts = k % kChunk == 0;
+                    if (starts && !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acce(b), free_phase, p.budget_ns))) {
+                        if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
                         go = false;
                         break;
                     }
-                    if (!mbar_wait_bounded(full(s), phase, p.budget_ns)) {
-                        report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), phase, p.budget_ns))) {
+                        if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
                         go = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = base + s * kStage;
+                    const bool ends = k % kChunk == kChunk - 1 || k == p.boxes - 1;
+                    const uint64_t at = (uint64_t)(uint32_t)(s * (kStage >> 4));
+                    if (one) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        pair_mma(tmem + (uint32_t)(b * kSetCols), operand_desc<AX>(st, j), operand_desc<BX>(st + kHalf, j), idesc,
-                                 k % kChunk || j ? 1u : 0u);
-                    pair_commit(empty(s));
-                    if (k % kChunk == kChunk - 1 || k == p.boxes - 1) {
-                        pair_commit(accf(b));
-                        ++c;
+                        for (int j = 0; j < 4; ++j)
+                            pair_mma(tmem + (uint32_t)(b * kSetCols), da + at + j * kStepA, db + at + j * kStepB, idesc,
+                                     !starts || j ? 1u : 0u);
+                        pair_commit(empty(s));
+                        if (ends) pair_commit(accf(b));
+                    }
+                    __syncwarp();
+                    if (ends) {
+                        b ^= 1;
+                        if (b == 0) free_phase ^= 1;
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
                     }
                 }
             }
-            if (!go) let_land();
-            pair_commit(done);
-            if (mbar_wait_bounded(done, 0, kDrainNs)) {
-                *mma_ok = 1;
-                asm volatile("st.shared::cluster.u32 [%0], %1;"
-                             :: "r"(mapa_shared(smem_u32(const_cast<int *>(mma_ok)), 1)), "r"(1) : "memory");
-            } else {
-                report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+            if (one) {
+                if (!go) let_land();
+                pair_commit(done);
+                if (mbar_wait_bounded(done, 0, kDrainNs)) {
+                    *mma_ok = 1;
+                    asm volatile("st.shared::cluster.u32 [%0], %1;"
+                                 :: "r"(mapa_shared(smem_u32(const_cast<int *>(mma_ok)), 1)), "r"(1) : "memory");
+                } else {
+                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+                }
             }
         }
         __syncwarp();

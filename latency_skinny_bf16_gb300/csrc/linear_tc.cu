@@ -167,30 +167,45 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         tc_fence_after();
         const uint32_t tmem = *tmem_slot;
         griddep_wait();
-        if (lane == 0) {
-            // ---- MMA issuer
-            constexpr uint32_t idesc = product_idesc<BN, 128, AX, BX>();
-            for (int i = 0; i < nb; ++i) {
-                const int s = i % kStages, c = i / 4, b = c % kSets;
-                if (i % 4 == 0 && c >= kSets && !mbar_wait_bounded(acce(b), (uint32_t)((c / kSets - 1) & 1), p.budget_ns)) {
-                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
-                    break;
-                }
-                if (!mbar_wait_bounded(full(s), (uint32_t)((i / kStages) & 1), p.budget_ns)) {
-                    report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = base + s * kStage;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int q = i % 4 * 4 + j;     // of the set's 16
-                    umma_bf16(tmem + (uint32_t)(b * kCols + q % P * BN), operand_desc<AX>(st, j), operand_desc<BX>(st + kABytes, j),
-                              idesc, q < P ? 0u : 1u);
-                }
-                umma_commit(empty(s));
-                if (i % 4 == 3 || i == nb - 1) umma_commit(accf(b));
+        // ---- MMA issuer: the warp stays together, so that what the MMAs take is uniform
+        constexpr uint32_t idesc = product_idesc<BN, 128, AX, BX>();
+        constexpr uint64_t kStepA = AX ? 2048 >> 4 : 32 >> 4, kStepB = BX ? 2048 >> 4 : 32 >> 4;
+        const uint64_t da = operand_desc<AX>(base, 0), db = operand_desc<BX>(base + kABytes, 0);
+        const bool one = elect_one();
+        int s = 0, b = 0;
+        uint32_t phase = 0, free_phase = 1;          // of the ring's place and of the set; the sets are free at first
+        for (int i = 0; i < nb; ++i) {
+            const int in = i % 4;                    // stages of the set before this one
+            if (in == 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(acce(b), free_phase, p.budget_ns))) {
+                if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitAccEmpty);
+                break;
             }
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(full(s), phase, p.budget_ns))) {
+                if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitConsumerFull);
+                break;
+            }
+            tc_fence_after();
+            const bool ends = in == 3 || i == nb - 1;
+            const uint64_t at = (uint64_t)(uint32_t)(s * (kStage >> 4));
+            if (one) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)          // a stage's four MMAs go to the set's P accumulators in turn
+                    umma_bf16(tmem + (uint32_t)(b * kCols + j % P * BN), da + at + j * kStepA, db + at + j * kStepB, idesc,
+                              in == 0 && j < P ? 0u : 1u);
+                umma_commit(empty(s));
+                if (ends) umma_commit(accf(b));
+            }
+            __syncwarp();
+            if (ends && ++b == kSets) {
+                b = 0;
+                free_phase ^= 1;
+            }
+            if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        if (one) {
             umma_commit(done);
             if (mbar_wait_bounded(done, 0, kDrainNs)) *mma_ok = 1;
             else report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);

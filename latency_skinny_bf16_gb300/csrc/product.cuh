@@ -30,6 +30,13 @@ __host__ __device__ constexpr uint32_t product_idesc() {
     return idesc_bf16<N, M>() | ((uint32_t)AX << 15) | ((uint32_t)BX << 16);
 }
 
+// One lane of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 struct Epilogue {
     const uint16_t *bias;
     const void *R;
