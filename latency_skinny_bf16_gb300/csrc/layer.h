@@ -38,6 +38,7 @@ cudaError_t launch_product_any(const ProductArgs &a, const CallCtx &c, cudaStrea
 // tcgen05 (linear_tc.cu): 16-byte aligned rows, a depth of 1 at least
 bool linear_tc_supported(const ProductArgs &a);
 cudaError_t linear_tc_prepare();
+int64_t linear_tc_ns(const ProductArgs &a, int num_sms);
 cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
 
 // tcgen05 by pairs of SMs (linear_pair.cu), as above

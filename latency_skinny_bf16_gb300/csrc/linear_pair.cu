@@ -389,9 +389,15 @@ cudaError_t linear_pair_prepare() {
     return e;
 }
 
+// Up to 64 rows the tiles of 256 are mostly empty: 64 rows 24576 x 1536 22.6 us, and 15.3 with the depth split.
+// Above, by the time of each: a tile's 0.33 us a box and 2.5 beside.  GB300, us, this kernel and the other: 1024 rows
+// 7168 x 2048 25.8 and 29.7, 2112 x 7168 39.4 and 31.4, 2048 x 2048 14.7 and 16.1; 192 rows 7168 x 2048 15.2 and 16.2;
+// 128 rows 15.2 and 15.0; 384 rows 24576 x 1536 30.2 and 29.3, 512 rows 30.9 and 39.5.
 bool linear_pair_faster(const ProductArgs &a, int num_sms) {
-    const int64_t tiles = (a.rows + 255) / 256 * ((a.cols + (act_gated(a.act) ? 127 : 255)) / (act_gated(a.act) ? 128 : 256));
-    return tiles >= num_sms / 4;
+    if (a.rows <= 64 && !a.B.crossed) return false;
+    const int64_t wide = act_gated(a.act) ? 128 : 256, pairs = num_sms / 2;
+    const int64_t tiles = (a.rows + 255) / 256 * ((a.cols + wide - 1) / wide), boxes = (a.depth + 63) / 64;
+    return (tiles + pairs - 1) / pairs * (330 * boxes + 2500) + 1500 < linear_tc_ns(a, num_sms);
 }
 
 cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStream_t stream) {

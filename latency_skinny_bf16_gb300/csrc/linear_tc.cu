@@ -13,9 +13,10 @@
 //     into fp32 registers.
 //   * Both operands may lie crossed (the depth along the rows of memory), as the
 //     backward pass needs them: the MMA reads either order.
-//   * At the end every CTA sends row r's partial sums to CTA r % S of its
-//     cluster, which adds them in the order of the CTAs and runs the epilogue,
-//     neighbouring threads on neighbouring outputs.
+//   * At the end every CTA sends each CTA of its cluster the partial sums of that
+//     one's rows (BN / S of them), which it adds in the order of the CTAs before
+//     the epilogue, neighbouring threads on neighbouring outputs.  One CTA for
+//     the whole depth runs the epilogue from its registers.
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing.
 #include <cuda.h>
 
@@ -49,6 +50,7 @@ struct Params {
     Epilogue e;
     int64_t mt;          // tiles along the rows of B
     int boxes;           // 64-step boxes of the depth
+    int ta;              // outputs of a tile: 8 to 128 (gated: 64)
     int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
     int early;           // A may be read before the preceding kernel is done
     int *status;
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
 {
     constexpr int kStages = ring_stages(BN), kStage = stage_bytes(BN), kSets = acc_sets(BN), kCols = set_cols(BN);
     constexpr int P = kCols / BN;                    // accumulators of a set, taken in turn
-    constexpr int TA = GATED ? 64 : 128;             // outputs of a tile
+    const int TA = p.ta;
     static_assert(!BX || BN >= 64, "crossed boxes hold 64 indexes");
     extern __shared__ uint8_t smem_raw[];
     griddep_launch_dependents();
@@ -131,10 +133,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                     tma_load_2d(st, &maps.b, c, (int)r0, full(s));
                 }
             };
+            const int tx = (AX ? kABytes : (GATED ? 2 : 1) * TA * 128) + BN * 128;
             const int pre = min(nb, kStages);
             if (!p.early) griddep_wait();
             for (int i = 0; i < pre; ++i) {
-                mbar_arrive_expect_tx(full(i), (uint32_t)kStage);
+                mbar_arrive_expect_tx(full(i), (uint32_t)tx);
                 load_a(i, i);
             }
             if (p.early) griddep_wait();
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                     report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitProducerEmpty);
                     break;
                 }
-                mbar_arrive_expect_tx(full(s), (uint32_t)kStage);
+                mbar_arrive_expect_tx(full(s), (uint32_t)tx);
                 load_a(i, s);
                 load_b(i, s);
                 issued = i + 1;
@@ -258,16 +261,29 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         cluster_arrive_release();                    // every CTA's ring has been read
         cluster_wait_acquire();
     }
-    const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = (BN + S - 1) >> shift;
     const bool ok = *failed == 0 && *mma_ok != 0;
+    const Epilogue &e = p.e;
+    if (!GATED && S == 1) {                          // from the registers: a thread has all rows of its output
+        const int nl = 32 * (warp & 3) + lane, n = n0 + nl;
+        if (warp >= 2 && ok && nl < TA && n < e.cols) {
+            const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
+#pragma unroll
+            for (int j = 0; j < BN; ++j) acc[j] += bias;
+            if (e.Z) store_rows(acc, e.Z + r0 * e.ldz + n, e.ldz, live);
+            act_rows(acc, e.act);
+            out_rows(e, acc, r0, n, live);
+        }
+        return;
+    }
+    const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = BN >> shift;      // rows of an owner
     if (warp >= 2 && ok) {
         const uint32_t at = base + 4u * (uint32_t)(rank * per * 128 + 32 * (warp & 3) + lane);
+        uint32_t to = at;
 #pragma unroll
         for (int j = 0; j < BN; ++j) {
-            const uint32_t to = at + 512u * (uint32_t)(j >> shift);
-            if (j >= live) continue;
-            if (S == 1) *reinterpret_cast<float *>(smem + (to - base)) = acc[j];
-            else st_shared_cluster_f32(mapa_shared(to, (uint32_t)(j & (S - 1))), acc[j]);
+            if ((j & (per - 1)) == 0) to = mapa_shared(at, (uint32_t)(S == 1 ? rank : j / (BN / 8) >> (3 - shift)));
+            if (j < live) st_shared_cluster_f32(to, acc[j]);
+            to += 512u;
         }
     }
     if (S > 1) {
@@ -277,18 +293,44 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         __syncthreads();
     }
     if (!ok) return;
+    // kRows rows of an output a thread at a time, the output's threads taking turns
+    constexpr int kRows = BN < 8 ? BN : 8, kOuts = GATED ? 64 : 128, kTurns = kThreads / kOuts;
     const float *slots = reinterpret_cast<const float *>(smem);
-    const int mine = (live - rank + S - 1) >> shift;
-    for (int i = tid; i < mine * TA; i += kThreads) {
-        const int ci = i / TA, nl = i % TA, n = n0 + nl;
-        if (n >= p.e.cols) continue;
-        float z = 0.f, up = 0.f;
+    const int nl = tid % kOuts, turn = tid / kOuts, n = n0 + nl, mine = min(per, live - rank * per);
+    if (turn >= kTurns || nl >= TA || n >= e.cols) return;
+    const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
+    const float ubias = GATED && e.bias ? bf16_one(ldg_u16(e.bias + e.cols + n)) : 0.f;
+    for (int c = turn * kRows; c < mine; c += kTurns * kRows) {
+        const int rows = min(kRows, mine - c);
+        float z[kRows], up[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) z[i] = up[i] = 0.f;
         for (int s = 0; s < S; ++s) {
-            const float *slot = slots + (s * per + ci) * 128 + nl;
-            z += slot[0];
-            if (GATED) up += slot[64];
+            const float *slot = slots + (s * per + c) * 128 + nl;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (i < rows) {
+                    z[i] += slot[i * 128];
+                    if (GATED) up[i] += slot[i * 128 + 64];
+                }
+            }
         }
-        finish<GATED>(p.e, r0 + (int64_t)ci * S + rank, n, z, up);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            z[i] += bias;
+            up[i] += ubias;
+        }
+        const int64_t r = r0 + rank * per + c;
+        if (e.Z) {
+            store_rows(z, e.Z + r * e.ldz + n, e.ldz, rows);
+            if (GATED) store_rows(up, e.Z + r * e.ldz + e.cols + n, e.ldz, rows);
+        }
+        act_rows(z, e.act);
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) z[i] *= up[i];
+        }
+        out_rows(e, z, r, n, rows);
     }
 }
 
@@ -320,7 +362,45 @@ cudaError_t prepare_bn() {
 
 bool rows16(const Operand &o) { return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0; }
 
+int rows_of_tile(const ProductArgs &a) {
+    return a.B.crossed || a.rows > 64 ? 128 : a.rows > 32 ? 64 : a.rows > 16 ? 32 : 16;
+}
+
+// The depth over as many CTAs as the GPU holds clusters for, each with a set of MMAs at least; then tiles as low as
+// make that many.  GB300, us, one token and 64: 24576 x 1536, 192 tiles of 128 and 280 of 88 14.5 and 13.9, 23 and
+// 15; 7168 x 2048, four CTAs along the depth and two 9.7 and 9.6, 14.0 and 14.8; SwiGLU 2048 x 7168, eight and four
+// 12.4 and 13.3, 16.2 and 17.4.  Of clusters of eight, 32 are at work at a time.
+struct Split {
+    int split, ta;
+    int64_t ctas;
+};
+Split split_of(const ProductArgs &a, int BN, int num_sms) {
+    const int full = act_gated(a.act) ? 64 : 128, boxes = (a.depth + 63) / 64;
+    const int64_t mt = (a.rows + BN - 1) / BN, across = mt * ((a.cols + full - 1) / full);
+    const int64_t held[4] = {2ll * num_sms, 2ll * num_sms, 288ll * num_sms / 152, 256ll * num_sms / 152};
+    int lg = 0;
+    while (lg < 3 && across << (lg + 1) <= held[lg + 1] && boxes >= 4 << (lg + 1)) ++lg;
+    Split s{1 << lg, full, 0};
+    if (!a.A.crossed) {
+        const int64_t most = (lg == 2 ? held[3] : held[lg]) / (s.split * mt);     // tiles along A
+        int ta = full < 64 ? full : 64;
+        while (ta < full && (a.cols + ta - 1) / ta > most) ta += 8;
+        s.ta = ta;
+    }
+    s.ctas = mt * ((a.cols + s.ta - 1) / s.ta) * s.split;
+    return s;
+}
+
 }  // namespace
+
+// About the time of a call with more than 64 rows, in ns: two CTAs share an SM's tensor cores.  GB300, us, as
+// measured and by this: 1024 rows 7168 x 2048 29.7 and 31.6, 24576 x 1536 73.7 and 75.6, 2112 x 7168 (two along the
+// depth) 31.4 and 31.4, 512 rows SwiGLU 2048 x 7168 31.8 and 31.4, 2048 x 2048 (four) 13.4 and 12.2.
+int64_t linear_tc_ns(const ProductArgs &a, int num_sms) {
+    const Split s = split_of(a, 128, num_sms);
+    const int64_t rounds = (s.ctas + 2 * num_sms - 1) / (2 * num_sms), boxes = ((a.depth + 63) / 64 + s.split - 1) / s.split;
+    return rounds * (400 * boxes + 3000) + (s.split > 1 ? 6000 : 0);
+}
 
 bool linear_tc_supported(const ProductArgs &a) { return a.depth >= 1 && rows16(a.A) && rows16(a.B); }
 
@@ -335,8 +415,14 @@ cudaError_t linear_tc_prepare() {
 
 cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream) {
     const bool gated = act_gated(a.act), ax = a.A.crossed, bx = a.B.crossed;
-    const int BN = bx || a.rows > 64 ? 128 : a.rows > 32 ? 64 : a.rows > 16 ? 32 : 16;
-    const int TA = gated ? 64 : 128;
+    const int BN = rows_of_tile(a);
+    Params p{};
+    const Split plan = split_of(a, BN, c.num_sms);
+    p.mt = (a.rows + BN - 1) / BN;
+    p.boxes = (a.depth + 63) / 64;
+    p.split = plan.split;
+    p.ta = plan.ta;
+    const int TA = p.ta;
     Maps maps;
     const int arows = gated ? 2 * a.cols : a.cols;
     if (!(ax ? encode_bf16_2d(&maps.a, a.A.p, a.cols, a.depth, a.A.ld, 64)
@@ -344,16 +430,11 @@ cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_
         !(bx ? encode_bf16_2d(&maps.b, a.B.p, (int)a.rows, a.depth, a.B.ld, 64)
              : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, BN)))
         return cudaErrorInvalidValue;
-    Params p{};
     p.e = epilogue_of(a);
-    p.mt = (a.rows + BN - 1) / BN;
-    p.boxes = (a.depth + 63) / 64;
     p.early = a.early;
     p.status = c.status;
     p.budget_ns = c.budget_ns;
-    const int64_t tiles = p.mt * ((a.cols + TA - 1) / TA);
-    for (p.split = 1; p.split < 8 && tiles * p.split * 2 <= 2 * c.num_sms && p.boxes >= 4 * p.split;) p.split *= 2;
-    const int64_t ctas = tiles * p.split;
+    const int64_t ctas = plan.ctas;
     if (ctas >= 1ll << 31) return cudaErrorInvalidValue;
 #define SKINNY_TC(BNv)                                                              \
     case BNv:                                                                       \
