@@ -129,7 +129,8 @@ skinny_status_t init_device_current(DeviceState &d, int device) {
         stream_prepare() != cudaSuccess || dotprod_f32w_prepare() != cudaSuccess ||
         dotmma_f32w_prepare() != cudaSuccess || tc_prepare() != cudaSuccess ||
         expert_rows_prepare() != cudaSuccess || experts_tc_prepare() != cudaSuccess ||
-        linear_tc_prepare() != cudaSuccess || linear_pair_prepare() != cudaSuccess)
+        linear_tc_prepare() != cudaSuccess || linear_pair_prepare() != cudaSuccess ||
+        heads_prepare() != cudaSuccess)
         return SKINNY_ERR_LAUNCH;
     void *sym = nullptr;
     if (cudaGetSymbolAddress(&sym, g_status_word) != cudaSuccess) return SKINNY_ERR_LAUNCH;

@@ -4,15 +4,17 @@
 //     dx = r h - x r^3 mean(h x),  dw = sum g x r,   g = dy turned back, h = g w
 // Every element is read once and written once: the kernels are a stream through
 // device memory, and what they do beside it has to stay out of its way.
-//   * L lanes hold a head (L a power of two), 32 / L heads a warp; a lane holds
-//     chunks of V elements of both halves of the pairs, so that the rotation
-//     stays within the lane and the only exchange is the sum over the L lanes.
-//     V is the widest piece (16 bytes at most) that sizes, strides and pointers
-//     allow.
+//   * L lanes hold a head, 32 / L heads a warp; a lane holds chunks of V elements
+//     of both halves of the pairs (or of neighbours), so that the rotation stays
+//     within the lane and the only exchange is the sum over the L lanes.  V is the
+//     widest piece (16 bytes at most) that sizes, strides and pointers allow.
 //   * The angles of a token serve all of its heads: a warp takes one token and
-//     walks its heads with cosines, sines and the norm's weight in registers,
-//     kAhead steps of loads in flight.  With few tokens their heads are dealt to
-//     more warps.
+//     walks its heads with the weights and the angles in registers as the two
+//     factors that an element and its partner take, y = r (x p + partner q).
+//     With few tokens their heads are dealt to more warps.
+//   * The loads of the next steps are under way to shared memory (cp.async, each
+//     thread's own slots, so no barrier) while one is computed, and the arithmetic
+//     is in packed pairs of fp32.
 //   * The gradient of the weights is summed in registers over all that a warp
 //     walks, then over the CTA's warps, then over the CTAs by a second kernel:
 //     the order is fixed.
@@ -28,6 +30,95 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPairs = 8;                    // pairs per lane at most
 
+// ------------------------------------------------------------------ V values, two to a register pair
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int V>
+struct Vals {
+    uint64_t p[V / 2];
+    __device__ __forceinline__ void set(const float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) p[i] = pair2(v[2 * i], v[2 * i + 1]);
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) split2(p[i], v[2 * i], v[2 * i + 1]);
+    }
+};
+template <>
+struct Vals<1> {
+    float p[1];
+    __device__ __forceinline__ void set(const float (&v)[1]) { p[0] = v[0]; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = p[0]; }
+};
+template <int V>
+__device__ __forceinline__ Vals<V> vfma(const Vals<V> &a, const Vals<V> &b, const Vals<V> &c) {
+    Vals<V> r;
+    if constexpr (V == 1) {
+        r.p[0] = fmaf(a.p[0], b.p[0], c.p[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.p[i] = fma2(a.p[i], b.p[i], c.p[i]);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> vmul(const Vals<V> &a, const Vals<V> &b) {
+    Vals<V> r;
+    if constexpr (V == 1) {
+        r.p[0] = a.p[0] * b.p[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.p[i] = mul2(a.p[i], b.p[i]);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> vall(float x) {
+    Vals<V> r;
+    if constexpr (V == 1) {
+        r.p[0] = x;
+    } else {
+        const uint64_t two = pair2(x, x);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.p[i] = two;
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ float vsum(const Vals<V> &a) {
+    if constexpr (V == 1) {
+        return a.p[0];
+    } else {
+        uint64_t s = a.p[0];
+#pragma unroll
+        for (int i = 1; i < V / 2; ++i) s = add2(s, a.p[i]);
+        float lo, hi;
+        split2(s, lo, hi);
+        return lo + hi;
+    }
+}
+
+// ------------------------------------------------------------------ V elements of memory
 template <typename E, int V> struct RawOf;
 template <> struct RawOf<uint16_t, 8> { using T = uint4; };
 template <> struct RawOf<uint16_t, 4> { using T = uint2; };
@@ -40,255 +131,486 @@ template <> struct RawOf<float, 1> { using T = float; };
 template <typename E, int V>
 struct Piece {
     using Raw = typename RawOf<E, V>::T;
-    union { Raw raw; E e[V]; };
-    __device__ __forceinline__ void load(const E *p) { raw = __ldcg(reinterpret_cast<const Raw *>(p)); }
-    __device__ __forceinline__ void load_shared(const E *p) { raw = __ldg(reinterpret_cast<const Raw *>(p)); }
+    static constexpr int kWords = sizeof(Raw) < 4 ? 1 : sizeof(Raw) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void put(const Raw &r) {
+        if constexpr (sizeof(Raw) == 2) w[0] = r;
+        else memcpy(w, &r, sizeof(Raw));
+    }
+    __device__ __forceinline__ void load(const E *p) { put(__ldcg(reinterpret_cast<const Raw *>(p))); }
+    __device__ __forceinline__ void load_shared(const E *p) { put(__ldg(reinterpret_cast<const Raw *>(p))); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = E(0);
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (std::is_same<E, float>::value) return e[i];
-        else return bf16_one(e[i]);
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (std::is_same<E, float>::value) return __uint_as_float(w[i]);
+        else return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
     }
-    __device__ __forceinline__ void set(int i, float v) {
-        if constexpr (std::is_same<E, float>::value) e[i] = v;
-        else e[i] = f32_to_bf16_rn(v);
-    }
-    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<Raw *>(p) = raw; }
 };
-
-struct Params {
-    HeadsArgs a;
-    int L;               // lanes per head
-    int chunks, turned;  // chunks of a head, those that are turned
-    int per, units;      // steps per unit, units per token
-};
-
-// Pairs (a[i], b[i]), or neighbours within a and within b, turned by the angles (back: turned back).
-template <int V>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float (&cs)[V], const float (&sn)[V], bool inter,
-                                     bool back)
-{
-    const float f = back ? -1.f : 1.f;
-    if (V > 1 && inter) {
+// The firsts and seconds of the pairs in a lane's two pieces: the pieces themselves, or, INTER, neighbours in both.
+template <typename E, int V, bool INTER>
+__device__ __forceinline__ void unpack(const Piece<E, V> &p, const Piece<E, V> &q, Vals<V> &a, Vals<V> &b) {
+    float va[V], vb[V];
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float c0 = cs[i], s0 = f * sn[i], c1 = cs[V / 2 + i], s1 = f * sn[V / 2 + i];
-            const float u = a[2 * i], v = a[2 * i + 1], x = b[2 * i], y = b[2 * i + 1];
-            a[2 * i] = u * c0 - v * s0;
-            a[2 * i + 1] = v * c0 + u * s0;
-            b[2 * i] = x * c1 - y * s1;
-            b[2 * i + 1] = y * c1 + x * s1;
+    for (int i = 0; i < V; ++i) {
+        if constexpr (INTER && V > 1) {
+            const Piece<E, V> &from = 2 * i < V ? p : q;
+            va[i] = from.at(2 * i % V);
+            vb[i] = from.at(2 * i % V + 1);
+        } else {
+            va[i] = p.at(i);
+            vb[i] = q.at(i);
         }
+    }
+    a.set(va);
+    b.set(vb);
+}
+template <typename E, int V>
+__device__ __forceinline__ void store_piece(E *p, const float (&v)[V]) {
+    using Raw = typename RawOf<E, V>::T;
+    Raw r;
+    if constexpr (std::is_same<E, float>::value) {
+        memcpy(&r, v, sizeof(Raw));
+    } else if constexpr (V == 1) {
+        r = f32_to_bf16_rn(v[0]);
     } else {
+        uint32_t o[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        memcpy(&r, o, sizeof(Raw));
+    }
+    *reinterpret_cast<Raw *>(p) = r;
+}
+template <typename E, int V, bool INTER>
+__device__ __forceinline__ void store_pair(E *y, int ea, int eb, const Vals<V> &a, const Vals<V> &b) {
+    float va[V], vb[V];
+    a.get(va);
+    b.get(vb);
+    if constexpr (INTER && V > 1) {
+        float p[V], q[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float u = a[i], v = b[i], s = f * sn[i];
-            a[i] = u * cs[i] - v * s;
-            b[i] = v * cs[i] + u * s;
+            (2 * i < V ? p : q)[2 * i % V] = va[i];
+            (2 * i < V ? p : q)[2 * i % V + 1] = vb[i];
         }
+        if (ea >= 0) store_piece<E, V>(y + ea, p);
+        if (eb >= 0) store_piece<E, V>(y + eb, q);
+    } else {
+        if (ea >= 0) store_piece<E, V>(y + ea, va);
+        if (eb >= 0) store_piece<E, V>(y + eb, vb);
     }
 }
 
-template <typename E, int V, bool GRAD>
+struct Params {
+    HeadsArgs a;
+    int L;               // lanes per head: 1 to 8, 16 or 32
+    int chunks, turned;  // chunks of a head, those that are turned
+    int table4;          // four entries of a table's row lie on a 16-byte boundary
+    int per[2], units[2];   // heads' steps per unit and units per token, of queries and of keys
+    float inv_d;
+};
+
+// 1 / sqrt(v): the approximation and a Newton step; 0 and infinity keep the approximation's.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v);
+    return v > 0.f && v < __int_as_float(0x7f800000) ? r * (1.5f - 0.5f * v * r * r) : r;
+}
+
+// Pieces of a step of heads under way to shared memory, each thread's own: kDepth steps of them.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__host__ __device__ constexpr int heads_at_once(bool grad) { return grad ? 1 : 2; }     // of a lane, in a step
+__host__ __device__ constexpr int ring_depth(int el, bool grad) { return grad && el == 2 ? 3 : 2; }
+__host__ __device__ constexpr int ring_bytes(int el, bool grad) {
+    return ring_depth(el, grad) * heads_at_once(grad) * (grad ? 4 : 2) * kPairs * el * kThreads;
+}
+
+template <typename E, int V, bool GRAD, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constant__ Params p)
 {
     constexpr int NC = kPairs / V;           // chunks per lane
-    constexpr int kAhead = GRAD ? 2 : 4;     // steps of loads in flight
+    constexpr int kTensors = GRAD ? 2 : 1, M = heads_at_once(GRAD);
+    constexpr int kPieces = M * NC * 2 * kTensors, kBytes = V * (int)sizeof(E);
+    constexpr int kDepth = ring_depth(sizeof(E), GRAD);
+    constexpr bool kAsync = kBytes >= 4;     // what the copies can move; single bf16 elements go through registers
+    using Pc = Piece<E, V>;
+    using Vs = Vals<V>;
+    extern __shared__ __align__(16) uint8_t ring[];
     const HeadsArgs &a = p.a;
     griddep_launch_dependents();
-    griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = p.L, sub = lane & (L - 1), hs = lane / L, HP = 32 / L;
+    const int L = p.L, HP = 32 / L, hs = lane / L, sub = lane - hs * L;
     const int D = a.D, R = a.R, half = R / 2, rest = (D - R + 1) / 2;
-    const bool inter = a.interleaved != 0;
+    // slots that no copy writes stay zero
+    auto slot = [&](int stage, int piece) { return ((stage * kPieces + piece) * kThreads + (int)threadIdx.x) * kBytes; };
+    for (int i = 0; i < kDepth * kPieces; ++i) {
+        Pc z;
+        z.zero();
+        *reinterpret_cast<typename Pc::Raw *>(ring + slot(0, i)) = *reinterpret_cast<const typename Pc::Raw *>(z.w);
+    }
+    griddep_wait();
 
     int ea[NC], eb[NC];                      // elements of the lane's chunks; -1: none
+    uint32_t axes[NC];                       // the axis of each of a chunk's pairs, four bits each; 15: none
+    // pair i of chunk c: neighbours of one piece, then of the other, or element i of both
+    auto pair_of = [&](int c, int i) {
+        return INTER && V > 1 ? (i < V / 2 ? V * c / 2 + i : R / 4 + V * c / 2 + i - V / 2) : V * c + i;
+    };
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        const int c = sub + L * j;
+        const int c = hs < HP ? sub + L * j : p.chunks;
         ea[j] = eb[j] = -1;
+        axes[j] = 0;
         if (c < p.turned) {
-            ea[j] = inter ? 2 * V * c : V * c;
-            eb[j] = inter ? 2 * V * c + V : half + V * c;
+            ea[j] = INTER && V == 1 ? 2 * c : V * c;
+            eb[j] = INTER && V == 1 ? 2 * c + 1 : half + V * c;
+            if (a.pair_axis) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int ax = __ldg(a.pair_axis + pair_of(c, i));
+                    axes[j] |= (uint32_t)(ax >= 0 && ax < a.axes ? ax : 15) << (4 * i);
+                }
+            }
         } else if (c < p.chunks) {
             ea[j] = R + V * (c - p.turned);
             eb[j] = ea[j] + rest;
             if (eb[j] >= D) eb[j] = -1;      // V == 1: the odd last element
         }
     }
-    [[maybe_unused]] float dw[2][NC][2][V];
-    if constexpr (GRAD) {
+    // the sums over a head's lanes, the same in each of them
+    const bool pow2 = (L & (L - 1)) == 0;
+    auto over_head = [&](float (&v)[M]) {
+        if (pow2) {
 #pragma unroll
-        for (int i = 0; i < 2 * NC * 2 * V; ++i) (&dw[0][0][0][0])[i] = 0.f;
-    }
-    auto over_head = [&](float v) {
-        for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        return v;
+            for (int o = 16; o > 0; o >>= 1) {
+                if (o >= L) continue;
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xFFFFFFFFu, v[m], o);
+            }
+            return;
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float t = 0.f;
+            for (int i = 0; i < L; ++i) t += __shfl_sync(0xFFFFFFFFu, v[m], hs * L + i);
+            v[m] = t;
+        }
     };
 
-    const int nq = (a.side[0].H + HP - 1) / HP, nk = (a.side[1].H + HP - 1) / HP, steps = nq + nk;
-    const int64_t all = (int64_t)a.T * p.units;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < all; u += (int64_t)gridDim.x * kWarps) {
-        const int t = (int)(u / p.units), s0 = (int)(u - (int64_t)t * p.units) * p.per, s1 = min(steps, s0 + p.per);
-        float cs[NC][V], sn[NC][V];
+    // The angles of token t: cosines and sines of the lane's pairs, and a bit for each pair that is not turned.
+    constexpr int kRun = INTER && V > 1 ? V / 2 : V;         // pairs that follow each other in the table
+    auto angles = [&](int t, Vs (&cs)[NC], Vs (&sn)[NC]) {
+        uint32_t still = 0;
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
+        for (int j = 0; j < NC; ++j) {
+            cs[j] = vall<V>(1.f);
+            sn[j] = vall<V>(0.f);
+            float cv[V], sv[V];
+            const int c = hs < HP ? sub + L * j : p.chunks;
+            if (c >= p.turned) {
+                still |= ((1u << V) - 1) << (j * V);
+                continue;
+            }
+            int at[V];                       // a pair's position
+            uint32_t last = 16;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                cs[j][i] = 1.f;
-                sn[j][i] = 0.f;
-                const int c = sub + L * j;
-                if (c < p.turned) {
-                    const int pair = V * c + i, ax = a.pair_axis ? __ldg(a.pair_axis + pair) : 0;
-                    const int at = ax >= 0 && ax < a.axes ? __ldg(a.positions + (int64_t)ax * a.T + t) : -1;
-                    if (at >= 0 && at < a.P) {
-                        const float *row = a.table + (int64_t)at * R + pair;
-                        cs[j][i] = __ldg(row);
-                        sn[j][i] = __ldg(row + half);
+                const uint32_t ax = axes[j] >> (4 * i) & 15;
+                if (i > 0 && ax == last) {
+                    at[i] = at[i - 1];
+                } else {
+                    at[i] = ax < 15 ? __ldg(a.positions + (int64_t)ax * a.T + t) : -1;
+                    if (at[i] >= a.P) at[i] = -1;
+                }
+                last = ax;
+            }
+#pragma unroll
+            for (int i = 0; i < V; i += kRun) {
+                bool one = p.table4 && kRun >= 4;
+                if constexpr (kRun >= 4) {
+#pragma unroll
+                    for (int k = 1; k < kRun; ++k) one = one && at[i + k] == at[i];
+                }
+                if (one && at[i] >= 0) {
+                    const float *row = a.table + (int64_t)at[i] * R + pair_of(c, i);
+#pragma unroll
+                    for (int k = 0; k + 4 <= kRun; k += 4) {
+                        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + k));
+                        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + k));
+                        cv[i + k] = c4.x; cv[i + k + 1] = c4.y; cv[i + k + 2] = c4.z; cv[i + k + 3] = c4.w;
+                        sv[i + k] = s4.x; sv[i + k + 1] = s4.y; sv[i + k + 2] = s4.z; sv[i + k + 3] = s4.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kRun; ++k) {
+                        const int pos = at[i + k];
+                        const float *row = a.table + (int64_t)(pos < 0 ? 0 : pos) * R + pair_of(c, i + k);
+                        const float c1 = __ldg(row), s1 = __ldg(row + half);
+                        cv[i + k] = pos >= 0 ? c1 : 1.f;
+                        sv[i + k] = pos >= 0 ? s1 : 0.f;
+                        if (pos < 0) still |= 1u << (j * V + i + k);
                     }
                 }
             }
-        auto walk = [&](auto SIDE, int b0, int b1) {
-            constexpr int side = decltype(SIDE)::value;
-            const HeadsSide &s = a.side[side];
-            float w[NC][2][V];
+            cs[j].set(cv);
+            sn[j].set(sv);
+        }
+        return still;
+    };
+
+    [[maybe_unused]] Vs dw[NC][2];
+    int64_t u = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t stride = (int64_t)gridDim.x * kWarps, first = (int64_t)a.T * p.units[0];
+
+    auto side_units = [&](auto SIDE) {
+        constexpr int side = decltype(SIDE)::value;
+        const HeadsSide &s = a.side[side];
+        const int per = p.per[side], units = p.units[side], steps = (s.H + M * HP - 1) / (M * HP);
+        const int64_t begin = side ? first : 0, end = begin + (int64_t)a.T * units;
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) dw[j][0] = dw[j][1] = vall<V>(0.f);
+        }
+        Pc wa[NC], wb[NC];                   // the norm's weight
+        const bool weighted = a.norm && s.w;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            wa[j].zero();
+            wb[j].zero();
+            if (weighted && ea[j] >= 0) wa[j].load_shared(static_cast<const E *>(s.w) + ea[j]);
+            if (weighted && eb[j] >= 0) wb[j].load_shared(static_cast<const E *>(s.w) + eb[j]);
+        }
+        // the place of the step whose loads go out next, kDepth steps ahead of the one computed
+        int64_t lu = u;
+        int lh = 0, lleft = 0, stage = 0;    // its head and the steps left in its unit
+        const E *lx = nullptr;
+        [[maybe_unused]] const E *ld = nullptr;
+        const int64_t xstep = HP * s.sh, ystep = HP * s.ysh;        // from head to head of a lane
+        [[maybe_unused]] const int64_t dstep = HP * s.dsh;
+        auto unit_at = [&](int64_t v, int &t, int &b0, int &b1) {
+            const int64_t in = v - begin;
+            t = (int)(in / units);
+            b0 = (int)(in - (int64_t)t * units) * per;
+            b1 = min(steps, b0 + per);
+        };
+        auto load_unit = [&] {
+            int t, b0, b1;
+            unit_at(lu, t, b0, b1);
+            lh = b0 * M * HP + hs;
+            lleft = b1 - b0;
+            lx = static_cast<const E *>(s.x) + (int64_t)t * s.st + (int64_t)lh * s.sh;
+            if constexpr (GRAD) ld = static_cast<const E *>(s.d) + (int64_t)t * s.dst + (int64_t)lh * s.dsh;
+        };
+        if (lu < end) load_unit();
+        auto issue = [&](int st) {
+            if (lu < end) {
+                E held[kAsync ? 1 : kPieces];                // all loads out before the first is stored
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int m = i / (NC * 2 * kTensors), q = i / (2 * NC) % kTensors, j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
+                    if (at < 0 || hs >= HP || lh + m * HP >= s.H || (GRAD && q == 0 && !a.norm)) continue;
+                    const E *from = (q ? ld + m * dstep : lx + m * xstep) + at;
+                    if constexpr (kAsync) copy_async<kBytes>(smem_u32(ring + slot(st, i)), from);
+                    else held[i] = __ldcg(from);
+                }
+                if constexpr (!kAsync) {
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int m = i / (NC * 2 * kTensors), q = i / (2 * NC) % kTensors, j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
+                        if (at < 0 || hs >= HP || lh + m * HP >= s.H || (GRAD && q == 0 && !a.norm)) continue;
+                        *reinterpret_cast<E *>(ring + slot(st, i)) = held[i];
+                    }
+                }
+                lh += M * HP;
+                lx += M * xstep;
+                if constexpr (GRAD) ld += M * dstep;
+                if (--lleft == 0) {
+                    lu += stride;
+                    if (lu < end) load_unit();
+                }
+            }
+            if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) issue(i);
+        for (; u < end; u += stride) {
+            int t, b0, b1;
+            unit_at(u, t, b0, b1);
+            Vs cs[NC], sn[NC];
+            const uint32_t still = angles(t, cs, sn);
+            const bool some_still = __any_sync(0xFFFFFFFFu, still != 0);
+            // factors of an element and of its partner, the weights among them (gradients: the angles themselves)
+            [[maybe_unused]] Vs pa[NC], qa[NC], pb[NC], qb[NC];
+            const Vs minus = vall<V>(-1.f);
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                Piece<E, V> pa, pb;
-                pa.zero();
-                pb.zero();
-                const bool has = a.norm && s.w;
-                if (has && ea[j] >= 0) pa.load_shared(static_cast<const E *>(s.w) + ea[j]);
-                if (has && eb[j] >= 0) pb.load_shared(static_cast<const E *>(s.w) + eb[j]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    w[j][0][i] = has ? pa.get(i) : 1.f;
-                    w[j][1][i] = has ? pb.get(i) : 1.f;
+                if constexpr (!GRAD) {
+                    Vs va = vall<V>(1.f), vb = va;
+                    if (weighted) unpack<E, V, INTER>(wa[j], wb[j], va, vb);
+                    pa[j] = vmul(va, cs[j]);
+                    qa[j] = vmul(vmul(vb, sn[j]), minus);
+                    pb[j] = vmul(vb, cs[j]);
+                    qb[j] = vmul(va, sn[j]);
                 }
             }
-            for (int b = b0; b < b1; b += kAhead) {
-                Piece<E, V> x[kAhead][NC][2];
-                [[maybe_unused]] Piece<E, V> d[GRAD ? kAhead : 1][NC][2];
+            // v p + partner q; a pair that is not turned takes nothing of its partner, whatever that is
+            auto turned = [&](int j, const Vs &va, const Vs &vb, Vs &oa, Vs &ob) {
+                Vs ta = vb, tb = va;
+                if (some_still) {
+                    float fa[V], fb[V];
+                    ta.get(fa);
+                    tb.get(fb);
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    const int h = (b + q) * HP + hs;
-                    const bool live = b + q < b1 && h < s.H;
-                    const E *xp = static_cast<const E *>(s.x) + (int64_t)t * s.st + (int64_t)h * s.sh;
-                    [[maybe_unused]] const E *dp = static_cast<const E *>(s.d) + (int64_t)t * s.dst + (int64_t)h * s.dsh;
+                    for (int i = 0; i < V; ++i)
+                        if (still >> (j * V + i) & 1) fa[i] = fb[i] = 0.f;
+                    ta.set(fa);
+                    tb.set(fb);
+                }
+                if constexpr (!GRAD) {
+                    oa = vfma(va, pa[j], vmul(ta, qa[j]));
+                    ob = vfma(vb, pb[j], vmul(tb, qb[j]));
+                } else {
+                    oa = vfma(va, cs[j], vmul(ta, sn[j]));
+                    ob = vfma(vmul(tb, sn[j]), minus, vmul(vb, cs[j]));
+                }
+            };
+            int h = b0 * M * HP + hs;
+            E *y = static_cast<E *>(s.y) + (int64_t)t * s.yst + (int64_t)h * s.ysh;
+            for (int b = b0; b < b1; ++b, h += M * HP, y += M * ystep) {
+                if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory");
+                Pc in[M][kTensors][NC][2];
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    in[i / (NC * 2 * kTensors)][i / (2 * NC) % kTensors][i / 2 % NC][i % 2].put(
+                        *reinterpret_cast<const typename Pc::Raw *>(ring + slot(stage, i)));
+                issue(stage);
+                if (++stage == kDepth) stage = 0;
+                float r[M];
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    r[m] = 1.f;
+                    if (!a.norm) continue;
+                    Vs ss = vall<V>(0.f);
 #pragma unroll
                     for (int j = 0; j < NC; ++j) {
-                        x[q][j][0].zero();
-                        x[q][j][1].zero();
-                        const bool need = live && (!GRAD || a.norm);
-                        if (need && ea[j] >= 0) x[q][j][0].load(xp + ea[j]);
-                        if (need && eb[j] >= 0) x[q][j][1].load(xp + eb[j]);
-                        if constexpr (GRAD) {
-                            d[q][j][0].zero();
-                            d[q][j][1].zero();
-                            if (live && ea[j] >= 0) d[q][j][0].load(dp + ea[j]);
-                            if (live && eb[j] >= 0) d[q][j][1].load(dp + eb[j]);
-                        }
+                        if (L * j >= p.chunks) break;
+                        Vs xa, xb;
+                        unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
+                        ss = vfma(xb, xb, vfma(xa, xa, ss));
                     }
+                    r[m] = vsum(ss);
                 }
+                if (a.norm) {
+                    over_head(r);
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    if (b + q >= b1) break;  // the whole warp
-                    const int h = (b + q) * HP + hs;
-                    float r = 1.f;
-                    if (a.norm) {
-                        float ss = 0.f;
+                    for (int m = 0; m < M; ++m) r[m] = inv_sqrt(fmaf(r[m], p.inv_d, a.eps));
+                }
+                if constexpr (!GRAD) {
 #pragma unroll
-                        for (int j = 0; j < NC; ++j)
+                    for (int m = 0; m < M; ++m) {
+                        const bool live = hs < HP && h + m * HP < s.H;
+                        const Vs rr = vall<V>(r[m]);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const float u0 = x[q][j][0].get(i), u1 = x[q][j][1].get(i);
-                                ss += u0 * u0 + u1 * u1;
-                            }
-                        r = 1.f / sqrtf(over_head(ss) / (float)D + a.eps);
+                        for (int j = 0; j < NC; ++j) {
+                            if (L * j >= p.chunks) break;
+                            Vs xa, xb, oa, ob;
+                            unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
+                            turned(j, xa, xb, oa, ob);
+                            if (live) store_pair<E, V, INTER>(y + m * ystep, ea[j], eb[j], vmul(oa, rr), vmul(ob, rr));
+                        }
                     }
-                    E *y = static_cast<E *>(s.y) + (int64_t)t * s.yst + (int64_t)h * s.ysh;
-                    if constexpr (!GRAD) {
+                } else {
+                    Vs ga[M][NC], gb[M][NC];
+                    float hx[M];
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const bool live = hs < HP && h + m * HP < s.H;
+                        const Vs rr = vall<V>(r[m]);
+                        Vs sum = vall<V>(0.f);
 #pragma unroll
                         for (int j = 0; j < NC; ++j) {
-                            float va[V], vb[V];
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                va[i] = x[q][j][0].get(i) * r * w[j][0][i];
-                                vb[i] = x[q][j][1].get(i) * r * w[j][1][i];
+                            if (L * j >= p.chunks) break;
+                            Vs da, db, xa, xb;
+                            unpack<E, V, INTER>(in[m][kTensors - 1][j][0], in[m][kTensors - 1][j][1], da, db);
+                            turned(j, da, db, ga[m][j], gb[m][j]);
+                            if (!a.norm) continue;
+                            unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
+                            xa = vmul(xa, rr);                   // x r: its part of dw, and of the sum
+                            xb = vmul(xb, rr);
+                            if (live) {
+                                dw[j][0] = vfma(ga[m][j], xa, dw[j][0]);
+                                dw[j][1] = vfma(gb[m][j], xb, dw[j][1]);
                             }
-                            if (R) turn<V>(va, vb, cs[j], sn[j], inter, false);
-                            Piece<E, V> o;
-#pragma unroll
-                            for (int i = 0; i < V; ++i) o.set(i, va[i]);
-                            if (h < s.H && ea[j] >= 0) o.store(y + ea[j]);
-#pragma unroll
-                            for (int i = 0; i < V; ++i) o.set(i, vb[i]);
-                            if (h < s.H && eb[j] >= 0) o.store(y + eb[j]);
+                            if (weighted) {
+                                Vs va, vb;
+                                unpack<E, V, INTER>(wa[j], wb[j], va, vb);
+                                ga[m][j] = vmul(ga[m][j], va);
+                                gb[m][j] = vmul(gb[m][j], vb);
+                            }
+                            sum = vfma(ga[m][j], xa, vfma(gb[m][j], xb, sum));
                         }
-                    } else {
-                        float ga[NC][V], gb[NC][V], hx = 0.f;
+                        hx[m] = vsum(sum);
+                    }
+                    if (a.norm) over_head(hx);
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const bool live = hs < HP && h + m * HP < s.H;
+                        // dx = r (h - x r mean(h x r))
+                        const Vs rr = vall<V>(r[m]), c = vall<V>(-(r[m] * (hx[m] * p.inv_d)));
 #pragma unroll
                         for (int j = 0; j < NC; ++j) {
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                ga[j][i] = d[q][j][0].get(i);
-                                gb[j][i] = d[q][j][1].get(i);
-                            }
-                            if (R) turn<V>(ga[j], gb[j], cs[j], sn[j], inter, true);
+                            if (L * j >= p.chunks) break;
                             if (a.norm) {
-#pragma unroll
-                                for (int i = 0; i < V; ++i) {
-                                    const float xa = x[q][j][0].get(i), xb = x[q][j][1].get(i);
-                                    if (h < s.H) {
-                                        dw[side][j][0][i] += ga[j][i] * xa * r;
-                                        dw[side][j][1][i] += gb[j][i] * xb * r;
-                                    }
-                                    ga[j][i] *= w[j][0][i];
-                                    gb[j][i] *= w[j][1][i];
-                                    hx += ga[j][i] * xa + gb[j][i] * xb;
-                                }
+                                Vs xa, xb;
+                                unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
+                                ga[m][j] = vmul(vfma(xa, c, ga[m][j]), rr);
+                                gb[m][j] = vmul(vfma(xb, c, gb[m][j]), rr);
                             }
-                        }
-                        float m = 0.f;
-                        if (a.norm) m = r * r * r * (over_head(hx) / (float)D);
-#pragma unroll
-                        for (int j = 0; j < NC; ++j) {
-                            Piece<E, V> o;
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                o.set(i, a.norm ? r * ga[j][i] - x[q][j][0].get(i) * m : ga[j][i]);
-                            if (h < s.H && ea[j] >= 0) o.store(y + ea[j]);
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                o.set(i, a.norm ? r * gb[j][i] - x[q][j][1].get(i) * m : gb[j][i]);
-                            if (h < s.H && eb[j] >= 0) o.store(y + eb[j]);
+                            if (live) store_pair<E, V, INTER>(y + m * ystep, ea[j], eb[j], ga[m][j], gb[m][j]);
                         }
                     }
                 }
             }
-        };
-        if (s0 < nq) walk(std::integral_constant<int, 0>{}, s0, min(s1, nq));
-        if (s1 > nq) walk(std::integral_constant<int, 1>{}, max(s0, nq) - nq, s1 - nq);
-    }
+        }
+        if constexpr (kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    };
 
-    if constexpr (GRAD) {
-        if (!a.partial) return;
+    if constexpr (!GRAD) {
+        side_units(std::integral_constant<int, 0>{});
+        side_units(std::integral_constant<int, 1>{});
+    } else {
         __shared__ float part[kWarps][2][SKINNY_MAX_HEAD];
-#pragma unroll
-        for (int side = 0; side < 2; ++side)
+        auto keep = [&](int side) {
+            if (!a.partial) return;
 #pragma unroll
             for (int j = 0; j < NC; ++j)
 #pragma unroll
-                for (int ab = 0; ab < 2; ++ab)
+                for (int ab = 0; ab < 2; ++ab) {
+                    float all[V];
+                    dw[j][ab].get(all);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float v = dw[side][j][ab][i];
-                        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-                        const int e = ab ? eb[j] : ea[j];
-                        if (hs == 0 && e >= 0) part[warp][side][e + i] = v;
+                        float v = all[i];
+                        float t = 0.f;
+                        for (int i2 = 0; i2 < HP; ++i2) t += __shfl_sync(0xFFFFFFFFu, v, sub + i2 * L);
+                        v = t;
+                        // INTER: pair i's first or second, in the piece that holds it
+                        const int e = INTER && V > 1 ? (2 * i < V ? ea[j] : eb[j]) : ab ? eb[j] : ea[j];
+                        const int k = INTER && V > 1 ? 2 * i % V + ab : i;
+                        if (hs == 0 && e >= 0) part[warp][side][e + k] = v;
                     }
+                }
+        };
+        side_units(std::integral_constant<int, 0>{});
+        keep(0);
+        side_units(std::integral_constant<int, 1>{});
+        keep(1);
+        if (!a.partial) return;
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
             const int side = i >= D, e = i - side * D;
@@ -329,24 +651,33 @@ bool rows_lie(const void *p, int64_t st, int64_t sh, int el, int T, int H, int b
     return bits % (uintptr_t)bytes == 0;
 }
 
-template <typename E, bool GRAD>
-cudaError_t launch_as(const Params &p, int V, int ctas, cudaStream_t stream, bool pdl) {
-    Params q = p;
-    void *args[] = {&q};
-    const void *fn;
-    if constexpr (std::is_same<E, float>::value) {
-        fn = V == 4 ? (const void *)heads_kernel<E, 4, GRAD> : V == 2 ? (const void *)heads_kernel<E, 2, GRAD>
-                                                                      : (const void *)heads_kernel<E, 1, GRAD>;
-    } else {
-        fn = V == 8   ? (const void *)heads_kernel<E, 8, GRAD>
-             : V == 4 ? (const void *)heads_kernel<E, 4, GRAD>
-             : V == 2 ? (const void *)heads_kernel<E, 2, GRAD>
-                      : (const void *)heads_kernel<E, 1, GRAD>;
-    }
-    return launch_plain(fn, dim3((unsigned)ctas), kThreads, 0, stream, pdl, args);
+template <typename E, bool GRAD, bool INTER>
+const void *kernel_for(int V) {
+    if constexpr (sizeof(E) == 2)
+        if (V == 8) return (const void *)heads_kernel<E, 8, GRAD, INTER>;
+    return V == 4   ? (const void *)heads_kernel<E, 4, GRAD, INTER>
+           : V == 2 ? (const void *)heads_kernel<E, 2, GRAD, INTER>
+                    : (const void *)heads_kernel<E, 1, GRAD, INTER>;
+}
+template <typename E>
+const void *kernel_for(int V, bool grad, bool inter) {
+    return grad ? (inter ? kernel_for<E, true, true>(V) : kernel_for<E, true, false>(V))
+                : (inter ? kernel_for<E, false, true>(V) : kernel_for<E, false, false>(V));
 }
 
 }  // namespace
+
+cudaError_t heads_prepare() {
+    for (int i = 0; i < 32; ++i) {
+        const bool b16 = i & 1, grad = i & 2, inter = i & 4;
+        const int V = 1 << (i >> 3);
+        if (V == 8 && !b16) continue;
+        const cudaError_t e = cudaFuncSetAttribute(b16 ? kernel_for<uint16_t>(V, grad, inter) : kernel_for<float>(V, grad, inter),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(b16 ? 2 : 4, grad));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stream) {
     const int el = a.b16 ? 2 : 4;
@@ -367,20 +698,41 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
     p.a = a;
     p.turned = a.R / 2 / V;
     p.chunks = p.turned + ((a.D - a.R + 1) / 2 + V - 1) / V;
-    for (p.L = 1; p.L < p.chunks && p.L < 32;) p.L *= 2;
-    const int HP = 32 / p.L, steps = (a.side[0].H + HP - 1) / HP + (a.side[1].H + HP - 1) / HP;
+    // the lanes per head that keep a warp's busiest: the fewest rounds of chunks for its heads, pieces of a head
+    // that are 32 bytes together at least
+    const int NC = kPairs / V;
+    p.L = 32;
+    for (int L : {16, 8, 7, 6, 5, 4, 3, 2, 1}) {
+        if (L * NC < p.chunks || (L * V * el < 32 && L < p.chunks)) continue;
+        const int rounds = (p.chunks + L - 1) / L, best = (p.chunks + p.L - 1) / p.L;
+        if (rounds * (32 / p.L) <= best * (32 / L)) p.L = L;
+    }
+    p.table4 = a.R % (a.interleaved ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
+    p.inv_d = 1.f / (float)a.D;
     // CTAs that an SM holds; a token's heads are dealt to more warps while there are fewer tokens than warps
     const int64_t ctas = 2ll * c.num_sms < kHeadsParts ? 2ll * c.num_sms : kHeadsParts, warps = ctas * kWarps;
-    int64_t per = ((int64_t)a.T * steps + warps - 1) / warps;
-    if (per > steps) per = steps;
-    p.per = (int)per;
-    p.units = (int)((steps + per - 1) / per);
-    const int64_t need = ((int64_t)a.T * p.units + kWarps - 1) / kWarps;
+    const int HP = 32 / p.L;
+    int64_t steps[2], all = 0, units = 0;
+    for (int i = 0; i < 2; ++i) {
+        steps[i] = (a.side[i].H + HP * heads_at_once(a.grad) - 1) / (HP * heads_at_once(a.grad));
+        all += a.T * steps[i];
+    }
+    for (int i = 0; i < 2; ++i) {
+        int64_t per = (all + warps - 1) / warps;
+        if (per > steps[i]) per = steps[i];
+        if (per < 1) per = 1;
+        p.per[i] = (int)per;
+        p.units[i] = (int)((steps[i] + per - 1) / per);
+        units += a.T * (int64_t)p.units[i];
+    }
+    const int64_t need = (units + kWarps - 1) / kWarps;
     const int grid = (int)(need < ctas ? need : ctas);
     const bool sums = a.grad && (a.side[0].dw || a.side[1].dw);
     if (!sums) p.a.partial = nullptr;
-    cudaError_t e = a.b16 ? (a.grad ? launch_as<uint16_t, true>(p, V, grid, stream, c.pdl) : launch_as<uint16_t, false>(p, V, grid, stream, c.pdl))
-                          : (a.grad ? launch_as<float, true>(p, V, grid, stream, c.pdl) : launch_as<float, false>(p, V, grid, stream, c.pdl));
+    const bool inter = a.interleaved != 0;
+    void *kargs[] = {&p};
+    const cudaError_t e = launch_plain(a.b16 ? kernel_for<uint16_t>(V, a.grad, inter) : kernel_for<float>(V, a.grad, inter),
+                                       dim3((unsigned)grid), kThreads, ring_bytes(el, a.grad), stream, c.pdl, kargs);
     if (e != cudaSuccess || !sums) return e;
     const float *partial = a.partial;
     int parts = grid, D = a.D;

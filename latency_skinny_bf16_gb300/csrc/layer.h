@@ -95,6 +95,7 @@ struct HeadsArgs {
     float *partial;          // gradients of the weights: [parts][2][D]
 };
 constexpr int kHeadsParts = 608;
+cudaError_t heads_prepare();
 cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stream);
 
 }  // namespace skinny
