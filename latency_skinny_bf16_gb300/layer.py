@@ -128,20 +128,26 @@ torch = None    # imported by the first call that takes tensors: the C-named fun
 
 
 def _import_torch():
-    global torch
+    global torch, _bf16, _f32, _i32, _device
     if _ex.torch is None:
         _ex._import_torch()
     torch = _ex.torch
+    _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _here(device, *tensors):
-    """The library launches on the current device, so every tensor has to be there."""
-    at = torch.cuda.current_device()
-    if device.index != at:
-        raise ValueError(f"tensors on {device}, and the current device is cuda:{at}")
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"tensors on {device} and on {t.device}")
+def _here(t, name):
+    """The current device, on which the library launches and every tensor has to be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, not on {t.device}")
+    at = _device()
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on {t.device}, and the current device is cuda:{at}")
+    return at
+
+
+def _elsewhere(t, name, at):
+    raise ValueError(f"{name} is on {t.device}, and the other tensors on cuda:{at}")
 
 
 def _act(activation, wrows):
@@ -156,29 +162,36 @@ def _act(activation, wrows):
     return act, wrows
 
 
-def _matrix(t, name, rows, cols, dtype):
+def _matrix(t, name, rows, cols, dtype, at):
     """(address, row stride) of a CUDA matrix of that size; None: (0, 0)."""
     if t is None:
         return 0, 0
+    if t.get_device() != at:
+        _elsewhere(t, name, at)
     m, n, ld = _rows(t, name, dtype)
     if m != rows or n != cols:
         raise ValueError(f"{name} must be {(rows, cols)}, not {(m, n)}")
     return t.data_ptr(), ld
 
 
-def _space(workspace, need, device):
-    """(address, bytes) of a workspace, and the tensor that holds it."""
-    if workspace is None:
-        if need == 0:
-            return 0, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace.data_ptr(), workspace.nbytes, workspace
+def _vector(t, name, n, dtype, at):
+    """Address of a contiguous CUDA tensor of n elements; None: 0."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != at:
+        _elsewhere(t, name, at)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
+    return t.data_ptr()
 
 
-def _vector(t, name, n, dtype):
-    return 0 if t is None else _ex._flat(t, name, n, dtype)
+def _space(workspace, at):
+    """(address, bytes) of a workspace."""
+    if workspace.get_device() != at or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def linear_workspace(x, w, activation=None):
@@ -204,27 +217,30 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, pre=None, 
     if stream is not None:
         with _ex._on(stream, x.device):
             return linear(x, w, bias, activation, residual, out, pre, workspace)
-    bf16 = torch.bfloat16
-    M, K, ldx = _rows(x, "x", bf16)
-    wrows, wcols, ldw = _rows(w, "w", bf16)
+    at = _here(x, "x")
+    M, K, ldx = _rows(x, "x", _bf16)
+    wrows, wcols, ldw = _rows(w, "w", _bf16)
     if wcols != K:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    if w.get_device() != at:
+        _elsewhere(w, "w", at)
     act, N = _act(activation, wrows)
     if out is None:
-        out = torch.empty((M, N), dtype=bf16 if residual is None else residual.dtype, device=x.device)
-    yp, ldy = _matrix(out, "out", M, N, None)
-    rp, ldr = _matrix(residual, "residual", M, N, out.dtype)
-    zp, ldz = _matrix(pre, "pre", M, wrows, bf16)
-    bp = _vector(bias, "bias", wrows, bf16)
+        out = torch.empty((M, N), dtype=_bf16 if residual is None else residual.dtype, device=x.device)
+    yp, ldy = _matrix(out, "out", M, N, None, at)
+    rp, ldr = _matrix(residual, "residual", M, N, out.dtype, at)
+    zp, ldz = _matrix(pre, "pre", M, wrows, _bf16, at)
+    bp = _vector(bias, "bias", wrows, _bf16, at)
     ot = _ex._dtype(out, "out")
     xp, wp = x.data_ptr(), w.data_ptr()
     lib = _lib()
+    sp = sb = 0
     if workspace is None:
-        need = lib.skinny_linear_workspace(xp, ldx, wp, ldw, M, N, K, act)
-    else:
-        need = 0
-    _here(x.device, w, bias, residual, out, pre, workspace)
-    sp, sb, workspace = _space(workspace, need, x.device)
+        need = lib.skinny_linear_workspace(xp, ldx, wp, ldw, M, N, K, act) if M > 64 else 0
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        sp, sb = _space(workspace, at)
     st = lib.skinny_linear_bf16(xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz, M, N, K, act, ot, sp, sb,
                                 _ex._current(x.device))
     if st:
@@ -255,36 +271,37 @@ def linear_grad(dy, x, w, pre=None, activation=None, dx=None, dw=None, dbias=Non
     if stream is not None:
         with _ex._on(stream, dy.device):
             return linear_grad(dy, x, w, pre, activation, dx, dw, dbias, input_grad, weight_grad, bias_grad, workspace)
-    bf16 = torch.bfloat16
-    M, K, ldx = _rows(x, "x", bf16)
-    wrows, wcols, ldw = _rows(w, "w", bf16)
+    at = _here(dy, "dy")
+    M, K, ldx = _rows(x, "x", _bf16)
+    wrows, wcols, ldw = _rows(w, "w", _bf16)
     if wcols != K:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    for t, name in ((x, "x"), (w, "w")):
+        if t.get_device() != at:
+            _elsewhere(t, name, at)
     act, N = _act(activation, wrows)
-    yp, lddy = _matrix(dy, "dy", M, N, bf16)
+    yp, lddy = _matrix(dy, "dy", M, N, _bf16, at)
     if act and pre is None:
         raise ValueError(f"{activation} needs pre, what the forward pass kept")
-    zp, ldz = _matrix(pre, "pre", M, wrows, bf16) if act else (0, 0)
+    zp, ldz = _matrix(pre, "pre", M, wrows, _bf16, at) if act else (0, 0)
     for wanted, t, name in ((input_grad, dx, "dx"), (weight_grad, dw, "dw"), (bias_grad, dbias, "dbias")):
         if not wanted and t is not None:
             raise ValueError(f"{name} is given, and not asked for")
     if input_grad and dx is None:
-        dx = torch.empty((M, K), dtype=bf16, device=dy.device)
+        dx = torch.empty((M, K), dtype=_bf16, device=dy.device)
     if weight_grad and dw is None:
-        dw = torch.empty((wrows, K), dtype=bf16, device=dy.device)
+        dw = torch.empty((wrows, K), dtype=_bf16, device=dy.device)
     if bias_grad and dbias is None:
-        dbias = torch.empty(wrows, dtype=torch.float32, device=dy.device)
-    gxp, lddx = _matrix(dx, "dx", M, K, bf16)
-    gwp, lddw = _matrix(dw, "dw", wrows, K, bf16)
-    gbp = _vector(dbias, "dbias", wrows, torch.float32)
+        dbias = torch.empty(wrows, dtype=_f32, device=dy.device)
+    gxp, lddx = _matrix(dx, "dx", M, K, _bf16, at)
+    gwp, lddw = _matrix(dw, "dw", wrows, K, _bf16, at)
+    gbp = _vector(dbias, "dbias", wrows, _f32, at)
     xp, wp = x.data_ptr(), w.data_ptr()
     lib = _lib()
     if workspace is None:
-        need = lib.skinny_linear_grad_workspace(yp, lddy, xp, ldx, wp, ldw, M, N, K, act)
-    else:
-        need = 0
-    _here(x.device, dy, w, pre if act else None, dx, dw, dbias, workspace)
-    sp, sb, workspace = _space(workspace, need, dy.device)
+        workspace = torch.empty(lib.skinny_linear_grad_workspace(yp, lddy, xp, ldx, wp, ldw, M, N, K, act),
+                                dtype=torch.uint8, device=dy.device)
+    sp, sb = _space(workspace, at)
     st = lib.skinny_linear_grad_bf16(yp, lddy, xp, ldx, wp, ldw, zp, ldz, gxp, lddx, gwp, lddw, gbp, M, N, K, act, sp, sb,
                                      _ex._current(dy.device))
     if st:
@@ -292,55 +309,62 @@ def linear_grad(dy, x, w, pre=None, activation=None, dx=None, dw=None, dbias=Non
     return dx, dw, dbias
 
 
-def _view(t, name, like=None):
-    """(T, H, D, token stride, head stride) of CUDA heads with unit stride along D."""
+def _view(t, name, at, shape=None, dtype=None):
+    """(address, token stride, head stride) of CUDA heads [T, H, D] with unit stride along D."""
     if t is None:
         raise ValueError(f"{name} is missing")
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, D], not {tuple(t.shape)} on {t.device}")
-    T, H, D = t.shape
+    if shape is not None and (t.shape != shape or t.dtype is not dtype):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != at:
+        _elsewhere(t, name, at)
     st, sh, one = t.stride()
-    if D > 1 and one != 1:
+    if one != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} needs unit stride along its last dimension")
-    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype):
-        raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, not {t.dtype} {tuple(t.shape)}")
-    if (T | H) >> 31:
-        _fits_int(name, T, H)
-    return T, H, D, st, sh
+    return t.data_ptr(), st, sh
 
 
 def _heads(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved):
-    """The header's structures for these tensors, and (T, D, dtype, norm, eps)."""
-    T, Hq, D, st, sh = _view(q, "q")
+    """The header's structures for these tensors, and (T, D, dtype, norm, eps, device)."""
+    at = _here(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, D], not {tuple(q.shape)}")
+    T, Hq, D = q.shape
+    dtype = q.dtype
     dt = _ex._dtype(q, "q")
-    norm = eps is not None
-    if not norm and (q_weight is not None or k_weight is not None):
+    if eps is None and (q_weight is not None or k_weight is not None):
         raise ValueError("weights are given, and no eps: without eps there is no norm")
-    hq = skinny_heads_t(q.data_ptr(), st, sh, _vector(q_weight, "q_weight", D, q.dtype), Hq)
+    p, st, sh = _view(q, "q", at)
+    hq = skinny_heads_t(p, st, sh, _vector(q_weight, "q_weight", D, dtype, at), Hq)
     if k is None:
         if k_weight is not None:
             raise ValueError("k_weight is given, and no k")
-        hk = skinny_heads_t(0, 0, 0, 0, 0)
+        hk = skinny_heads_t()
     else:
-        Tk, Hk, Dk, st, sh = _view(k, "k")
-        if Tk != T or Dk != D or k.dtype is not q.dtype:
-            raise ValueError(f"shape mismatch: q {q.dtype} {tuple(q.shape)}, k {k.dtype} {tuple(k.shape)}")
-        hk = skinny_heads_t(k.data_ptr(), st, sh, _vector(k_weight, "k_weight", D, q.dtype), Hk)
+        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype is not dtype:
+            raise ValueError(f"shape mismatch: q {dtype} {tuple(q.shape)}, k {k.dtype} {tuple(k.shape)}")
+        p, st, sh = _view(k, "k", at)
+        Hk = k.shape[1]
+        if Hk >> 31:
+            _fits_int("k", Hk)
+        hk = skinny_heads_t(p, st, sh, _vector(k_weight, "k_weight", D, dtype, at), Hk)
+    if (T | Hq) >> 31:
+        _fits_int("q", T, Hq)
     if table is None:
         rot = skinny_rotation_t(0, 1, 0, 0, 1, 0, 0)
     else:
         if table.dim() != 2 or positions is None:
             raise ValueError("a table [positions, R] goes with the tokens' positions")
         P, R = table.shape
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dim() not in (1, 2):
+        d = positions.dim()
+        axes = 1 if d == 1 else positions.shape[0]
+        if d != 1 and d != 2:
             raise ValueError(f"positions must be [tokens] or [axes, tokens], not {tuple(positions.shape)}")
-        if R >> 31:
-            _fits_int("table", R)
-        rot = skinny_rotation_t(_vector(table, "table", P * R, torch.float32), P,
-                                _vector(positions, "positions", axes * T, torch.int32),
-                                _vector(pair_axis, "pair_axis", R // 2, torch.int32), axes, R, 1 if interleaved else 0)
-    return hq, hk, rot, T, D, dt, 1 if norm else 0, eps if norm else 0.0
+        if (R | axes) >> 31:
+            _fits_int("table", R, axes)
+        rot = skinny_rotation_t(_vector(table, "table", P * R, _f32, at), P,
+                                _vector(positions, "positions", axes * T, _i32, at),
+                                _vector(pair_axis, "pair_axis", R // 2, _i32, at), axes, R, 1 if interleaved else 0)
+    return hq, hk, rot, T, D, dt, at
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, table=None, positions=None, eps=1e-6, pair_axis=None,
@@ -360,20 +384,18 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, table=None, positions=None,
     if stream is not None:
         with _ex._on(stream, q.device):
             return qk_norm_rope(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved, q_out, k_out)
-    hq, hk, rot, T, D, dt, norm, e = _heads(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved)
+    hq, hk, rot, T, D, dt, at = _heads(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _, _, _, qst, qsh = _view(q_out, "q_out", q)
+    qp, qst, qsh = _view(q_out, "q_out", at, q.shape, q.dtype)
     kp = kst = ksh = 0
     if k is not None:
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _, _, _, kst, ksh = _view(k_out, "k_out", k)
-        kp = k_out.data_ptr()
+        kp, kst, ksh = _view(k_out, "k_out", at, k.shape, k.dtype)
     elif k_out is not None:
         raise ValueError("k_out is given, and no k")
-    _here(q.device, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out)
-    st = _lib().skinny_qk_norm_rope(hq, hk, rot, T, D, norm, e, dt, q_out.data_ptr(), qst, qsh, kp, kst, ksh,
+    st = _lib().skinny_qk_norm_rope(hq, hk, rot, T, D, eps is not None, eps or 0.0, dt, qp, qst, qsh, kp, kst, ksh,
                                     _ex._current(q.device))
     if st:
         _refused(st, "skinny_qk_norm_rope")
@@ -400,37 +422,36 @@ def qk_norm_rope_grad(dq, dk, q, k, q_weight=None, k_weight=None, table=None, po
         with _ex._on(stream, q.device):
             return qk_norm_rope_grad(dq, dk, q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved,
                                      dq_in, dk_in, dq_weight, dk_weight, weight_grad, workspace)
-    hq, hk, rot, T, D, dt, norm, e = _heads(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved)
-    _, _, _, dqst, dqsh = _view(dq, "dq", q)
+    hq, hk, rot, T, D, dt, at = _heads(q, k, q_weight, k_weight, table, positions, eps, pair_axis, interleaved)
+    dqp, dqst, dqsh = _view(dq, "dq", at, q.shape, q.dtype)
     if dq_in is None:
         dq_in = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _, _, _, qst, qsh = _view(dq_in, "dq_in", q)
+    qp, qst, qsh = _view(dq_in, "dq_in", at, q.shape, q.dtype)
     dkp = dkst = dksh = kp = kst = ksh = 0
     if k is not None:
-        _, _, _, dkst, dksh = _view(dk, "dk", k)
+        dkp, dkst, dksh = _view(dk, "dk", at, k.shape, k.dtype)
         if dk_in is None:
             dk_in = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _, _, _, kst, ksh = _view(dk_in, "dk_in", k)
-        dkp, kp = dk.data_ptr(), dk_in.data_ptr()
+        kp, kst, ksh = _view(dk_in, "dk_in", at, k.shape, k.dtype)
     elif dk is not None or dk_in is not None or dk_weight is not None:
         raise ValueError("gradients of keys are given, and no k")
-    _here(q.device, dq, dk, k, q_weight, k_weight, table, positions, pair_axis, dq_in, dk_in, dq_weight, dk_weight, workspace)
     wqp = wkp = sp = sb = 0
+    norm = eps is not None
     if norm and weight_grad:
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=torch.float32, device=q.device)
-        wqp = _vector(dq_weight, "dq_weight", D, torch.float32)
+            dq_weight = torch.empty(D, dtype=_f32, device=q.device)
+        wqp = _vector(dq_weight, "dq_weight", D, _f32, at)
         if k is not None:
             if dk_weight is None:
-                dk_weight = torch.empty(D, dtype=torch.float32, device=q.device)
-            wkp = _vector(dk_weight, "dk_weight", D, torch.float32)
-        need = 0 if workspace is not None else skinny_qk_norm_rope_grad_workspace(T, hq.H, hk.H, D)
-        sp, sb, workspace = _space(workspace, need, q.device)
+                dk_weight = torch.empty(D, dtype=_f32, device=q.device)
+            wkp = _vector(dk_weight, "dk_weight", D, _f32, at)
+        if workspace is None:
+            workspace = torch.empty(skinny_qk_norm_rope_grad_workspace(T, hq.H, hk.H, D), dtype=torch.uint8, device=q.device)
+        sp, sb = _space(workspace, at)
     elif dq_weight is not None or dk_weight is not None:
         raise ValueError("a weight's gradient is given, and not asked for")
-    st = _lib().skinny_qk_norm_rope_grad(dq.data_ptr(), dqst, dqsh, dkp, dkst, dksh, hq, hk, rot, T, D, norm, e, dt,
-                                         dq_in.data_ptr(), qst, qsh, kp, kst, ksh, wqp, wkp, sp, sb,
-                                         _ex._current(q.device))
+    st = _lib().skinny_qk_norm_rope_grad(dqp, dqst, dqsh, dkp, dkst, dksh, hq, hk, rot, T, D, norm, eps or 0.0, dt, qp, qst,
+                                         qsh, kp, kst, ksh, wqp, wkp, sp, sb, _ex._current(q.device))
     if st:
         _refused(st, "skinny_qk_norm_rope_grad")
     return dq_in, dk_in, dq_weight, dk_weight
