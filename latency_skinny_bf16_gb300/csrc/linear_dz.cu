@@ -40,10 +40,10 @@ struct Cols {
     }
 };
 
-template <int V, bool GATED>
-__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const __grid_constant__ LinearDzArgs p)
+template <int V, bool GATED, int ACT>      // ACT: 0 none, 1 SiLU, 2 GELU
+__global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_constant__ LinearDzArgs p)
 {
-    constexpr int G = GATED ? 2 : 1;
+    constexpr int G = GATED ? 2 : 1, kBatch = 4;     // rows whose loads go out together
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
@@ -51,38 +51,46 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const __grid_consta
     const int64_t m0 = p.M * blockIdx.y / gridDim.y, m1 = p.M * (blockIdx.y + 1) / gridDim.y;
     float sum[G][V] = {};
     if (n < p.N) {
-#pragma unroll 2
-        for (int64_t m = m0 + row; m < m1; m += kRows) {
-            Cols<V> dy, z[G];
-            dy.load(p.dY + m * p.lddy + n);
-            if (p.Z) {
+        for (int64_t mb = m0 + row; mb < m1; mb += kBatch * kRows) {
+            Cols<V> dy[kBatch], z[kBatch][G];
 #pragma unroll
-                for (int g = 0; g < G; ++g) z[g].load(p.Z + m * p.ldz + (int64_t)g * p.N + n);
-            }
-            float d[G][V];
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t m = min(mb + k * kRows, m1 - 1);
+                dy[k].load(p.dY + m * p.lddy + n);
+                if constexpr (ACT != 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float y = bf16_one(dy.e[i]);
-                d[0][i] = y;
-                if (p.Z) {
-                    float a, da;
-                    act_both(p.act, bf16_one(z[0].e[i]), a, da);
-                    d[0][i] = y * da;
-                    if constexpr (GATED) {
-                        d[0][i] = y * bf16_one(z[G - 1].e[i]) * da;
-                        d[G - 1][i] = y * a;
-                    }
+                    for (int g = 0; g < G; ++g) z[k][g].load(p.Z + m * p.ldz + (int64_t)g * p.N + n);
                 }
             }
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                Cols<V> o;
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t m = mb + k * kRows;
+                if (m >= m1) break;
+                Cols<V> o[G];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sum[g][i] += d[g][i];
-                    o.e[i] = f32_to_bf16_rn(d[g][i]);
+                    float d[G];
+                    const float y = bf16_one(dy[k].e[i]);
+                    d[0] = y;
+                    if constexpr (ACT != 0) {
+                        float a, da;
+                        act_both<ACT == 2>(bf16_one(z[k][0].e[i]), a, da);
+                        d[0] = y * da;
+                        if constexpr (GATED) {
+                            d[0] = y * bf16_one(z[k][G - 1].e[i]) * da;
+                            d[G - 1] = y * a;
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        sum[g][i] += d[g];
+                        o[g].e[i] = f32_to_bf16_rn(d[g]);
+                    }
                 }
-                if (p.dZ) o.store(p.dZ + m * p.lddz + (int64_t)g * p.N + n);
+                if (p.dZ) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) o[g].store(p.dZ + m * p.lddz + (int64_t)g * p.N + n);
+                }
             }
         }
     }
@@ -118,6 +126,17 @@ __global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float *partia
     out[i] = v;
 }
 
+template <int V>
+const void *kernel_for(int act) {
+    switch (act) {
+        case SKINNY_ACT_SILU: return (const void *)linear_dz_kernel<V, false, 1>;
+        case SKINNY_ACT_GELU: return (const void *)linear_dz_kernel<V, false, 2>;
+        case SKINNY_ACT_SWIGLU: return (const void *)linear_dz_kernel<V, true, 1>;
+        case SKINNY_ACT_GEGLU: return (const void *)linear_dz_kernel<V, true, 2>;
+        default: return (const void *)linear_dz_kernel<V, false, 0>;
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream_t stream) {
@@ -128,8 +147,7 @@ cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream
     const int64_t parts = (a.M + kRows - 1) / kRows < kDbiasParts ? (a.M + kRows - 1) / kRows : kDbiasParts;
     LinearDzArgs p = a;
     void *args[] = {&p};
-    const void *fn = gated ? (wide ? (const void *)linear_dz_kernel<8, true> : (const void *)linear_dz_kernel<1, true>)
-                           : (wide ? (const void *)linear_dz_kernel<8, false> : (const void *)linear_dz_kernel<1, false>);
+    const void *fn = wide ? kernel_for<8>(a.act) : kernel_for<1>(a.act);
     cudaError_t e = launch_plain(fn, dim3((unsigned)((a.N + 32 * V - 1) / (32 * V)), (unsigned)parts), kThreads, 0, stream, c.pdl, args);
     if (e != cudaSuccess || !a.dbias) return e;
     const float *partial = a.partial;
