@@ -52,18 +52,17 @@ typedef enum {
  *         shared with a call that may run at the same time; NULL where that is 0
  *   M >= 0; 0 <= N, K <= 2^20.  M or N 0: no-op.  K 0: the empty sum.
  *
- * Rows that are not 16-byte aligned (pointer, ldx, ldw multiples of 8 elements) are taken too; with
- * more than 64 tokens they are laid out in the workspace first.
+ * Rows that are not 16-byte aligned (pointer, ldx, ldw multiples of 8 elements) are taken too: they are
+ * laid out in the workspace first, which is 0 bytes without such rows.
  *
  * With PDL on (SKINNY_OPT_PDL), W is read before the kernel waits for the preceding kernel in the
  * stream, as in skinny_gemm_bf16.
  *
  * SKINNY_OPT_FORCE_BACKEND, also for the products of the backward pass: SKINNY_BACKEND_TCGEN05 is the
- * kernel by pairs of SMs, SKINNY_BACKEND_SPLITK the one with the depth split over a cluster
- * (UNSUPPORTED where rows are not aligned and not laid out), SKINNY_BACKEND_DOTPROD the one for any rows.
+ * kernel by pairs of SMs, SKINNY_BACKEND_SPLITK the one with the depth split over a cluster.
  *
  * Errors: INVALID_VALUE (sizes, strides, NULL, act, dtype, overlap, workspace too small), UNSUPPORTED
- * (N or K too large, a forced kernel that cannot), MISALIGNED (a pointer not aligned to its element, the workspace), NO_DEVICE, LAUNCH.
+ * (N or K too large), MISALIGNED (a pointer not aligned to its element, the workspace), NO_DEVICE, LAUNCH.
  */
 SKINNY_API skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W, int ldw,
                                               const uint16_t *bias, const void *R, int ldr, void *Y, int ldy,

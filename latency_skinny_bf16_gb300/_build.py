@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "dotprod.cu", "dotprod_f32w.cu", "dotmma.cu", "dotmma_f32w.cu", "splitk.cu", "stream.cu",
            "topk.cu", "rmsnorm.cu", "tmem_gemm.cu", "expert_rows.cu", "experts_api.cu",
-           "experts_mma.cu", "experts_tc.cu", "lora.cu", "layer_api.cu", "linear_any.cu", "linear_dz.cu", "linear_tc.cu", "linear_pair.cu", "rows_pack.cu", "heads.cu"]
+           "experts_mma.cu", "experts_tc.cu", "lora.cu", "layer_api.cu", "linear_empty.cu", "linear_dz.cu", "linear_tc.cu", "linear_pair.cu", "rows_pack.cu", "heads.cu"]
 HEADERS = ["common.cuh", "internal.h", "tuning_table.inc", "tma.cuh", "dotmma_f32w.h", "expert_rows.h", "experts_gemm.h",
            "mma_rows.cuh", "tcgen05.cuh", "tma_stack.cuh", "calls.h", "ranges.h", "layer.h", "act.cuh", "product.cuh"]
 

@@ -32,11 +32,10 @@ struct ProductArgs {
     int out_bf16;
     bool early;              // A is a weight that no preceding kernel of the stream writes
 };
-// CUDA cores, operands of any strides and alignment (linear_any.cu)
-cudaError_t launch_product_any(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
+// a depth of 0 (linear_empty.cu)
+cudaError_t launch_linear_empty(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
 
 // tcgen05 (linear_tc.cu): 16-byte aligned rows, a depth of 1 at least
-bool linear_tc_supported(const ProductArgs &a);
 cudaError_t linear_tc_prepare();
 int64_t linear_tc_ns(const ProductArgs &a, int num_sms);
 cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);

@@ -19,7 +19,6 @@ skinny_status_t check_product(int M, int N, int K, int act) {
 }
 
 bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
-constexpr int kPackedM = 64;      // rows above which unaligned operands are laid out first
 
 // Where the pieces of a call lie in its workspace (-1: not used).
 struct Space {
@@ -32,7 +31,7 @@ struct Space {
 };
 Space linear_space(const void *X, int ldx, const void *W, int ldw, int M, int K, int rows) {
     Space s;
-    if (M <= kPackedM || K == 0) return s;
+    if (K == 0) return s;
     if (!rows16(X, ldx)) s.x = s.take((int64_t)M * pad8(K) * 2);
     if (!rows16(W, ldw)) s.w = s.take((int64_t)rows * pad8(K) * 2);
     return s;
@@ -48,11 +47,10 @@ Space grad_space(const void *dY, int lddy, const void *X, int ldx, const void *W
 }
 
 skinny_status_t launch_product(const ProductArgs &a, const CallCtx &c, cudaStream_t s) {
-    const bool tc = linear_tc_supported(a);
-    if (c.force_backend == SKINNY_BACKEND_TCGEN05) return tc ? launched(launch_linear_pair(a, c, s)) : SKINNY_ERR_UNSUPPORTED;
-    if (c.force_backend == SKINNY_BACKEND_SPLITK) return tc ? launched(launch_linear_tc(a, c, s)) : SKINNY_ERR_UNSUPPORTED;
-    if (c.force_backend == SKINNY_BACKEND_DOTPROD || !tc) return launched(launch_product_any(a, c, s));
-    return launched(linear_pair_faster(a, c.num_sms) ? launch_linear_pair(a, c, s) : launch_linear_tc(a, c, s));
+    if (a.depth == 0) return launched(launch_linear_empty(a, c, s));
+    const bool pair = c.force_backend == SKINNY_BACKEND_TCGEN05 ||
+                      (c.force_backend != SKINNY_BACKEND_SPLITK && linear_pair_faster(a, c.num_sms));
+    return launched(pair ? launch_linear_pair(a, c, s) : launch_linear_tc(a, c, s));
 }
 
 // [T, H] rows of D elements, strides st and sh.

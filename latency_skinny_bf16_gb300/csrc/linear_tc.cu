@@ -360,8 +360,6 @@ cudaError_t prepare_bn() {
     return e;
 }
 
-bool rows16(const Operand &o) { return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0; }
-
 int rows_of_tile(const ProductArgs &a) {
     return a.B.crossed || a.rows > 64 ? 128 : a.rows > 32 ? 64 : a.rows > 16 ? 32 : 16;
 }
@@ -401,8 +399,6 @@ int64_t linear_tc_ns(const ProductArgs &a, int num_sms) {
     const int64_t rounds = (s.ctas + 2 * num_sms - 1) / (2 * num_sms), boxes = ((a.depth + 63) / 64 + s.split - 1) / s.split;
     return rounds * (400 * boxes + 3000) + (s.split > 1 ? 6000 : 0);
 }
-
-bool linear_tc_supported(const ProductArgs &a) { return a.depth >= 1 && rows16(a.A) && rows16(a.B); }
 
 cudaError_t linear_tc_prepare() {
     cudaError_t e = prepare_bn<16>();

@@ -52,10 +52,6 @@ inline Epilogue epilogue_of(const ProductArgs &a) {
     return {a.bias, a.R, a.ldr, a.Y, a.ldy, a.Z, a.ldz, a.rows, a.cols, a.act, a.out_bf16};
 }
 
-__device__ __forceinline__ float residual_at(const Epilogue &e, int64_t r, int n) {
-    return e.out_bf16 ? bf16_one(ldg_u16(static_cast<const uint16_t *>(e.R) + r * e.ldr + n))
-                      : __ldcg(static_cast<const float *>(e.R) + r * e.ldr + n);
-}
 // ---- the epilogue of N rows of one output, from registers.  Each step by itself, its types and pointers
 // settled outside its loop, so that loads go out together and a row costs a step of a pointer.
 template <typename T>
@@ -114,23 +110,6 @@ __device__ __forceinline__ void out_rows(const Epilogue &e, float (&v)[N], int64
         if (e.R) add_rows(v, static_cast<const float *>(e.R) + r * e.ldr + n, e.ldr, live);
         store_rows(v, static_cast<float *>(e.Y) + r * e.ldy + n, e.ldy, live);
     }
-}
-
-// Output n of row r from its sum (gated: with the sum of its up).
-template <bool GATED>
-__device__ __forceinline__ void finish(const Epilogue &e, int64_t r, int n, float z, float up) {
-    if (e.bias) {
-        z += bf16_one(ldg_u16(e.bias + n));
-        if (GATED) up += bf16_one(ldg_u16(e.bias + e.cols + n));
-    }
-    if (e.Z) {
-        e.Z[r * e.ldz + n] = f32_to_bf16_rn(z);
-        if (GATED) e.Z[r * e.ldz + e.cols + n] = f32_to_bf16_rn(up);
-    }
-    float y = act_value(e.act, z);
-    if (GATED) y *= up;
-    if (e.R) y += residual_at(e, r, n);
-    store_y(e.Y, e.out_bf16, r * e.ldy + n, y);
 }
 
 }  // namespace skinny

@@ -236,9 +236,9 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, pre=None, 
     lib = _lib()
     sp = sb = 0
     if workspace is None:
-        need = lib.skinny_linear_workspace(xp, ldx, wp, ldw, M, N, K, act) if M > 64 else 0
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if (xp | wp) & 15 or (ldx | ldw) & 7:        # else none is needed
+            workspace = torch.empty(lib.skinny_linear_workspace(xp, ldx, wp, ldw, M, N, K, act), dtype=torch.uint8,
+                                    device=x.device)
     if workspace is not None:
         sp, sb = _space(workspace, at)
     st = lib.skinny_linear_bf16(xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz, M, N, K, act, ot, sp, sb,

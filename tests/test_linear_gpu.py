@@ -272,7 +272,7 @@ def test_grad_far_values(act):
 
 # ------------------------------------------------------------------ each kernel
 
-KERNELS = {"pair": sk.SKINNY_BACKEND_TCGEN05, "split": sk.SKINNY_BACKEND_SPLITK, "any": sk.SKINNY_BACKEND_DOTPROD}
+KERNELS = {"pair": sk.SKINNY_BACKEND_TCGEN05, "split": sk.SKINNY_BACKEND_SPLITK}
 
 
 @pytest.mark.parametrize("kernel", list(KERNELS))
