@@ -8,10 +8,9 @@
 //     of both halves of the pairs (or of neighbours), so that the rotation stays
 //     within the lane and the only exchange is the sum over the L lanes.  V is the
 //     widest piece (16 bytes at most) that sizes, strides and pointers allow.
-//   * The angles of a token serve all of its heads: a warp takes one token and
-//     walks its heads with the weights and the angles in registers as the two
-//     factors that an element and its partner take, y = r (x p + partner q).
-//     With few tokens their heads are dealt to more warps.
+//   * The angles of a token serve all of its heads: a warp walks an even share of
+//     all heads, token by token, with the weights and the angles in registers as
+//     the two factors that an element and its partner take, y = r (x p + partner q).
 //   * The loads of the next steps are under way to shared memory (cp.async, each
 //     thread's own slots, so no barrier) while one is computed, and the arithmetic
 //     is in packed pairs of fp32.
@@ -154,7 +153,7 @@ __device__ __forceinline__ void unpack(const Piece<E, V> &p, const Piece<E, V> &
     float va[V], vb[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if constexpr (INTER && V > 1) {
+        if constexpr (INTER) {
             const Piece<E, V> &from = 2 * i < V ? p : q;
             va[i] = from.at(2 * i % V);
             vb[i] = from.at(2 * i % V + 1);
@@ -188,7 +187,7 @@ __device__ __forceinline__ void store_pair(E *y, int ea, int eb, const Vals<V> &
     float va[V], vb[V];
     a.get(va);
     b.get(vb);
-    if constexpr (INTER && V > 1) {
+    if constexpr (INTER) {
         float p[V], q[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -206,9 +205,8 @@ __device__ __forceinline__ void store_pair(E *y, int ea, int eb, const Vals<V> &
 struct Params {
     HeadsArgs a;
     int L;               // lanes per head: 1 to 8, 16 or 32
-    int chunks, turned;  // chunks of a head, those that are turned
+    int chunks;          // of a head
     int table4;          // four entries of a table's row lie on a 16-byte boundary
-    int per[2], units[2];   // heads' steps per unit and units per token, of queries and of keys
     float inv_d;
 };
 
@@ -224,20 +222,22 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
-__host__ __device__ constexpr int heads_at_once(bool grad) { return grad ? 1 : 2; }     // of a lane, in a step
-__host__ __device__ constexpr int ring_depth(int el, bool grad) { return grad && el == 2 ? 3 : 2; }
-__host__ __device__ constexpr int ring_bytes(int el, bool grad) {
-    return ring_depth(el, grad) * heads_at_once(grad) * (grad ? 4 : 2) * kPairs * el * kThreads;
+__host__ __device__ constexpr int ring_depth(int el, bool grad) { return grad ? (el == 2 ? 3 : 2) : el == 2 ? 4 : 3; }
+// Bytes of a thread's slot.  A single bf16 element comes with the aligned four bytes that hold it: cp.async moves no
+// less, and its neighbour is in the same allocation, whose size is a multiple of that.
+__host__ __device__ constexpr int slot_bytes(int V, int el) { return V * el < 4 ? 4 : V * el; }
+__host__ __device__ constexpr int chunks_per_lane(int V, bool wide) { return V > 1 ? kPairs / V : wide ? 8 : 2; }
+__host__ __device__ constexpr int ring_bytes(int V, int NC, int el, bool grad) {
+    return ring_depth(el, grad) * (grad ? 4 : 2) * NC * slot_bytes(V, el) * kThreads;
 }
 
-template <typename E, int V, bool GRAD, bool INTER>
+template <typename E, int V, int NC, bool GRAD, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constant__ Params p)
 {
-    constexpr int NC = kPairs / V;           // chunks per lane
-    constexpr int kTensors = GRAD ? 2 : 1, M = heads_at_once(GRAD);
-    constexpr int kPieces = M * NC * 2 * kTensors, kBytes = V * (int)sizeof(E);
+    constexpr int kTensors = GRAD ? 2 : 1, kPieces = NC * 2 * kTensors, kBytes = slot_bytes(V, sizeof(E));
     constexpr int kDepth = ring_depth(sizeof(E), GRAD);
-    constexpr bool kAsync = kBytes >= 4;     // what the copies can move; single bf16 elements go through registers
+    constexpr bool kHalves = V * sizeof(E) < 4;      // slots hold an element and a neighbour
+    static_assert(!INTER || V > 1, "neighbours in a piece");
     using Pc = Piece<E, V>;
     using Vs = Vals<V>;
     extern __shared__ __align__(16) uint8_t ring[];
@@ -245,98 +245,89 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = p.L, HP = 32 / L, hs = lane / L, sub = lane - hs * L;
-    const int D = a.D, R = a.R, half = R / 2, rest = (D - R + 1) / 2;
+    const int D = a.D, R = a.R, half = R / 2, rest = (D - R + 1) / 2, turned_chunks = half / V;
     // slots that no copy writes stay zero
-    auto slot = [&](int stage, int piece) { return ((stage * kPieces + piece) * kThreads + (int)threadIdx.x) * kBytes; };
-    for (int i = 0; i < kDepth * kPieces; ++i) {
-        Pc z;
-        z.zero();
-        *reinterpret_cast<typename Pc::Raw *>(ring + slot(0, i)) = *reinterpret_cast<const typename Pc::Raw *>(z.w);
-    }
+    const uint32_t slots = smem_u32(ring) + threadIdx.x * kBytes;
+    auto slot = [&](int stage, int piece) { return (stage * kPieces + piece) * kThreads * kBytes; };
+    for (int i = 0; i < kDepth * kPieces; ++i)
+#pragma unroll
+        for (int k = 0; k < kBytes; k += 4) asm volatile("st.shared.u32 [%0], %1;" :: "r"(slots + slot(0, i) + k), "r"(0) : "memory");
     griddep_wait();
 
-    int ea[NC], eb[NC];                      // elements of the lane's chunks; -1: none
-    uint32_t axes[NC];                       // the axis of each of a chunk's pairs, four bits each; 15: none
-    // pair i of chunk c: neighbours of one piece, then of the other, or element i of both
+    // The lane's chunks: their two pieces' first elements (-1: none) and their pairs, by which the table is read.
+    // Halves: elements i and R / 2 + i, then what is not turned in two halves.  INTER: neighbours, pieces c and
+    // ceil(pieces / 2) + c of the head.
+    const int second = (D / V + 1) / 2;
+    int ea[NC], eb[NC];
+    uint32_t axes[NC];                       // the axis of each of a chunk's pairs, four bits each; 15: not turned
     auto pair_of = [&](int c, int i) {
-        return INTER && V > 1 ? (i < V / 2 ? V * c / 2 + i : R / 4 + V * c / 2 + i - V / 2) : V * c + i;
+        if constexpr (INTER) return V * (i < V / 2 ? c : c + second) / 2 + i % (V / 2);
+        else return c < turned_chunks ? V * c + i : half;
     };
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        const int c = hs < HP ? sub + L * j : p.chunks;
+        const int c = sub + L * j;
         ea[j] = eb[j] = -1;
-        axes[j] = 0;
-        if (c < p.turned) {
-            ea[j] = INTER && V == 1 ? 2 * c : V * c;
-            eb[j] = INTER && V == 1 ? 2 * c + 1 : half + V * c;
-            if (a.pair_axis) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int ax = __ldg(a.pair_axis + pair_of(c, i));
-                    axes[j] |= (uint32_t)(ax >= 0 && ax < a.axes ? ax : 15) << (4 * i);
-                }
-            }
-        } else if (c < p.chunks) {
-            ea[j] = R + V * (c - p.turned);
+        axes[j] = 0xFFFFFFFFu;
+        if (hs >= HP || c >= p.chunks) continue;
+        if constexpr (INTER) {
+            ea[j] = V * c;
+            eb[j] = V * (c + second) < D ? V * (c + second) : -1;
+        } else if (c < turned_chunks) {
+            ea[j] = V == 1 && a.interleaved ? 2 * c : V * c;
+            eb[j] = V == 1 && a.interleaved ? 2 * c + 1 : half + V * c;
+        } else {
+            ea[j] = R + V * (c - turned_chunks);
             eb[j] = ea[j] + rest;
             if (eb[j] >= D) eb[j] = -1;      // V == 1: the odd last element
         }
+        axes[j] = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int pair = pair_of(c, i), ax = pair >= half ? -1 : a.pair_axis ? __ldg(a.pair_axis + pair) : 0;
+            axes[j] |= (uint32_t)(ax >= 0 && ax < a.axes ? ax : 15) << (4 * i);
+        }
     }
-    // the sums over a head's lanes, the same in each of them
+    // the sum over a head's lanes, the same in each of them
     const bool pow2 = (L & (L - 1)) == 0;
-    auto over_head = [&](float (&v)[M]) {
+    auto over_head = [&](float v) {
         if (pow2) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                if (o >= L) continue;
-#pragma unroll
-                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xFFFFFFFFu, v[m], o);
-            }
-            return;
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < L) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            return v;
         }
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            float t = 0.f;
-            for (int i = 0; i < L; ++i) t += __shfl_sync(0xFFFFFFFFu, v[m], hs * L + i);
-            v[m] = t;
-        }
+        float t = 0.f;
+        for (int i = 0; i < L; ++i) t += __shfl_sync(0xFFFFFFFFu, v, hs * L + i);
+        return t;
     };
 
     // The angles of token t: cosines and sines of the lane's pairs, and a bit for each pair that is not turned.
-    constexpr int kRun = INTER && V > 1 ? V / 2 : V;         // pairs that follow each other in the table
+    constexpr int kRun = INTER ? V / 2 : V;                  // pairs that follow each other in the table
     auto angles = [&](int t, Vs (&cs)[NC], Vs (&sn)[NC]) {
         uint32_t still = 0;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            cs[j] = vall<V>(1.f);
-            sn[j] = vall<V>(0.f);
             float cv[V], sv[V];
-            const int c = hs < HP ? sub + L * j : p.chunks;
-            if (c >= p.turned) {
-                still |= ((1u << V) - 1) << (j * V);
-                continue;
-            }
-            int at[V];                       // a pair's position
-            uint32_t last = 16;
+            int at[V];                       // a pair's position; -1: not turned
+            const int c = sub + L * j;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t ax = axes[j] >> (4 * i) & 15;
-                if (i > 0 && ax == last) {
+                if (i > 0 && ax == (axes[j] >> (4 * i - 4) & 15)) {
                     at[i] = at[i - 1];
                 } else {
                     at[i] = ax < 15 ? __ldg(a.positions + (int64_t)ax * a.T + t) : -1;
-                    if (at[i] >= a.P) at[i] = -1;
+                    if (at[i] < 0 || at[i] >= a.P) at[i] = -1;
                 }
-                last = ax;
+                if (at[i] < 0) still |= 1u << (j * V + i);
             }
 #pragma unroll
             for (int i = 0; i < V; i += kRun) {
-                bool one = p.table4 && kRun >= 4;
-                if constexpr (kRun >= 4) {
+                bool one = kRun >= 4 && p.table4 && at[i] >= 0;
 #pragma unroll
-                    for (int k = 1; k < kRun; ++k) one = one && at[i + k] == at[i];
-                }
-                if (one && at[i] >= 0) {
+                for (int k = 1; k < kRun; ++k) one = one && at[i + k] == at[i];
+                if (one) {
                     const float *row = a.table + (int64_t)at[i] * R + pair_of(c, i);
 #pragma unroll
                     for (int k = 0; k + 4 <= kRun; k += 4) {
@@ -348,12 +339,13 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                 } else {
 #pragma unroll
                     for (int k = 0; k < kRun; ++k) {
-                        const int pos = at[i + k];
-                        const float *row = a.table + (int64_t)(pos < 0 ? 0 : pos) * R + pair_of(c, i + k);
-                        const float c1 = __ldg(row), s1 = __ldg(row + half);
-                        cv[i + k] = pos >= 0 ? c1 : 1.f;
-                        sv[i + k] = pos >= 0 ? s1 : 0.f;
-                        if (pos < 0) still |= 1u << (j * V + i + k);
+                        cv[i + k] = 1.f;
+                        sv[i + k] = 0.f;
+                        if (at[i + k] >= 0) {
+                            const float *row = a.table + (int64_t)at[i + k] * R + pair_of(c, i + k);
+                            cv[i + k] = __ldg(row);
+                            sv[i + k] = __ldg(row + half);
+                        }
                     }
                 }
             }
@@ -364,18 +356,21 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     };
 
     [[maybe_unused]] Vs dw[NC][2];
-    int64_t u = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t stride = (int64_t)gridDim.x * kWarps, first = (int64_t)a.T * p.units[0];
+    // Every warp has an even share of the queries' steps (a step is HP heads of a token) and of the keys', as they
+    // follow each other in memory; the shares of the keys from the other end, for the calls with few.
+    const int64_t warps = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + warp;
 
-    auto side_units = [&](auto SIDE) {
+    auto walk = [&](auto SIDE) {
         constexpr int side = decltype(SIDE)::value;
         const HeadsSide &s = a.side[side];
-        const int per = p.per[side], units = p.units[side], steps = (s.H + M * HP - 1) / (M * HP);
-        const int64_t begin = side ? first : 0, end = begin + (int64_t)a.T * units;
+        const int steps = (s.H + HP - 1) / HP;
+        const int64_t all = (int64_t)a.T * steps, mine = side ? warps - 1 - me : me;
+        const int64_t begin = all * mine / warps, end = all * (mine + 1) / warps;
         if constexpr (GRAD) {
 #pragma unroll
             for (int j = 0; j < NC; ++j) dw[j][0] = dw[j][1] = vall<V>(0.f);
         }
+        if (begin == end) return;
         Pc wa[NC], wb[NC];                   // the norm's weight
         const bool weighted = a.norm && s.w;
 #pragma unroll
@@ -385,62 +380,43 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             if (weighted && ea[j] >= 0) wa[j].load_shared(static_cast<const E *>(s.w) + ea[j]);
             if (weighted && eb[j] >= 0) wb[j].load_shared(static_cast<const E *>(s.w) + eb[j]);
         }
+        int t = (int)(begin / steps), b = (int)(begin - (int64_t)t * steps), stage = 0;
         // the place of the step whose loads go out next, kDepth steps ahead of the one computed
-        int64_t lu = u;
-        int lh = 0, lleft = 0, stage = 0;    // its head and the steps left in its unit
-        const E *lx = nullptr;
-        [[maybe_unused]] const E *ld = nullptr;
-        const int64_t xstep = HP * s.sh, ystep = HP * s.ysh;        // from head to head of a lane
+        int64_t left = end - begin;
+        int lt = t, lb = b;
+        const E *lx, *ld = nullptr;
+        const int64_t xstep = HP * s.sh, ystep = HP * s.ysh;
         [[maybe_unused]] const int64_t dstep = HP * s.dsh;
-        auto unit_at = [&](int64_t v, int &t, int &b0, int &b1) {
-            const int64_t in = v - begin;
-            t = (int)(in / units);
-            b0 = (int)(in - (int64_t)t * units) * per;
-            b1 = min(steps, b0 + per);
+        auto load_token = [&] {
+            lx = static_cast<const E *>(s.x) + (int64_t)lt * s.st + (int64_t)(lb * HP + hs) * s.sh;
+            if constexpr (GRAD) ld = static_cast<const E *>(s.d) + (int64_t)lt * s.dst + (int64_t)(lb * HP + hs) * s.dsh;
         };
-        auto load_unit = [&] {
-            int t, b0, b1;
-            unit_at(lu, t, b0, b1);
-            lh = b0 * M * HP + hs;
-            lleft = b1 - b0;
-            lx = static_cast<const E *>(s.x) + (int64_t)t * s.st + (int64_t)lh * s.sh;
-            if constexpr (GRAD) ld = static_cast<const E *>(s.d) + (int64_t)t * s.dst + (int64_t)lh * s.dsh;
-        };
-        if (lu < end) load_unit();
+        load_token();
         auto issue = [&](int st) {
-            if (lu < end) {
-                E held[kAsync ? 1 : kPieces];                // all loads out before the first is stored
+            if (left > 0) {
+                --left;
+                const bool live = lb * HP + hs < s.H;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    const int m = i / (NC * 2 * kTensors), q = i / (2 * NC) % kTensors, j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
-                    if (at < 0 || hs >= HP || lh + m * HP >= s.H || (GRAD && q == 0 && !a.norm)) continue;
-                    const E *from = (q ? ld + m * dstep : lx + m * xstep) + at;
-                    if constexpr (kAsync) copy_async<kBytes>(smem_u32(ring + slot(st, i)), from);
-                    else held[i] = __ldcg(from);
+                    const int q = i / (2 * NC), j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
+                    if (at < 0 || !live || (GRAD && q == 0 && !a.norm)) continue;
+                    const E *from = (q ? ld : lx) + at;
+                    if constexpr (kHalves) from = reinterpret_cast<const E *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3);
+                    copy_async<kBytes>(slots + slot(st, i), from);
                 }
-                if constexpr (!kAsync) {
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int m = i / (NC * 2 * kTensors), q = i / (2 * NC) % kTensors, j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
-                        if (at < 0 || hs >= HP || lh + m * HP >= s.H || (GRAD && q == 0 && !a.norm)) continue;
-                        *reinterpret_cast<E *>(ring + slot(st, i)) = held[i];
-                    }
-                }
-                lh += M * HP;
-                lx += M * xstep;
-                if constexpr (GRAD) ld += M * dstep;
-                if (--lleft == 0) {
-                    lu += stride;
-                    if (lu < end) load_unit();
+                lx += xstep;
+                if constexpr (GRAD) ld += dstep;
+                if (++lb == steps) {
+                    lb = 0;
+                    ++lt;
+                    load_token();
                 }
             }
-            if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue(i);
-        for (; u < end; u += stride) {
-            int t, b0, b1;
-            unit_at(u, t, b0, b1);
+        for (int64_t todo = end - begin; todo > 0; b = 0, ++t) {
             Vs cs[NC], sn[NC];
             const uint32_t still = angles(t, cs, sn);
             const bool some_still = __any_sync(0xFFFFFFFFu, still != 0);
@@ -479,110 +455,99 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                     ob = vfma(vmul(tb, sn[j]), minus, vmul(vb, cs[j]));
                 }
             };
-            int h = b0 * M * HP + hs;
+            int h = b * HP + hs;
             E *y = static_cast<E *>(s.y) + (int64_t)t * s.yst + (int64_t)h * s.ysh;
-            for (int b = b0; b < b1; ++b, h += M * HP, y += M * ystep) {
-                if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory");
-                Pc in[M][kTensors][NC][2];
+            for (; b < steps && todo > 0; ++b, --todo, h += HP, y += ystep) {
+                asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory");
+                Pc in[kTensors][NC][2];
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    in[i / (NC * 2 * kTensors)][i / (2 * NC) % kTensors][i / 2 % NC][i % 2].put(
-                        *reinterpret_cast<const typename Pc::Raw *>(ring + slot(stage, i)));
+                for (int i = 0; i < kPieces; ++i) {
+                    Pc &to = in[i / (2 * NC)][i / 2 % NC][i % 2];
+                    const uint32_t from = slots + slot(stage, i);
+                    if constexpr (kBytes == 16)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(to.w[0]), "=r"(to.w[1]), "=r"(to.w[2]), "=r"(to.w[3]) : "r"(from) : "memory");
+                    else if constexpr (kBytes == 8)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(to.w[0]), "=r"(to.w[1]) : "r"(from) : "memory");
+                    else
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(to.w[0]) : "r"(from) : "memory");
+                    if constexpr (kHalves) {
+                        // which half: the parity of the element's place
+                        const bool d = i >= 2 * NC;
+                        const uint32_t place = (uint32_t)(reinterpret_cast<uintptr_t>(d ? s.d : s.x) >> 1) +
+                                               (uint32_t)t * (uint32_t)(d ? s.dst : s.st) + (uint32_t)h * (uint32_t)(d ? s.dsh : s.sh) +
+                                               (uint32_t)(i % 2 ? eb[i / 2 % NC] : ea[i / 2 % NC]);
+                        to.w[0] = to.w[0] >> (16 * (place & 1)) & 0xFFFFu;
+                    }
+                }
                 issue(stage);
                 if (++stage == kDepth) stage = 0;
-                float r[M];
+                const bool live = hs < HP && h < s.H;
+                Vs ss = vall<V>(0.f);
 #pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    r[m] = 1.f;
-                    if (!a.norm) continue;
-                    Vs ss = vall<V>(0.f);
+                for (int j = 0; j < NC; ++j) {
+                    if (L * j >= p.chunks) break;
+                    Vs xa, xb;
+                    unpack<E, V, INTER>(in[0][j][0], in[0][j][1], xa, xb);
+                    ss = vfma(xb, xb, vfma(xa, xa, ss));
+                }
+                const float r = a.norm ? inv_sqrt(fmaf(over_head(vsum(ss)), p.inv_d, a.eps)) : 1.f;
+                const Vs rr = vall<V>(r);
+                if constexpr (!GRAD) {
 #pragma unroll
                     for (int j = 0; j < NC; ++j) {
                         if (L * j >= p.chunks) break;
-                        Vs xa, xb;
-                        unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
-                        ss = vfma(xb, xb, vfma(xa, xa, ss));
-                    }
-                    r[m] = vsum(ss);
-                }
-                if (a.norm) {
-                    over_head(r);
-#pragma unroll
-                    for (int m = 0; m < M; ++m) r[m] = inv_sqrt(fmaf(r[m], p.inv_d, a.eps));
-                }
-                if constexpr (!GRAD) {
-#pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        const bool live = hs < HP && h + m * HP < s.H;
-                        const Vs rr = vall<V>(r[m]);
-#pragma unroll
-                        for (int j = 0; j < NC; ++j) {
-                            if (L * j >= p.chunks) break;
-                            Vs xa, xb, oa, ob;
-                            unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
-                            turned(j, xa, xb, oa, ob);
-                            if (live) store_pair<E, V, INTER>(y + m * ystep, ea[j], eb[j], vmul(oa, rr), vmul(ob, rr));
-                        }
+                        Vs xa, xb, oa, ob;
+                        unpack<E, V, INTER>(in[0][j][0], in[0][j][1], xa, xb);
+                        turned(j, xa, xb, oa, ob);
+                        if (live) store_pair<E, V, INTER>(y, ea[j], eb[j], vmul(oa, rr), vmul(ob, rr));
                     }
                 } else {
-                    Vs ga[M][NC], gb[M][NC];
-                    float hx[M];
+                    Vs ga[NC], gb[NC], hx = vall<V>(0.f);
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        const bool live = hs < HP && h + m * HP < s.H;
-                        const Vs rr = vall<V>(r[m]);
-                        Vs sum = vall<V>(0.f);
-#pragma unroll
-                        for (int j = 0; j < NC; ++j) {
-                            if (L * j >= p.chunks) break;
-                            Vs da, db, xa, xb;
-                            unpack<E, V, INTER>(in[m][kTensors - 1][j][0], in[m][kTensors - 1][j][1], da, db);
-                            turned(j, da, db, ga[m][j], gb[m][j]);
-                            if (!a.norm) continue;
-                            unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
-                            xa = vmul(xa, rr);                   // x r: its part of dw, and of the sum
-                            xb = vmul(xb, rr);
-                            if (live) {
-                                dw[j][0] = vfma(ga[m][j], xa, dw[j][0]);
-                                dw[j][1] = vfma(gb[m][j], xb, dw[j][1]);
-                            }
-                            if (weighted) {
-                                Vs va, vb;
-                                unpack<E, V, INTER>(wa[j], wb[j], va, vb);
-                                ga[m][j] = vmul(ga[m][j], va);
-                                gb[m][j] = vmul(gb[m][j], vb);
-                            }
-                            sum = vfma(ga[m][j], xa, vfma(gb[m][j], xb, sum));
+                    for (int j = 0; j < NC; ++j) {
+                        if (L * j >= p.chunks) break;
+                        Vs da, db, xa, xb;
+                        unpack<E, V, INTER>(in[kTensors - 1][j][0], in[kTensors - 1][j][1], da, db);
+                        turned(j, da, db, ga[j], gb[j]);
+                        if (!a.norm) continue;
+                        unpack<E, V, INTER>(in[0][j][0], in[0][j][1], xa, xb);
+                        xa = vmul(xa, rr);                   // x r: its part of dw, and of the sum
+                        xb = vmul(xb, rr);
+                        if (live) {
+                            dw[j][0] = vfma(ga[j], xa, dw[j][0]);
+                            dw[j][1] = vfma(gb[j], xb, dw[j][1]);
                         }
-                        hx[m] = vsum(sum);
+                        if (weighted) {
+                            Vs va, vb;
+                            unpack<E, V, INTER>(wa[j], wb[j], va, vb);
+                            ga[j] = vmul(ga[j], va);
+                            gb[j] = vmul(gb[j], vb);
+                        }
+                        hx = vfma(ga[j], xa, vfma(gb[j], xb, hx));
                     }
-                    if (a.norm) over_head(hx);
+                    // dx = r (h - x r mean(h x r))
+                    const Vs c = vall<V>(a.norm ? -(r * (over_head(vsum(hx)) * p.inv_d)) : 0.f);
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        const bool live = hs < HP && h + m * HP < s.H;
-                        // dx = r (h - x r mean(h x r))
-                        const Vs rr = vall<V>(r[m]), c = vall<V>(-(r[m] * (hx[m] * p.inv_d)));
-#pragma unroll
-                        for (int j = 0; j < NC; ++j) {
-                            if (L * j >= p.chunks) break;
-                            if (a.norm) {
-                                Vs xa, xb;
-                                unpack<E, V, INTER>(in[m][0][j][0], in[m][0][j][1], xa, xb);
-                                ga[m][j] = vmul(vfma(xa, c, ga[m][j]), rr);
-                                gb[m][j] = vmul(vfma(xb, c, gb[m][j]), rr);
-                            }
-                            if (live) store_pair<E, V, INTER>(y + m * ystep, ea[j], eb[j], ga[m][j], gb[m][j]);
+                    for (int j = 0; j < NC; ++j) {
+                        if (L * j >= p.chunks) break;
+                        if (a.norm) {
+                            Vs xa, xb;
+                            unpack<E, V, INTER>(in[0][j][0], in[0][j][1], xa, xb);
+                            ga[j] = vmul(vfma(xa, c, ga[j]), rr);
+                            gb[j] = vmul(vfma(xb, c, gb[j]), rr);
                         }
+                        if (live) store_pair<E, V, INTER>(y, ea[j], eb[j], ga[j], gb[j]);
                     }
                 }
             }
         }
-        if constexpr (kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     };
 
     if constexpr (!GRAD) {
-        side_units(std::integral_constant<int, 0>{});
-        side_units(std::integral_constant<int, 1>{});
+        walk(std::integral_constant<int, 0>{});
+        walk(std::integral_constant<int, 1>{});
     } else {
         __shared__ float part[kWarps][2][SKINNY_MAX_HEAD];
         auto keep = [&](int side) {
@@ -600,15 +565,15 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                         for (int i2 = 0; i2 < HP; ++i2) t += __shfl_sync(0xFFFFFFFFu, v, sub + i2 * L);
                         v = t;
                         // INTER: pair i's first or second, in the piece that holds it
-                        const int e = INTER && V > 1 ? (2 * i < V ? ea[j] : eb[j]) : ab ? eb[j] : ea[j];
-                        const int k = INTER && V > 1 ? 2 * i % V + ab : i;
+                        const int e = INTER ? (2 * i < V ? ea[j] : eb[j]) : ab ? eb[j] : ea[j];
+                        const int k = INTER ? 2 * i % V + ab : i;
                         if (hs == 0 && e >= 0) part[warp][side][e + k] = v;
                     }
                 }
         };
-        side_units(std::integral_constant<int, 0>{});
+        walk(std::integral_constant<int, 0>{});
         keep(0);
-        side_units(std::integral_constant<int, 1>{});
+        walk(std::integral_constant<int, 1>{});
         keep(1);
         if (!a.partial) return;
         __syncthreads();
@@ -651,29 +616,29 @@ bool rows_lie(const void *p, int64_t st, int64_t sh, int el, int T, int H, int b
     return bits % (uintptr_t)bytes == 0;
 }
 
-template <typename E, bool GRAD, bool INTER>
-const void *kernel_for(int V) {
+// wide: heads of more than 128 elements, where V == 1
+template <typename E, bool GRAD>
+const void *kernel_as(int V, bool wide, bool inter) {
     if constexpr (sizeof(E) == 2)
-        if (V == 8) return (const void *)heads_kernel<E, 8, GRAD, INTER>;
-    return V == 4   ? (const void *)heads_kernel<E, 4, GRAD, INTER>
-           : V == 2 ? (const void *)heads_kernel<E, 2, GRAD, INTER>
-                    : (const void *)heads_kernel<E, 1, GRAD, INTER>;
+        if (V == 8) return inter ? (const void *)heads_kernel<E, 8, 1, GRAD, true> : (const void *)heads_kernel<E, 8, 1, GRAD, false>;
+    if (V == 4) return inter ? (const void *)heads_kernel<E, 4, 2, GRAD, true> : (const void *)heads_kernel<E, 4, 2, GRAD, false>;
+    if (V == 2) return inter ? (const void *)heads_kernel<E, 2, 4, GRAD, true> : (const void *)heads_kernel<E, 2, 4, GRAD, false>;
+    return wide ? (const void *)heads_kernel<E, 1, 8, GRAD, false> : (const void *)heads_kernel<E, 1, 2, GRAD, false>;
 }
-template <typename E>
-const void *kernel_for(int V, bool grad, bool inter) {
-    return grad ? (inter ? kernel_for<E, true, true>(V) : kernel_for<E, true, false>(V))
-                : (inter ? kernel_for<E, false, true>(V) : kernel_for<E, false, false>(V));
+const void *kernel_for(bool b16, int V, bool wide, bool grad, bool inter) {
+    return b16 ? (grad ? kernel_as<uint16_t, true>(V, wide, inter) : kernel_as<uint16_t, false>(V, wide, inter))
+               : (grad ? kernel_as<float, true>(V, wide, inter) : kernel_as<float, false>(V, wide, inter));
 }
 
 }  // namespace
 
 cudaError_t heads_prepare() {
-    for (int i = 0; i < 32; ++i) {
-        const bool b16 = i & 1, grad = i & 2, inter = i & 4;
-        const int V = 1 << (i >> 3);
+    for (int i = 0; i < 64; ++i) {
+        const bool b16 = i & 1, grad = i & 2, inter = i & 4, wide = i & 8;
+        const int V = 1 << (i >> 4);
         if (V == 8 && !b16) continue;
-        const cudaError_t e = cudaFuncSetAttribute(b16 ? kernel_for<uint16_t>(V, grad, inter) : kernel_for<float>(V, grad, inter),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(b16 ? 2 : 4, grad));
+        const cudaError_t e = cudaFuncSetAttribute(kernel_for(b16, V, wide, grad, inter), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   ring_bytes(V, chunks_per_lane(V, wide), b16 ? 2 : 4, grad));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -683,7 +648,7 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
     const int el = a.b16 ? 2 : 4;
     int V = 16 / el;
     for (; V > 1; V /= 2) {
-        if (a.R / 2 % V || (a.D - a.R) % (2 * V)) continue;
+        if (a.interleaved ? a.D % V != 0 : a.R / 2 % V || (a.D - a.R) % (2 * V)) continue;
         bool lie = true;
         for (const HeadsSide &s : a.side) {
             if (s.H == 0) continue;
@@ -696,43 +661,29 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
     }
     Params p{};
     p.a = a;
-    p.turned = a.R / 2 / V;
-    p.chunks = p.turned + ((a.D - a.R + 1) / 2 + V - 1) / V;
+    const bool inter = a.interleaved && V > 1, wide = a.D > 128;
+    p.chunks = inter ? (a.D / V + 1) / 2 : a.R / 2 / V + ((a.D - a.R + 1) / 2 + V - 1) / V;
     // the lanes per head that keep a warp's busiest: the fewest rounds of chunks for its heads, pieces of a head
     // that are 32 bytes together at least
-    const int NC = kPairs / V;
+    const int NC = chunks_per_lane(V, wide);
     p.L = 32;
     for (int L : {16, 8, 7, 6, 5, 4, 3, 2, 1}) {
         if (L * NC < p.chunks || (L * V * el < 32 && L < p.chunks)) continue;
         const int rounds = (p.chunks + L - 1) / L, best = (p.chunks + p.L - 1) / p.L;
         if (rounds * (32 / p.L) <= best * (32 / L)) p.L = L;
     }
-    p.table4 = a.R % (a.interleaved ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
+    p.table4 = a.R % 8 == 0 && reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
     p.inv_d = 1.f / (float)a.D;
-    // CTAs that an SM holds; a token's heads are dealt to more warps while there are fewer tokens than warps
-    const int64_t ctas = 2ll * c.num_sms < kHeadsParts ? 2ll * c.num_sms : kHeadsParts, warps = ctas * kWarps;
-    const int HP = 32 / p.L;
-    int64_t steps[2], all = 0, units = 0;
-    for (int i = 0; i < 2; ++i) {
-        steps[i] = (a.side[i].H + HP * heads_at_once(a.grad) - 1) / (HP * heads_at_once(a.grad));
-        all += a.T * steps[i];
-    }
-    for (int i = 0; i < 2; ++i) {
-        int64_t per = (all + warps - 1) / warps;
-        if (per > steps[i]) per = steps[i];
-        if (per < 1) per = 1;
-        p.per[i] = (int)per;
-        p.units[i] = (int)((steps[i] + per - 1) / per);
-        units += a.T * (int64_t)p.units[i];
-    }
-    const int64_t need = (units + kWarps - 1) / kWarps;
+    const int64_t ctas = 2ll * c.num_sms < kHeadsParts ? 2ll * c.num_sms : kHeadsParts;      // what an SM holds
+    int64_t steps = 0;
+    for (const HeadsSide &s : a.side) steps += (int64_t)a.T * ((s.H + 32 / p.L - 1) / (32 / p.L));
+    const int64_t need = (steps + kWarps - 1) / kWarps;
     const int grid = (int)(need < ctas ? need : ctas);
     const bool sums = a.grad && (a.side[0].dw || a.side[1].dw);
     if (!sums) p.a.partial = nullptr;
-    const bool inter = a.interleaved != 0;
     void *kargs[] = {&p};
-    const cudaError_t e = launch_plain(a.b16 ? kernel_for<uint16_t>(V, a.grad, inter) : kernel_for<float>(V, a.grad, inter),
-                                       dim3((unsigned)grid), kThreads, ring_bytes(el, a.grad), stream, c.pdl, kargs);
+    const cudaError_t e = launch_plain(kernel_for(a.b16, V, wide, a.grad, inter), dim3((unsigned)grid), kThreads,
+                                       ring_bytes(V, NC, el, a.grad), stream, c.pdl, kargs);
     if (e != cudaSuccess || !sums) return e;
     const float *partial = a.partial;
     int parts = grid, D = a.D;
