@@ -268,6 +268,12 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
         for (int64_t t = first; t < tiles; t += pairs) {
             int tn, tr;
             tile_at(p, t, tn, tr);
+            if (p.e.R) {                                         // the residual's rows on their way to L2
+                const int el = p.e.out_bf16 ? 2 : 4, n = GATED ? tn * 128 + rank * 64 + (32 * q & 63) : tn * 256 + rank * 128 + 32 * q;
+                for (int j = lane; j < 128; j += 32)
+                    if ((int64_t)tr * 256 + 128 * h + j < p.e.rows && n < p.e.cols)
+                        prefetch_l2(static_cast<const char *>(p.e.R) + (((int64_t)tr * 256 + 128 * h + j) * p.e.ldr + n) * el);
+            }
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
