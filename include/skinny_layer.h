@@ -39,8 +39,9 @@ typedef enum {
  *     SKINNY_ACT_SWIGLU, GEGLU:      Y[m,n] = act(Z[m,n]) * Z[m,N+n] + R[m,n]         W [2N, K], bias [2N]
  *                                    (act is silu or gelu: gates, then ups)
  *
- * Sums in fp32 (tensor-core chains of at most 16 MMAs, then rounded adds), the
- * epilogue in fp32, one rounding to out_dtype.  Z, for the backward pass, is
+ * Sums in fp32, within 1e-5 of sum_k |x w| as in skinny_gemm_bf16 (tensor-core
+ * chains of at most 16 MMAs, or 64 where there are many rows, then rounded
+ * adds), the epilogue in fp32, one rounding to out_dtype.  Z, for the backward pass, is
  * rounded to bf16 beside it; Y is computed from what was not rounded.
  *
  *   X     device, bf16 [M, K], row stride ldx >= K;  W  device, bf16, row stride ldw >= K

@@ -64,7 +64,7 @@ struct View {
         const int64_t s = T > 1 ? st : INT64_MAX, h = H > 1 ? sh : INT64_MAX;
         if (s < D || h < D) return false;
         if (T <= 1 || H <= 1) return true;
-        return st >= (int64_t)(H - 1) * sh + D || sh >= (int64_t)(T - 1) * st + D;
+        return st - D >= (H - 1) * sh || (sh - D) / (T - 1) >= st;
     }
     int64_t extent() const { return ((T - 1) * (T > 1 ? st : 0) + (H - 1) * (H > 1 ? sh : 0) + D) * el; }
     bool same(const View &o) const {
@@ -90,7 +90,7 @@ bool view_meets_range(const View &a, const Range &r) {
     return ranges_overlap(addr(a.p), addr(a.p) + (uintptr_t)a.extent(), r.lo, r.hi);
 }
 
-constexpr int64_t kMaxStride = 1ll << 40;
+constexpr int64_t kMaxStride = 1ll << 40, kMaxExtent = 1ll << 48;      // elements
 
 // What both directions ask of their arguments.
 skinny_status_t check_heads(const skinny_heads_t *q, const skinny_heads_t *k, const skinny_rotation_t *rot, int T, int D,
@@ -110,6 +110,7 @@ skinny_status_t check_heads(const skinny_heads_t *q, const skinny_heads_t *k, co
 skinny_status_t check_view(const View &v) {
     if (v.T == 0 || v.H == 0) return SKINNY_OK;
     if (!v.p || v.st < 0 || v.sh < 0 || v.st > kMaxStride || v.sh > kMaxStride || !v.ok()) return SKINNY_ERR_INVALID_VALUE;
+    if ((v.T > 1 && v.st > kMaxExtent / v.T) || (v.H > 1 && v.sh > kMaxExtent / v.H)) return SKINNY_ERR_INVALID_VALUE;
     return aligned(v.p, v.el) ? SKINNY_OK : SKINNY_ERR_MISALIGNED;
 }
 // Whether what is written meets the small inputs.
