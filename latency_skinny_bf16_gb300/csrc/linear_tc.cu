@@ -34,14 +34,20 @@ constexpr int kTmemCols = 256;
 constexpr int kABytes = 128 * 128;     // 128 indexes of A, 64 steps of the depth
 
 __host__ __device__ constexpr int stage_bytes(int BN) { return kABytes + BN * 128; }
-__host__ __device__ constexpr int ring_stages(int BN) { return BN <= 32 ? 5 : BN <= 64 ? 4 : 3; }
+__host__ __device__ constexpr int ring_stages(int BN) { return BN <= 16 ? 5 : BN <= 32 ? 4 : 3; }
 __host__ __device__ constexpr int acc_sets(int BN) { return BN <= 64 ? 4 : 2; }
 __host__ __device__ constexpr int set_cols(int BN) { return BN <= 64 ? 64 : BN; }
 constexpr int kTail = 256;             // barriers, tensor-memory address, flags
-__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + ring_stages(BN) * stage_bytes(BN) + kTail; }
+// The partial sums that a CTA receives: 128 outputs by BN rows.  Up to 64 rows they have a place of their own, so that
+// a CTA may send while others still sum; with 128 they take the ring's, once all of the cluster are done with theirs.
+__host__ __device__ constexpr bool own_slots(int BN) { return BN <= 64; }
+__host__ __device__ constexpr int slot_bytes(int BN) { return own_slots(BN) ? BN * 128 * 4 : 0; }
+__host__ __device__ constexpr int smem_bytes(int BN) {
+    return 1024 + ring_stages(BN) * stage_bytes(BN) + slot_bytes(BN) + kTail;
+}
 // tensor memory for two CTAs on an SM, as for every kernel that takes 256 columns of it
 static_assert(smem_bytes(16) >= kTcMinSmem && smem_bytes(32) >= kTcMinSmem && smem_bytes(64) >= kTcMinSmem &&
-              smem_bytes(128) >= kTcMinSmem && 2 * (smem_bytes(32) + 1024) <= 228 * 1024, "two CTAs on an SM");
+              smem_bytes(128) >= kTcMinSmem && 2 * (smem_bytes(64) + 1024) <= 228 * 1024, "two CTAs on an SM");
 
 struct Maps {
     CUtensorMap a, b;
@@ -69,14 +75,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
-    const uint32_t bars = base + kStages * kStage;
+    constexpr int kSlots = own_slots(BN) ? kStages * kStage : 0;       // where the partial sums arrive
+    constexpr int kBars = kStages * kStage + slot_bytes(BN);
+    const uint32_t bars = base + kBars;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (kStages + s); };
     auto accf = [&](int b) { return bars + 8u * (2 * kStages + b); };
     auto acce = [&](int b) { return bars + 8u * (2 * kStages + kSets + b); };
     const uint32_t done = bars + 8u * (2 * kStages + 2 * kSets);
     static_assert(8 * (2 * kStages + 2 * kSets + 1) + 16 <= kTail, "tail");
-    uint8_t *tail = smem + kStages * kStage + 8 * (2 * kStages + 2 * kSets + 1);
+    uint8_t *tail = smem + kBars + 8 * (2 * kStages + 2 * kSets + 1);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
     volatile int *mma_ok = reinterpret_cast<volatile int *>(tail + 4);
     volatile int *failed = reinterpret_cast<volatile int *>(tail + 8);
@@ -88,9 +96,19 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     const int64_t r0 = tile % p.mt * BN;
     const int live = (int)min((int64_t)BN, p.e.rows - r0);
     const int b0 = (int)((int64_t)p.boxes * rank / S), nb = (int)((int64_t)p.boxes * (rank + 1) / S) - b0;
+    auto load_a = [&](int i, int s) {
+        const uint32_t st = base + s * kStage;
+        const int c = (b0 + i) * 64;
+        if constexpr (AX) {
+            tma_load_2d(st, &maps.a, n0, c, full(s));
+            tma_load_2d(st + kBox, &maps.a, n0 + 64, c, full(s));
+        } else {
+            tma_load_2d(st, &maps.a, c, n0, full(s));
+            if (GATED) tma_load_2d(st + 64 * 128, &maps.a, c, p.e.cols + n0, full(s));
+        }
+    };
+    const int tx = (AX ? kABytes : (GATED ? 2 : 1) * TA * 128) + BN * 128, pre = min(nb, kStages);
     if (tid == 0) {
-        prefetch_tensormap(&maps.a);
-        prefetch_tensormap(&maps.b);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
@@ -103,8 +121,21 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         *mma_ok = 0;
         *failed = 0;
         fence_mbarrier_init_cluster();
+        if (p.early) {                               // the weight's first boxes, before anything is waited for
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(full(i), (uint32_t)tx);
+                load_a(i, i);
+            }
+        }
+        prefetch_tensormap(&maps.b);
     }
+    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    if (own_slots(BN) && S > 1) cluster_arrive_relaxed();              // this CTA is there to be sent to
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
 
     float acc[BN];
 #pragma unroll
@@ -112,17 +143,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     if (warp == 0) {
         if (lane == 0) {
             // ---- TMA producer
-            auto load_a = [&](int i, int s) {
-                const uint32_t st = base + s * kStage;
-                const int c = (b0 + i) * 64;
-                if constexpr (AX) {
-                    tma_load_2d(st, &maps.a, n0, c, full(s));
-                    tma_load_2d(st + kBox, &maps.a, n0 + 64, c, full(s));
-                } else {
-                    tma_load_2d(st, &maps.a, c, n0, full(s));
-                    if (GATED) tma_load_2d(st + 64 * 128, &maps.a, c, p.e.cols + n0, full(s));
-                }
-            };
             auto load_b = [&](int i, int s) {
                 const uint32_t st = base + s * kStage + kABytes;
                 const int c = (b0 + i) * 64;
@@ -133,14 +153,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                     tma_load_2d(st, &maps.b, c, (int)r0, full(s));
                 }
             };
-            const int tx = (AX ? kABytes : (GATED ? 2 : 1) * TA * 128) + BN * 128;
-            const int pre = min(nb, kStages);
-            if (!p.early) griddep_wait();
-            for (int i = 0; i < pre; ++i) {
+            for (int i = 0; !p.early && i < pre; ++i) {
                 mbar_arrive_expect_tx(full(i), (uint32_t)tx);
                 load_a(i, i);
             }
-            if (p.early) griddep_wait();
             for (int i = 0; i < pre; ++i) load_b(i, i);
             int issued = pre;
             for (int i = pre; i < nb; ++i) {
@@ -162,14 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                 }
         }
         __syncwarp();
-        griddep_wait();
     } else if (warp == 1) {
-        tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
-        tc_fence_before();
-        named_bar_sync(1, kThreads - 32);
-        tc_fence_after();
-        const uint32_t tmem = *tmem_slot;
-        griddep_wait();
         // ---- MMA issuer: the warp stays together, so that what the MMAs take is uniform
         constexpr uint32_t idesc = product_idesc<BN, 128, AX, BX>();
         constexpr uint64_t kStepA = AX ? 2048 >> 4 : 32 >> 4, kStepB = BX ? 2048 >> 4 : 32 >> 4;
@@ -216,10 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         __syncwarp();
     } else {
         // ---- draining warps: lane quarter warp % 4 of tensor memory
-        named_bar_sync(1, kThreads - 32);
-        tc_fence_after();
-        griddep_wait();
-        const uint32_t lanes = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int chunks = (nb + 3) / 4;
         for (int c = 0; c < chunks; ++c) {
             const int b = c % kSets;
@@ -252,14 +258,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        if (*mma_ok) tmem_dealloc(*tmem_slot, kTmemCols);
+        if (*mma_ok) tmem_dealloc(tmem, kTmemCols);
         // else an issued MMA may still write it: it stays allocated until the CTA exits
     }
 
-    // ---- partial sums to the rows' owners, through the ring
+    // ---- partial sums to the rows' owners
     if (S > 1) {
-        cluster_arrive_release();                    // every CTA's ring has been read
-        cluster_wait_acquire();
+        if (!own_slots(BN)) cluster_arrive_release();          // every CTA's ring has been read
+        cluster_wait_acquire();                                // or: every CTA has started
     }
     const bool ok = *failed == 0 && *mma_ok != 0;
     const Epilogue &e = p.e;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     }
     const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = BN >> shift;      // rows of an owner
     if (warp >= 2 && ok) {
-        const uint32_t at = base + 4u * (uint32_t)(rank * per * 128 + 32 * (warp & 3) + lane);
+        const uint32_t at = base + kSlots + 4u * (uint32_t)(rank * per * 128 + 32 * (warp & 3) + lane);
         uint32_t to = at;
 #pragma unroll
         for (int j = 0; j < BN; ++j) {
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     if (!ok) return;
     // kRows rows of an output a thread at a time, the output's threads taking turns
     constexpr int kRows = BN < 8 ? BN : 8, kOuts = GATED ? 64 : 128, kTurns = kThreads / kOuts;
-    const float *slots = reinterpret_cast<const float *>(smem);
+    const float *slots = reinterpret_cast<const float *>(smem + kSlots);
     const int nl = tid % kOuts, turn = tid / kOuts, n = n0 + nl, mine = min(per, live - rank * per);
     if (turn >= kTurns || nl >= TA || n >= e.cols) return;
     const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
