@@ -19,6 +19,7 @@
 //     the whole depth runs the epilogue from its registers.
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing.
 #include <cuda.h>
+#include <type_traits>
 
 #include "experts_gemm.h"
 #include "product.cuh"
@@ -282,14 +283,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         return;
     }
     const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = BN >> shift;      // rows of an owner
+    // kVec rows of an output side by side, the outputs behind one another
+    constexpr int kVec = BN < 32 ? 2 : 4;
     if (warp >= 2 && ok) {
-        const uint32_t at = base + kSlots + 4u * (uint32_t)(rank * per * 128 + 32 * (warp & 3) + lane);
+        const uint32_t at = base + kSlots + 4u * (uint32_t)(rank * per * 128 + (32 * (warp & 3) + lane) * kVec);
         uint32_t to = at;
 #pragma unroll
-        for (int j = 0; j < BN; ++j) {
+        for (int j = 0; j < BN; j += kVec) {
             if ((j & (per - 1)) == 0) to = mapa_shared(at, (uint32_t)(S == 1 ? rank : j / (BN / 8) >> (3 - shift)));
-            if (j < live) st_shared_cluster_f32(to, acc[j]);
-            to += 512u;
+            if (j < live) {
+                if constexpr (kVec == 2)
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]) : "memory");
+                else
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3]) : "memory");
+            }
+            to += 512u * kVec;
         }
     }
     if (S > 1) {
@@ -312,12 +321,18 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < kRows; ++i) z[i] = up[i] = 0.f;
         for (int s = 0; s < S; ++s) {
-            const float *slot = slots + (s * per + c) * 128 + nl;
+            const float *slot = slots + (s * per + c) * 128 + nl * kVec;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (i < rows) {
-                    z[i] += slot[i * 128];
-                    if (GATED) up[i] += slot[i * 128 + 64];
+            for (int i = 0; i < kRows; i += kVec) {
+                if (i >= rows) continue;
+                using Vec = typename std::conditional<kVec == 2, float2, float4>::type;
+                const Vec fz = *reinterpret_cast<const Vec *>(slot + i * 128);
+                const Vec fu = *reinterpret_cast<const Vec *>(slot + i * 128 + (GATED ? 64 * kVec : 0));
+                const float *v = reinterpret_cast<const float *>(&fz), *w = reinterpret_cast<const float *>(&fu);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    z[i + k] += v[k];
+                    if (GATED) up[i + k] += w[k];
                 }
             }
         }
