@@ -1,7 +1,9 @@
 // linear_dz.cu -- the elementwise part of a product's backward pass: dZ from dY
 // and the kept Z, and the bias gradient, sums of dZ over the tokens.
 //     dZ = dY act'(Z);  gated: dY U act'(G) for the gates, dY act(G) for the ups
-// A stream through device memory (dY, Z, dZ once each).  A CTA takes 32 lanes
+// A stream through device memory (dY, Z, dZ once each); the exponentials take three
+// fifths of the issue slots beside it (GB300: 8192 x 2 * 2048 SwiGLU 33 us, 5.0 TB/s;
+// odd widths go element by element, 1001 x 1437 10 us).  A CTA takes 32 lanes
 // of V columns and every eighth of its part of the tokens a row of threads; the
 // bias gradient is summed along a thread's tokens, over the CTA's eight rows and
 // then over the parts by a second kernel, in a fixed order.
