@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             float v = 0.f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) v += part[q][side][e];
-            a.partial[((int64_t)blockIdx.x * 2 + side) * D + e] = v;
+            if (gridDim.x > 1) a.partial[((int64_t)blockIdx.x * 2 + side) * D + e] = v;
+            else if (a.side[side].dw) a.side[side].dw[e] = v;
         }
     }
 }
@@ -685,14 +686,14 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
     const int64_t ctas = 2ll * c.num_sms < kHeadsParts ? 2ll * c.num_sms : kHeadsParts;      // what an SM holds
     int64_t steps = 0;
     for (const HeadsSide &s : a.side) steps += (int64_t)a.T * ((s.H + 32 / p.L - 1) / (32 / p.L));
-    const int64_t need = (steps + kWarps - 1) / kWarps;
-    const int grid = (int)(need < ctas ? need : ctas);
     const bool sums = a.grad && (a.side[0].dw || a.side[1].dw);
+    const int64_t need = (steps + kWarps - 1) / kWarps;      // one CTA's sums are the weights' gradients themselves
+    const int grid = (int)(need < ctas ? need : ctas);
     if (!sums) p.a.partial = nullptr;
     void *kargs[] = {&p};
     const cudaError_t e = launch_plain(kernel_for(a.b16, V, wide, a.grad, inter), dim3((unsigned)grid), kThreads,
                                        ring_bytes(V, NC, el, a.grad), stream, c.pdl, kargs);
-    if (e != cudaSuccess || !sums) return e;
+    if (e != cudaSuccess || !sums || grid == 1) return e;
     const float *partial = a.partial;
     int parts = grid, D = a.D;
     float *qw = a.side[0].dw, *kw = a.side[1].dw;

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        sum[g][i] += d[g];
+                        sum[g][i] = __fadd_rn(sum[g][i], d[g]);      // the same sum with and without dZ: never fused
                         o[g].e[i] = f32_to_bf16_rn(d[g]);
                     }
                 }
@@ -146,12 +146,14 @@ cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.dY) | reinterpret_cast<uintptr_t>(a.Z) | reinterpret_cast<uintptr_t>(a.dZ);
     const bool wide = bits % 16 == 0 && a.N % 8 == 0 && a.lddy % 8 == 0 && (!a.Z || a.ldz % 8 == 0) && (!a.dZ || a.lddz % 8 == 0);
     const int V = wide ? 8 : 1, rows = gated ? 2 * a.N : a.N;
-    const int64_t parts = (a.M + kRows - 1) / kRows < kDbiasParts ? (a.M + kRows - 1) / kRows : kDbiasParts;
+    // a part is four rows a thread at least, what it loads at once; one part's sums are the bias gradient itself
+    const int64_t least = 4 * kRows, want = (a.M + least - 1) / least, parts = want < kDbiasParts ? want : kDbiasParts;
     LinearDzArgs p = a;
+    if (parts == 1) p.partial = a.dbias;
     void *args[] = {&p};
     const void *fn = wide ? kernel_for<8>(a.act) : kernel_for<1>(a.act);
     cudaError_t e = launch_plain(fn, dim3((unsigned)((a.N + 32 * V - 1) / (32 * V)), (unsigned)parts), kThreads, 0, stream, c.pdl, args);
-    if (e != cudaSuccess || !a.dbias) return e;
+    if (e != cudaSuccess || !a.dbias || parts == 1) return e;
     const float *partial = a.partial;
     int np = (int)parts, n = rows;
     float *out = a.dbias;
