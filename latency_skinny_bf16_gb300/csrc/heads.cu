@@ -20,8 +20,8 @@
 // What bounds it: device memory nearly, for heads of whole 16-byte pieces, and the
 // instructions (two thirds of the issue slots at 16 warps an SM, which is what the
 // factors' registers leave).  GB300, bf16 heads of 128, 64 + 8 of them: 8192 tokens
-// 55 us (5.5 TB/s), 16384 with three axes 109, the gradient for 8192 97 (4.7 TB/s);
-// fp32 32 + 8 heads 63 and 100.  Unusual sizes pay in instructions: 32 + 8 heads of
+// 55 us (5.5 TB/s), 16384 with three axes 108, the gradient for 8192 91 (5.0 TB/s);
+// fp32 32 + 8 heads 63 and 91.  Unusual sizes pay in instructions: 32 + 8 heads of
 // 61 47 us (1.7 TB/s), of 72 36, 16 + 2 heads of 80 for 20000 tokens 50.  Tried and
 // slower: 24 warps of 80 registers (87 us where 16 take 59), two heads a lane at a
 // time (the same), loads held in registers (60 against 55).
@@ -214,7 +214,7 @@ struct Params {
     HeadsArgs a;
     int L;               // lanes per head: 1 to 8, 16 or 32
     int chunks;          // of a head
-    int table4;          // four entries of a table's row lie on a 16-byte boundary
+    int together;        // entries of a table's row that lie on a boundary of their size: 4, 2 or 1
     float inv_d;
 };
 
@@ -332,17 +332,25 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             }
 #pragma unroll
             for (int i = 0; i < V; i += kRun) {
-                bool one = kRun >= 4 && p.table4 && at[i] >= 0;
+                constexpr int kWide = kRun < 4 ? kRun : 4;
+                bool one = kWide > 1 && p.together >= kWide && at[i] >= 0;
 #pragma unroll
                 for (int k = 1; k < kRun; ++k) one = one && at[i + k] == at[i];
                 if (one) {
                     const float *row = a.table + (int64_t)at[i] * R + pair_of(c, i);
 #pragma unroll
-                    for (int k = 0; k + 4 <= kRun; k += 4) {
-                        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + k));
-                        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + k));
-                        cv[i + k] = c4.x; cv[i + k + 1] = c4.y; cv[i + k + 2] = c4.z; cv[i + k + 3] = c4.w;
-                        sv[i + k] = s4.x; sv[i + k + 1] = s4.y; sv[i + k + 2] = s4.z; sv[i + k + 3] = s4.w;
+                    for (int k = 0; k < kRun; k += kWide) {
+                        if constexpr (kWide == 4) {
+                            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + k));
+                            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + k));
+                            cv[i + k] = c4.x; cv[i + k + 1] = c4.y; cv[i + k + 2] = c4.z; cv[i + k + 3] = c4.w;
+                            sv[i + k] = s4.x; sv[i + k + 1] = s4.y; sv[i + k + 2] = s4.z; sv[i + k + 3] = s4.w;
+                        } else if constexpr (kWide == 2) {
+                            const float2 c2 = __ldg(reinterpret_cast<const float2 *>(row + k));
+                            const float2 s2 = __ldg(reinterpret_cast<const float2 *>(row + half + k));
+                            cv[i + k] = c2.x; cv[i + k + 1] = c2.y;
+                            sv[i + k] = s2.x; sv[i + k + 1] = s2.y;
+                        }
                     }
                 } else {
 #pragma unroll
@@ -557,9 +565,10 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
         walk(std::integral_constant<int, 0>{});
         walk(std::integral_constant<int, 1>{});
     } else {
-        __shared__ float part[kWarps][2][SKINNY_MAX_HEAD];
+        // every head's lanes by themselves: HP heads of D elements are no more than 32 lanes' pairs
+        __shared__ float part[kWarps][2][32 * 2 * kPairs];
         auto keep = [&](int side) {
-            if (!a.partial) return;
+            if (!a.partial || hs >= HP) return;
 #pragma unroll
             for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -568,14 +577,10 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                     dw[j][ab].get(all);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float v = all[i];
-                        float t = 0.f;
-                        for (int i2 = 0; i2 < HP; ++i2) t += __shfl_sync(0xFFFFFFFFu, v, sub + i2 * L);
-                        v = t;
                         // INTER: pair i's first or second, in the piece that holds it
                         const int e = INTER ? (2 * i < V ? ea[j] : eb[j]) : ab ? eb[j] : ea[j];
                         const int k = INTER ? 2 * i % V + ab : i;
-                        if (hs == 0 && e >= 0) part[warp][side][e + k] = v;
+                        if (e >= 0) part[warp][side][hs * D + e + k] = all[i];
                     }
                 }
         };
@@ -589,29 +594,31 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             const int side = i >= D, e = i - side * D;
             float v = 0.f;
 #pragma unroll
-            for (int q = 0; q < kWarps; ++q) v += part[q][side][e];
+            for (int q = 0; q < kWarps; ++q)
+                for (int g = 0; g < HP; ++g) v += part[q][side][g * D + e];
             if (gridDim.x > 1) a.partial[((int64_t)blockIdx.x * 2 + side) * D + e] = v;
             else if (a.side[side].dw) a.side[side].dw[e] = v;
         }
     }
 }
 
-// The CTAs' sums, 32 elements a CTA: eight warps take every eighth part, then their sums in order.
-__global__ void __launch_bounds__(kThreads) heads_weight_grad_kernel(const float *partial, int parts, int D, float *qw,
-                                                                     float *kw)
+// The CTAs' sums, 32 elements a CTA: its warps take the parts in turn, then their sums in order.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) heads_weight_grad_kernel(const float *partial, int parts, int D, float *qw,
+                                                                           float *kw)
 {
-    __shared__ float sum[kWarps][32];
+    __shared__ float sum[kSumWarps][32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (i < 2 * D)
-#pragma unroll 8
-        for (int q = warp; q < parts; q += kWarps) v += __ldcg(partial + (int64_t)q * 2 * D + i);
+#pragma unroll 10
+        for (int q = warp; q < parts; q += kSumWarps) v += __ldcg(partial + (int64_t)q * 2 * D + i);
     sum[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && i < 2 * D) {
-        for (int q = 1; q < kWarps; ++q) v += sum[q][lane];
+        for (int q = 1; q < kSumWarps; ++q) v += sum[q][lane];
         float *out = i < D ? qw : kw;
         if (out) out[i < D ? i : i - D] = v;
     }
@@ -681,7 +688,8 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
         const int rounds = (p.chunks + L - 1) / L, best = (p.chunks + p.L - 1) / p.L;
         if (rounds * (32 / p.L) <= best * (32 / L)) p.L = L;
     }
-    p.table4 = a.R % 8 == 0 && reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
+    const uintptr_t table = reinterpret_cast<uintptr_t>(a.table);
+    p.together = a.R % 8 == 0 && table % 16 == 0 ? 4 : a.R % 4 == 0 && table % 8 == 0 ? 2 : 1;
     p.inv_d = 1.f / (float)a.D;
     const int64_t ctas = 2ll * c.num_sms < kHeadsParts ? 2ll * c.num_sms : kHeadsParts;      // what an SM holds
     int64_t steps = 0;
@@ -698,8 +706,8 @@ cudaError_t launch_heads(const HeadsArgs &a, const CallCtx &c, cudaStream_t stre
     int parts = grid, D = a.D;
     float *qw = a.side[0].dw, *kw = a.side[1].dw;
     void *args[] = {&partial, &parts, &D, &qw, &kw};
-    return launch_plain((const void *)heads_weight_grad_kernel, dim3((unsigned)((2 * D + 31) / 32)), kThreads, 0, stream,
-                        c.pdl, args);
+    return launch_plain((const void *)heads_weight_grad_kernel, dim3((unsigned)((2 * D + 31) / 32)), 32 * kSumWarps, 0,
+                        stream, c.pdl, args);
 }
 
 }  // namespace skinny
