@@ -21,18 +21,17 @@
 //     MMAs of the next tile go on for two sets.  With a gated activation a CTA's
 //     lanes are 64 gates and their 64 ups; half of the rows of each change sides
 //     through shared memory, so that all eight warps have the same work.
-// What bounds it: the tensor cores, whose sums are held up where a set is read, and
-// at each call's start and last tile.  GB300: 4864 x 4096 x 8192 185 us (1760 TFLOP/s,
-// 90% of the library's plain product), 8192 rows SwiGLU 2048 x 7168 with the sums kept
-// 288, its two backward products 287 and 304 (251 the library's), 2047 rows 7168 x
-// 2048 38, with bias and residual 44 (35).
+// What bounds it: the tensor cores, and each call's start and last tile.  GB300:
+// 4864 x 4096 x 8192 174 us (1875 TFLOP/s, 98% of the library's plain product), 8192
+// rows SwiGLU 2048 x 7168 with the sums kept 266, its two backward products 254 and
+// 255 (251 the library's), 2047 rows 7168 x 2048 with bias and residual 43 (35).
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing
 // from there on, and both CTAs of a pair still meet at the end.
 #include <cuda.h>
 
 #include "experts_gemm.h"
 #include "product.cuh"
-#include "tma.cuh"
+#include "tma_stack.cuh"
 
 namespace skinny {
 namespace {
@@ -88,6 +87,12 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *ma
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(cluster_bar) : "memory");
 }
 
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar) : "memory");
+}
 // The issuer waits for every stage, so all copies have landed once both CTAs meet at the end.  After a give-up
 // some stages may never be complete on the barrier: a time in which any copy lands.
 __device__ __forceinline__ void let_land() {
@@ -102,6 +107,7 @@ struct Params {
     Epilogue e;
     int nt, rt;          // tiles along A and along the rows
     int boxes;           // 64-step boxes of the depth
+    int a3, b3;          // crossed operands by views [index / 64][step][64]: both boxes of a stage in one copy
     int *status;
     uint64_t budget_ns;
 };
@@ -169,45 +175,64 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- TMA producer
-            int64_t i = 0;
-            bool go = true;
-            for (int64_t t = first; go && t < tiles; t += pairs) {
-                int tn, tr;
-                tile_at(p, t, tn, tr);
-                const int n0 = tn * 2 * TA + rank * TA, r0 = tr * 256 + rank * 128;
-                for (int k = 0; k < p.boxes; ++k, ++i) {
-                    const int s = (int)(i % kStages), c = k * 64;
-                    if (i >= kStages && !mbar_wait_bounded(empty(s), (uint32_t)((i / kStages - 1) & 1), p.budget_ns)) {
-                        report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitProducerEmpty);
-                        go = false;
-                        break;
-                    }
+        // ---- TMA producer; the warp stays together and counts the ring's place, as the issuer.  An operand is one
+        // copy a stage where its tensor map can say so (8192 x 4096 x 7168, both crossed: 303 us by one lane with two
+        // copies each, 288 with one, 255 so).
+        const bool one = elect_one();
+        int s = 0;
+        uint32_t phase = 1;                          // the ring is free at first
+        bool go = true;
+        for (int64_t t = first; go && t < tiles; t += pairs) {
+            int tn, tr;
+            tile_at(p, t, tn, tr);
+            const int n0 = tn * 2 * TA + rank * TA, r0 = tr * 256 + rank * 128;
+            for (int k = 0; k < p.boxes; ++k) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), phase, p.budget_ns))) {
+                    if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitProducerEmpty);
+                    go = false;
+                    break;
+                }
+                const int c = k * 64;
+                const uint32_t st = base + s * kStage, bar = mapa_shared(full(s), 0);
+                if (one) {
                     if (rank == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(2 * kStage));
-                    const uint32_t st = base + s * kStage, bar = mapa_shared(full(s), 0);
                     if constexpr (AX) {
-                        pair_load_2d(st, &maps.a, n0, c, bar);
-                        pair_load_2d(st + kBox, &maps.a, n0 + 64, c, bar);
+                        if (p.a3) {
+                            pair_load_3d(st, &maps.a, 0, c, n0 / 64, bar);
+                        } else {
+                            pair_load_2d(st, &maps.a, n0, c, bar);
+                            pair_load_2d(st + kBox, &maps.a, n0 + 64, c, bar);
+                        }
+                    } else if constexpr (GATED) {    // a stack of two: the gates' rows and the ups'
+                        pair_load_3d(st, &maps.a, c, n0, 0, bar);
                     } else {
                         pair_load_2d(st, &maps.a, c, n0, bar);
-                        if (GATED) pair_load_2d(st + kBox, &maps.a, c, p.e.cols + n0, bar);
                     }
                     if constexpr (BX) {
-                        pair_load_2d(st + kHalf, &maps.b, r0, c, bar);
-                        pair_load_2d(st + kHalf + kBox, &maps.b, r0 + 64, c, bar);
+                        if (p.b3) {
+                            pair_load_3d(st + kHalf, &maps.b, 0, c, r0 / 64, bar);
+                        } else {
+                            pair_load_2d(st + kHalf, &maps.b, r0, c, bar);
+                            pair_load_2d(st + kHalf + kBox, &maps.b, r0 + 64, c, bar);
+                        }
                     } else {
                         pair_load_2d(st + kHalf, &maps.b, c, r0, bar);
                     }
                 }
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            if (!go) let_land();
         }
+        if (!go && one) let_land();
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
             // ---- MMA issuer: the warp stays together, so that what the MMAs take is uniform, and the ring's
-            // place is counted, not divided for (4864 x 4096 x 8192: 223 us by one lane with divisions)
+            // place is counted, not divided for (4864 x 4096 x 8192: 223 us by one lane with divisions, 185 so,
+            // 174 with the producer's too)
             constexpr uint32_t idesc = product_idesc<256, 256, AX, BX>();
             constexpr uint64_t kStepA = AX ? 2048 >> 4 : 32 >> 4, kStepB = BX ? 2048 >> 4 : 32 >> 4;
             const uint64_t da = operand_desc<AX>(base, 0), db = operand_desc<BX>(base + kHalf, 0);
@@ -413,15 +438,21 @@ bool linear_pair_faster(const ProductArgs &a, int num_sms) {
 
 cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStream_t stream) {
     const bool gated = act_gated(a.act), ax = a.A.crossed, bx = a.B.crossed;
-    const int TA = gated ? 64 : 128, arows = gated ? 2 * a.cols : a.cols;
+    const int TA = gated ? 64 : 128;
+    const bool a3 = ax && a.cols % 64 == 0, b3 = bx && a.rows % 64 == 0;
     Maps maps;
-    if (!(ax ? encode_bf16_2d(&maps.a, a.A.p, a.cols, a.depth, a.A.ld, 64)
-             : encode_bf16_2d(&maps.a, a.A.p, a.depth, arows, a.A.ld, TA)) ||
-        !(bx ? encode_bf16_2d(&maps.b, a.B.p, (int)a.rows, a.depth, a.B.ld, 64)
-             : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, 128)))
+    if (!(a3      ? encode_bf16_3d(&maps.a, a.A.p, a.cols, a.depth, a.A.ld, 64, 2)
+          : ax    ? encode_bf16_2d(&maps.a, a.A.p, a.cols, a.depth, a.A.ld, 64)
+          : gated ? encode_bf16_stack(&maps.a, a.A.p, a.depth, a.cols, 2, a.A.ld, a.A.ld * a.cols, 64, 2)
+                  : encode_bf16_2d(&maps.a, a.A.p, a.depth, a.cols, a.A.ld, 128)) ||
+        !(b3   ? encode_bf16_3d(&maps.b, a.B.p, (int)a.rows, a.depth, a.B.ld, 64, 2)
+          : bx ? encode_bf16_2d(&maps.b, a.B.p, (int)a.rows, a.depth, a.B.ld, 64)
+               : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, 128)))
         return cudaErrorInvalidValue;
     Params p{};
     p.e = epilogue_of(a);
+    p.a3 = a3;
+    p.b3 = b3;
     p.nt = (a.cols + 2 * TA - 1) / (2 * TA);
     p.rt = (int)((a.rows + 255) / 256);
     p.boxes = (a.depth + 63) / 64;

@@ -15,8 +15,8 @@ __device__ __forceinline__ void tma_load_stack(uint32_t dst, const CUtensorMap *
 }
 
 // Host side (tmem_gemm.cu).  bf16 [n, rows, cols], row stride ld, matrix stride
-// lde (elements), boxes of 64 columns x box_rows rows of one matrix.
+// lde (elements), boxes of 64 columns x box_rows rows of box_n matrices.
 bool encode_bf16_stack(CUtensorMap *map, const void *ptr, int cols, int64_t rows, int n, int64_t ld, int64_t lde,
-                       int box_rows);
+                       int box_rows, int box_n = 1);
 
 }  // namespace skinny

@@ -645,15 +645,15 @@ bool encode_bf16_2d(CUtensorMap *map, const void *ptr, int cols, int rows, int64
 }
 
 // bf16 [n, rows, cols] with row stride ld and matrix stride lde (elements),
-// boxes of 64 columns x box_rows rows of one matrix, 128-byte swizzle, zeros
+// boxes of 64 columns x box_rows rows of box_n matrices, 128-byte swizzle, zeros
 // outside a matrix.
 bool encode_bf16_stack(CUtensorMap *map, const void *ptr, int cols, int64_t rows, int n, int64_t ld, int64_t lde,
-                       int box_rows) {
+                       int box_rows, int box_n) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)lde * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_n};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
