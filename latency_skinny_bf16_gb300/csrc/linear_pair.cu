@@ -15,7 +15,7 @@
 //     in rotation, eight warps add each set into fp32 registers (128 rows of one
 //     output each) while the tensor cores work on the other.  Reading a set holds
 //     the tensor cores up, whatever it overlaps (4864 x 4096 x 8192:
-//     197 us with 16 MMAs a set, 189 with 32, 185 with 64); 64 keep the bound of
+//     181 us with 16 MMAs a set, 177 with 32, 174 with 64); 64 keep the bound of
 //     the products, 64 * 2 * 2^-24 = 7.6e-6 of the terms' sum (measured: a third).
 //   * At a tile's end these warps run the epilogue from their registers, and the
 //     MMAs of the next tile go on for two sets.  With a gated activation a CTA's
@@ -24,7 +24,8 @@
 // What bounds it: the tensor cores, and each call's start and last tile.  GB300:
 // 4864 x 4096 x 8192 174 us (1875 TFLOP/s, 98% of the library's plain product), 8192
 // rows SwiGLU 2048 x 7168 with the sums kept 266, its two backward products 254 and
-// 255 (251 the library's), 2047 rows 7168 x 2048 with bias and residual 43 (35).
+// 255 (251 the library's), 2048 rows 7168 x 2048 35 (35), with
+// bias and residual 43.
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing
 // from there on, and both CTAs of a pair still meet at the end.
 #include <cuda.h>
@@ -425,15 +426,15 @@ cudaError_t linear_pair_prepare() {
     return e;
 }
 
-// Up to 64 rows the tiles of 256 are mostly empty: 64 rows 24576 x 1536 22.6 us, and 15.3 with the depth split.
-// Above, by the time of each: a tile's 0.33 us a box and 2.5 beside.  GB300, us, this kernel and the other: 1024 rows
-// 7168 x 2048 25.8 and 29.7, 2112 x 7168 39.4 and 31.4, 2048 x 2048 14.7 and 16.1; 192 rows 7168 x 2048 15.2 and 16.2;
-// 128 rows 15.2 and 15.0; 384 rows 24576 x 1536 30.2 and 29.3, 512 rows 30.9 and 39.5.
+// Up to 64 rows the tiles of 256 are mostly empty: 64 rows 24576 x 1536 22.6 us, and 15.2 with the depth split.
+// Above, by the time of each: 0.276 us a box, 0.5 a tile and 4 a call.  GB300, us, this kernel and the other: 1024 rows
+// 7168 x 2048 23.6 and 29.7, 2112 x 7168 35.6 and 30.9, 2048 x 2048 14.1 and 15.3; 192 rows 7168 x 2048 15.0 and 15.2;
+// 128 rows 14.8 and 14.4; 512 rows 24576 x 1536 28.2 and 38.8, 384 rows 26.9 and 28.7 (where it takes the other).
 bool linear_pair_faster(const ProductArgs &a, int num_sms) {
     if (a.rows <= 64 && !a.B.crossed) return false;
     const int64_t wide = act_gated(a.act) ? 128 : 256, pairs = num_sms / 2;
     const int64_t tiles = (a.rows + 255) / 256 * ((a.cols + wide - 1) / wide), boxes = (a.depth + 63) / 64;
-    return (tiles + pairs - 1) / pairs * (330 * boxes + 2500) + 1500 < linear_tc_ns(a, num_sms);
+    return (tiles + pairs - 1) / pairs * (276 * boxes + 500) + 4000 < linear_tc_ns(a, num_sms);
 }
 
 cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStream_t stream) {
