@@ -185,3 +185,40 @@ def test_a_wait_that_gives_up_reports_and_later_calls_work(M, act, backend):
         assert sk.skinny_get_device_status() & 0xFF == sk.SKINNY_ERR_DEVICE_TIMEOUT
         assert torch.equal(sk.linear(x, w, activation=act), want)
     assert sk.skinny_get_device_status() == 0
+
+
+@pytest.mark.parametrize("pdl", [1, 2])
+def test_beside_the_other_kernels_with_tensor_memory(pdl):
+    """The projections, the experts' products and these products by turns, each allowed to start while the one
+    before it still runs: all of them take tensor memory, and none waits for another's."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def rand(*shape):
+        return (torch.randn(shape, generator=g, device="cuda") * 0.1).bfloat16()
+
+    x, big, w, we = rand(40, 1024), rand(1300, 1024), rand(2112, 1024), rand(8, 512, 1024)
+    offsets = torch.tensor([0, 5, 10, 15, 20, 25, 30, 35, 40], dtype=torch.int32, device="cuda")
+    q = rand(40, 8, 128)
+
+    def steps():
+        out = []
+        for i in range(12):
+            with sk.options(backend=sk.SKINNY_BACKEND_TCGEN05):
+                out.append(sk.gemm(x, w))
+                out.append(sk.experts_gemm(x, offsets, we))
+                out.append(sk.linear(big[:100 + 100 * i], w, activation="silu"))
+            with sk.options(backend=sk.SKINNY_BACKEND_SPLITK):
+                out.append(sk.linear(x[:1 + 3 * i], w, activation="swiglu"))
+                out.append(sk.linear(big[:90], w[:128 + 8 * i]))
+            out.append(sk.qk_norm_rope(q, None)[0])
+            out.extend(sk.linear_grad(out[-3][:, :1056], x[:1 + 3 * i], w, activation="swiglu",
+                                      pre=out[-4][:1 + 3 * i])[:2])
+        return out
+
+    want = [t.clone() for t in steps()]
+    torch.cuda.synchronize()
+    with sk.options(pdl=pdl):
+        for _ in range(3):
+            got = steps()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -109,6 +109,44 @@ def test_residual_in_place(M):
     assert torch.equal(y, sk.linear(x, w, residual=r))
 
 
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("M", [3, 70, 600])
+def test_residual_in_place_activated(M, act):
+    g = gen(15)
+    x, w, y = rand(g, M, 264), rand(g, 2 * 136, 264, scale=1 / 16), rand(g, M, 136 if act == "swiglu" else 272, dtype=torch.float32)
+    want = sk.linear(x, w, activation=act, residual=y.clone())
+    assert want.dtype == torch.float32
+    assert torch.equal(sk.linear(x, w, activation=act, residual=y, out=y), want)
+
+
+@pytest.mark.parametrize("ld", [(1 << 30) + 8, (1 << 30) + 3])
+def test_rows_past_32_bits(ld):
+    """Row strides that carry the last rows past 2^32 bytes, of every operand and output."""
+    g = gen(16)
+    M, N, K = 4, 3, 136
+    x, w, dy = rand(g, M, K), rand(g, N, K), rand(g, M, N)
+    want, dwant = sk.linear(x, w), sk.linear_grad(dy, x, w, bias_grad=True)
+    bufs = [torch.empty(3 * ld + 256, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    far = torch.as_strided(bufs[0], (M, K), (ld, 1))
+    far.copy_(x)
+    out = torch.as_strided(bufs[1], (M, N), (ld, 1))
+    assert torch.equal(sk.linear(far, w, out=out), want)
+    dx = torch.as_strided(bufs[1], (M, K), (ld, 1))
+    got = sk.linear_grad(dy, far, w, dx=dx, bias_grad=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, dwant))
+    wide = torch.as_strided(bufs[0], (N, K), (ld, 1))
+    wide.copy_(w)
+    dw = torch.as_strided(bufs[1], (N, K), (ld, 1))
+    got = sk.linear_grad(dy, x, wide, dw=dw, bias_grad=True)
+    assert torch.equal(sk.linear(x, wide), want) and all(torch.equal(a, b) for a, b in zip(got, dwant))
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_very_many_rows(act):
+    forward(200003, 40, 64, act)
+    backward(70001, 40, 72, act)
+
+
 @pytest.mark.parametrize("M", [1, 40, 100])
 def test_same_sign_sums(M):
     """Nothing cancels: a biased sum would show."""
