@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     using Vs = Vals<V>;
     extern __shared__ __align__(16) uint8_t ring[];
     const HeadsArgs &a = p.a;
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = p.L, HP = 32 / L, hs = lane / L, sub = lane - hs * L;
     const int D = a.D, R = a.R, half = R / 2, rest = (D - R + 1) / 2, turned_chunks = half / V;
@@ -261,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < kBytes; k += 4) asm volatile("st.shared.u32 [%0], %1;" :: "r"(slots + slot(0, i) + k), "r"(0) : "memory");
     griddep_wait();
+    griddep_launch_dependents();
 
     // The lane's chunks: their two pieces' first elements (-1: none) and their pairs, by which the table is read.
     // Halves: elements i and R / 2 + i, then what is not turned in two halves.  INTER: neighbours, pieces c and
@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) heads_weight_grad_kernel(const
                                                                            float *kw)
 {
     __shared__ float sum[kSumWarps][32];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (i < 2 * D)

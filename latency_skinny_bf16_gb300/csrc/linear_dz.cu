@@ -46,8 +46,8 @@ template <int V, bool GATED, int ACT>      // ACT: 0 none, 1 SiLU, 2 GELU
 __global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_constant__ LinearDzArgs p)
 {
     constexpr int G = GATED ? 2 : 1, kBatch = 4;     // rows whose loads go out together
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int n = (blockIdx.x * 32 + lane) * V;
     const int64_t m0 = p.M * blockIdx.y / gridDim.y, m1 = p.M * (blockIdx.y + 1) / gridDim.y;
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_con
 // out[i] = the parts' sums in order.
 __global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float *partial, int parts, int n, float *out)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i >= n) return;
     float v = 0.f;

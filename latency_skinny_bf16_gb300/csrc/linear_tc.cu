@@ -64,6 +64,7 @@ struct Params {
     int boxes;           // 64-step boxes of the depth
     int ta;              // outputs of a tile: 8 to 128 (gated: 64)
     int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
+    Order order;
     int early;           // A may be read before the preceding kernel is done
     int *status;
     uint64_t budget_ns;
@@ -77,7 +78,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     const int TA = p.ta;
     static_assert(!BX || BN >= 64, "crossed boxes hold 64 indexes");
     extern __shared__ uint8_t smem_raw[];
-    griddep_launch_dependents();
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     tc_fence_after();
     if (own_slots(BN) && S > 1) cluster_arrive_relaxed();              // this CTA is there to be sent to
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();
+    if (p.order != Order::kSecond) follow();
 
     float acc[BN];
 #pragma unroll
@@ -275,89 +275,95 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     }
     const bool ok = *failed == 0 && *mma_ok != 0;
     const Epilogue &e = p.e;
-    if (!GATED && S == 1) {                          // from the registers: a thread has all rows of its output
-        const int nl = 32 * (warp & 3) + lane, n = n0 + nl;
-        if (warp >= 2 && ok && nl < TA && n < e.cols) {
-            const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
+    auto epilogue = [&] {
+        if (!GATED && S == 1) {                          // from the registers: a thread has all rows of its output
+            const int nl = 32 * (warp & 3) + lane, n = n0 + nl;
+            if (warp >= 2 && ok && nl < TA && n < e.cols) {
+                const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
 #pragma unroll
-            for (int j = 0; j < BN; ++j) acc[j] += bias;
-            if (e.Z) store_rows(acc, e.Z + r0 * e.ldz + n, e.ldz, live);
-            act_rows(acc, e.act);
-            out_rows(e, acc, r0, n, live);
-        }
-        return;
-    }
-    const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = BN >> shift;      // rows of an owner
-    // kVec rows of an output side by side, the outputs behind one another
-    constexpr int kVec = BN < 32 ? 2 : 4;
-    if (warp >= 2 && ok) {
-        const uint32_t at = base + kSlots + 4u * (uint32_t)(rank * per * 128 + (32 * (warp & 3) + lane) * kVec);
-        uint32_t to = at;
-#pragma unroll
-        for (int j = 0; j < BN; j += kVec) {
-            if ((j & (per - 1)) == 0) to = mapa_shared(at, (uint32_t)(S == 1 ? rank : j / (BN / 8) >> (3 - shift)));
-            if (j < live) {
-                if constexpr (kVec == 2)
-                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]) : "memory");
-                else
-                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
-                                 :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3]) : "memory");
+                for (int j = 0; j < BN; ++j) acc[j] += bias;
+                if (e.Z) store_rows(acc, e.Z + r0 * e.ldz + n, e.ldz, live);
+                act_rows(acc, e.act);
+                out_rows(e, acc, r0, n, live);
             }
-            to += 512u * kVec;
+            return;
         }
-    }
-    if (S > 1) {
-        cluster_arrive_release();
-        cluster_wait_acquire();
-    } else {
-        __syncthreads();
-    }
-    if (!ok) return;
-    // kRows rows of an output a thread at a time, the output's threads taking turns
-    constexpr int kRows = BN < 8 ? BN : 8, kOuts = GATED ? 64 : 128, kTurns = kThreads / kOuts;
-    const float *slots = reinterpret_cast<const float *>(smem + kSlots);
-    const int nl = tid % kOuts, turn = tid / kOuts, n = n0 + nl, mine = min(per, live - rank * per);
-    if (turn >= kTurns || nl >= TA || n >= e.cols) return;
-    const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
-    const float ubias = GATED && e.bias ? bf16_one(ldg_u16(e.bias + e.cols + n)) : 0.f;
-    for (int c = turn * kRows; c < mine; c += kTurns * kRows) {
-        const int rows = min(kRows, mine - c);
-        float z[kRows], up[kRows];
+        const int shift = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3, per = BN >> shift;      // rows of an owner
+        // kVec rows of an output side by side, the outputs behind one another
+        constexpr int kVec = BN < 32 ? 2 : 4;
+        if (warp >= 2 && ok) {
+            const uint32_t at = base + kSlots + 4u * (uint32_t)(rank * per * 128 + (32 * (warp & 3) + lane) * kVec);
+            uint32_t to = at;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) z[i] = up[i] = 0.f;
-        for (int s = 0; s < S; ++s) {
-            const float *slot = slots + (s * per + c) * 128 + nl * kVec;
+            for (int j = 0; j < BN; j += kVec) {
+                if ((j & (per - 1)) == 0) to = mapa_shared(at, (uint32_t)(S == 1 ? rank : j / (BN / 8) >> (3 - shift)));
+                if (j < live) {
+                    if constexpr (kVec == 2)
+                        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};"
+                                     :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]) : "memory");
+                    else
+                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                                     :: "r"(to), "f"(acc[j]), "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3])
+                                     : "memory");
+                }
+                to += 512u * kVec;
+            }
+        }
+        if (S > 1) {
+            cluster_arrive_release();
+            cluster_wait_acquire();
+        } else {
+            __syncthreads();
+        }
+        if (!ok) return;
+        // kRows rows of an output a thread at a time, the output's threads taking turns
+        constexpr int kRows = BN < 8 ? BN : 8, kOuts = GATED ? 64 : 128, kTurns = kThreads / kOuts;
+        const float *slots = reinterpret_cast<const float *>(smem + kSlots);
+        const int nl = tid % kOuts, turn = tid / kOuts, n = n0 + nl, mine = min(per, live - rank * per);
+        if (turn >= kTurns || nl >= TA || n >= e.cols) return;
+        const float bias = e.bias ? bf16_one(ldg_u16(e.bias + n)) : 0.f;
+        const float ubias = GATED && e.bias ? bf16_one(ldg_u16(e.bias + e.cols + n)) : 0.f;
+        for (int c = turn * kRows; c < mine; c += kTurns * kRows) {
+            const int rows = min(kRows, mine - c);
+            float z[kRows], up[kRows];
 #pragma unroll
-            for (int i = 0; i < kRows; i += kVec) {
-                if (i >= rows) continue;
-                using Vec = typename std::conditional<kVec == 2, float2, float4>::type;
-                const Vec fz = *reinterpret_cast<const Vec *>(slot + i * 128);
-                const Vec fu = *reinterpret_cast<const Vec *>(slot + i * 128 + (GATED ? 64 * kVec : 0));
-                const float *v = reinterpret_cast<const float *>(&fz), *w = reinterpret_cast<const float *>(&fu);
+            for (int i = 0; i < kRows; ++i) z[i] = up[i] = 0.f;
+            for (int s = 0; s < S; ++s) {
+                const float *slot = slots + (s * per + c) * 128 + nl * kVec;
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    z[i + k] += v[k];
-                    if (GATED) up[i + k] += w[k];
+                for (int i = 0; i < kRows; i += kVec) {
+                    if (i >= rows) continue;
+                    using Vec = typename std::conditional<kVec == 2, float2, float4>::type;
+                    const Vec fz = *reinterpret_cast<const Vec *>(slot + i * 128);
+                    const Vec fu = *reinterpret_cast<const Vec *>(slot + i * 128 + (GATED ? 64 * kVec : 0));
+                    const float *v = reinterpret_cast<const float *>(&fz), *w = reinterpret_cast<const float *>(&fu);
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) {
+                        z[i + k] += v[k];
+                        if (GATED) up[i + k] += w[k];
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            z[i] += bias;
-            up[i] += ubias;
-        }
-        const int64_t r = r0 + rank * per + c;
-        if (e.Z) {
-            store_rows(z, e.Z + r * e.ldz + n, e.ldz, rows);
-            if (GATED) store_rows(up, e.Z + r * e.ldz + e.cols + n, e.ldz, rows);
-        }
-        act_rows(z, e.act);
-        if (GATED) {
+            for (int i = 0; i < kRows; ++i) {
+                z[i] += bias;
+                up[i] += ubias;
+            }
+            const int64_t r = r0 + rank * per + c;
+            if (e.Z) {
+                store_rows(z, e.Z + r * e.ldz + n, e.ldz, rows);
+                if (GATED) store_rows(up, e.Z + r * e.ldz + e.cols + n, e.ldz, rows);
+            }
+            act_rows(z, e.act);
+            if (GATED) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) z[i] *= up[i];
+                for (int i = 0; i < kRows; ++i) z[i] *= up[i];
+            }
+            out_rows(e, z, r, n, rows);
         }
-        out_rows(e, z, r, n, rows);
-    }
+    };
+    epilogue();
+    if (p.order == Order::kSecond) follow();
 }
 
 template <int BN, bool GATED, bool AX, bool BX>
@@ -454,6 +460,7 @@ cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_
         return cudaErrorInvalidValue;
     p.e = epilogue_of(a);
     p.early = a.early;
+    p.order = a.order;
     p.status = c.status;
     p.budget_ns = c.budget_ns;
     const int64_t ctas = plan.ctas;
