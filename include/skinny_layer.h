@@ -56,8 +56,7 @@ typedef enum {
  * Rows that are not 16-byte aligned (pointer, ldx, ldw multiples of 8 elements) are taken too: they are
  * laid out in the workspace first, which is 0 bytes without such rows.
  *
- * With PDL on (SKINNY_OPT_PDL), W is read before the kernel waits for the preceding kernel in the
- * stream, as in skinny_gemm_bf16.
+ * Unlike skinny_gemm_bf16, W may be written by the kernel just before on the stream, with PDL on as well.
  *
  * SKINNY_OPT_FORCE_BACKEND, also for the products of the backward pass: SKINNY_BACKEND_TCGEN05 is the
  * kernel by pairs of SMs, SKINNY_BACKEND_SPLITK the one with the depth split over a cluster.

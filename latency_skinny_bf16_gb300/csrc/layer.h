@@ -38,7 +38,6 @@ struct ProductArgs {
     uint16_t *Z;             // NULL: not kept
     int64_t ldz;
     int out_bf16;
-    bool early;              // A is a weight that no preceding kernel of the stream writes
     Order order;
 };
 // a depth of 0 (linear_empty.cu)

@@ -164,7 +164,7 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
     if (st != SKINNY_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     ProductArgs a{{W, ldw, false}, {X, ldx, false}, M, N, K, act, bias, R, ldr, Y, ldy, Z, ldz, out_dtype == SKINNY_BF16,
-                  true, Order::kAlone};
+                  Order::kAlone};
     const Space sp = linear_space(X, ldx, W, ldw, M, K, rows);
     if (sp.bytes > 0) {
         uint8_t *space = static_cast<uint8_t *>(workspace);
@@ -176,7 +176,6 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
         if (sp.w >= 0) {
             pw = {W, ldw, rows, K, reinterpret_cast<uint16_t *>(space + sp.w)};
             a.A = {pw.to, pad8(K), false};
-            a.early = false;
         }
         if (launch_rows_pack(px, pw, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
     }
@@ -252,14 +251,14 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
         if (to) dz = {to, pad8(rows), false};
     }
     if (dX) {
-        const ProductArgs a{wo, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1, false,
+        const ProductArgs a{wo, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1,
                             dW ? Order::kFirst : Order::kAlone};
         st = launch_product(a, c, s);
         if (st != SKINNY_OK) return st;
     }
     if (dW) {
         const ProductArgs a{xo, {dz.p, dz.ld, true}, rows, K, M, SKINNY_ACT_NONE, nullptr, nullptr, 0, dW, lddw, nullptr, 0,
-                            1, false, dX ? Order::kSecond : Order::kAlone};
+                            1, dX ? Order::kSecond : Order::kAlone};
         st = launch_product(a, c, s);
         if (st != SKINNY_OK) return st;
     }

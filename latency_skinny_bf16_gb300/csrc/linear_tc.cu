@@ -20,7 +20,7 @@
 // What bounds it: device memory for the weight, and, as far as calls follow each
 // other, what lies between the preceding call's end and the first sums, and between
 // the last sums and the stores (about 3 us).  GB300, us, chained with PDL, one token
-// and 64: 2112 x 7168 8.0 and 10.3 (floor 4.5), 24576 x 1536 13.0 and 15.2 (11.3),
+// and 64: 2112 x 7168 8.1 and 10.4 (floor 4.5), 24576 x 1536 13.0 and 15.2 (11.3),
 // SwiGLU 2048 x 7168 11.3 and 13.9 (8.8), 8192 x 8192 21.7 and 24.9 (20.0).
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing.
 #include <cuda.h>
@@ -65,7 +65,6 @@ struct Params {
     int ta;              // outputs of a tile: 8 to 128 (gated: 64)
     int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
     Order order;
-    int early;           // A may be read before the preceding kernel is done
     int *status;
     uint64_t budget_ns;
 };
@@ -127,13 +126,19 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         *mma_ok = 0;
         *failed = 0;
         fence_mbarrier_init_cluster();
-        if (p.early) {                               // the weight's first boxes, before anything is waited for
-            for (int i = 0; i < pre; ++i) {
-                mbar_arrive_expect_tx(full(i), (uint32_t)tx);
-                load_a(i, i);
+        prefetch_tensormap(&maps.b);
+        // A's first boxes, to L2 only: whatever the preceding kernel still writes, the copies behind the wait see it
+        // (one token, 2112 x 7168: 8.9 us without, 8.5 so, 8.4 with copies to shared memory here)
+        for (int i = 0; p.order != Order::kSecond && i < pre; ++i) {
+            const int c = (b0 + i) * 64;
+            if constexpr (AX) {
+                tma_prefetch_2d(&maps.a, n0, c);
+                tma_prefetch_2d(&maps.a, n0 + 64, c);
+            } else {
+                tma_prefetch_2d(&maps.a, c, n0);
+                if (GATED) tma_prefetch_2d(&maps.a, c, p.e.cols + n0);
             }
         }
-        prefetch_tensormap(&maps.b);
     }
     if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
     tc_fence_before();
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                     tma_load_2d(st, &maps.b, c, (int)r0, full(s));
                 }
             };
-            for (int i = 0; !p.early && i < pre; ++i) {
+            for (int i = 0; i < pre; ++i) {
                 mbar_arrive_expect_tx(full(i), (uint32_t)tx);
                 load_a(i, i);
             }
@@ -459,7 +464,6 @@ cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_
              : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, BN)))
         return cudaErrorInvalidValue;
     p.e = epilogue_of(a);
-    p.early = a.early;
     p.order = a.order;
     p.status = c.status;
     p.budget_ns = c.budget_ns;

@@ -222,3 +222,45 @@ def test_beside_the_other_kernels_with_tensor_memory(pdl):
             got = steps()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("between", [False, True])
+@pytest.mark.parametrize("M,N,K,act", [(1, 2112, 4096, None), (64, 1024, 1024, "swiglu"), (5, 300, 201, "gelu"),
+                                       (600, 2048, 2048, None)])
+@pytest.mark.parametrize("pdl", [1, 2])
+def test_weights_that_a_call_just_before_writes(M, N, K, act, between, pdl):
+    """In the stream's order, whatever starts early: as with a wait between any two calls."""
+    rows = 2 * N if act == "swiglu" else N
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def new(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    def buf(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, device="cuda", dtype=dtype)
+
+    lefts, right, few, x, z = [new(rows, 64) for _ in range(6)], new(K, 64), new(64, K), new(M, K), new(M, rows)
+    w, other, dy = buf(rows, K), buf(M, 64), new(M, N)
+    outs, grads = [buf(M, N) for _ in lefts], [buf(M, K) for _ in lefts]
+    space = buf(sk.linear_grad_workspace(dy, x, w, act), dtype=torch.uint8)
+
+    def run(wait):
+        w.zero_()
+        wait()
+        for left, out, dx in zip(lefts, outs, grads):
+            sk.linear(left, right, out=w)
+            if between:
+                wait()
+                sk.linear(x, few, out=other)
+            wait()
+            sk.linear(x, w, activation=act, out=out)
+            wait()
+            sk.linear_grad(dy, x, w, z if act else None, act, dx=dx, weight_grad=False, workspace=space)
+            wait()
+        torch.cuda.synchronize()
+        return [t.clone() for t in outs + grads]
+
+    with sk.options(pdl=pdl):
+        want = run(torch.cuda.synchronize)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
