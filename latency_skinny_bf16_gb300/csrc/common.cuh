@@ -72,6 +72,11 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// What precedes in the stream is done, and what follows may start.
+__device__ __forceinline__ void follow() {
+    griddep_wait();
+    griddep_launch_dependents();
+}
 
 // ------------------------------------------------------------------ shared-memory addresses
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

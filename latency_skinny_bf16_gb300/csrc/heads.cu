@@ -259,8 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     for (int i = 0; i < kDepth * kPieces; ++i)
 #pragma unroll
         for (int k = 0; k < kBytes; k += 4) asm volatile("st.shared.u32 [%0], %1;" :: "r"(slots + slot(0, i) + k), "r"(0) : "memory");
-    griddep_wait();
-    griddep_launch_dependents();
+    follow();
 
     // The lane's chunks: their two pieces' first elements (-1: none) and their pairs, by which the table is read.
     // Halves: elements i and R / 2 + i, then what is not turned in two halves.  INTER: neighbours, pieces c and
@@ -608,8 +607,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) heads_weight_grad_kernel(const
                                                                            float *kw)
 {
     __shared__ float sum[kSumWarps][32];
-    griddep_wait();
-    griddep_launch_dependents();
+    follow();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (i < 2 * D)

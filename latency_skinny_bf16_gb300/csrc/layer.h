@@ -15,14 +15,15 @@ struct Operand {
     bool crossed;
 };
 
-// These kernels let the next of the stream start (programmatic dependent launch) once what precedes themselves is done, so
-// that a kernel which reads a weight before it waits runs beside its predecessor alone, never beside the one before that.
-// Of a backward pass's two products the second needs nothing of the first: it starts beside the first's last tiles, and
-// waits for it at its own end, so that what follows may take both as done.  GB300, us, both products and dz, one behind
-// the other and so: 3000 rows 4096 x 2048 74.5 and 63.7, 1500 rows 1500 x 1500 GELU 41.3 and 30.9, 64 rows SwiGLU
-// 2048 x 7168 51.0 and 48.4, 300 rows 600 x 700 17.7 and 13.6; where the tiles fill the GPU, the same
-// (2048 x 2048 x 2048 34.3 and 34.3).
-enum class Order : int { kAlone, kFirst, kSecond };
+// These kernels let the next of the stream start (programmatic dependent launch) once what precedes themselves is done.
+// One that needs nothing of its predecessor in the same call is marked `beside`: it starts at once, as its successor in
+// the call does, and waits for the predecessor at its own end, so that what follows may take both as done.  So run, in a
+// backward pass, dz beside the laying out of rows, the input's gradient beside the last sums of the bias gradient, the
+// weight's beside the input's last tiles.  GB300, us, the two products one behind the other and so: 3000 rows
+// 4096 x 2048 74.5 and 63.7, 1500 rows 1500 x 1500 GELU 41.3 and 30.9, 300 rows 600 x 700 17.7 and 13.6; where the tiles
+// fill the GPU, the same (2048 x 2048 x 2048 34.3 and 34.3).  The other two, with a bias gradient: 4099 rows 1437 x 2049
+// SiLU 98 and 92.7, 33 rows 513 x 511 GELU 13.1 and 11.1.  The last of a call lets the next start at its end only: 64 rows
+// SwiGLU 2048 x 7168 47.3, from its start 52.0.
 // Y[r][n] = epilogue(sum_c B(r, c) A(n, c)), r < rows, n < cols.  A gated
 // activation takes A(cols + n, c) beside it.
 struct ProductArgs {
@@ -38,7 +39,8 @@ struct ProductArgs {
     uint16_t *Z;             // NULL: not kept
     int64_t ldz;
     int out_bf16;
-    Order order;
+    bool beside;             // of the kernel before: nothing of it is read or written
+    bool last;               // of a call; read with beside
 };
 // a depth of 0 (linear_empty.cu)
 cudaError_t launch_linear_empty(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
@@ -74,8 +76,13 @@ struct LinearDzArgs {
     float *partial;          // kDbiasParts rows
     int64_t M;
     int N, act;
+    bool beside;
 };
 constexpr int kDbiasParts = 64;
+inline int dbias_parts(int64_t M) {      // four rows a thread of eight at least, what it loads at once
+    const int64_t want = (M + 31) / 32;
+    return want < kDbiasParts ? (int)want : kDbiasParts;
+}
 cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream_t stream);
 
 // Heads of queries (side 0) and keys (side 1).

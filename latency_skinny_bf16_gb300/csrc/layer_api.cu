@@ -164,7 +164,7 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
     if (st != SKINNY_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     ProductArgs a{{W, ldw, false}, {X, ldx, false}, M, N, K, act, bias, R, ldr, Y, ldy, Z, ldz, out_dtype == SKINNY_BF16,
-                  Order::kAlone};
+                  false, true};
     const Space sp = linear_space(X, ldx, W, ldw, M, K, rows);
     if (sp.bytes > 0) {
         uint8_t *space = static_cast<uint8_t *>(workspace);
@@ -231,6 +231,7 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
     const Space sp = grad_space(dY, lddy, X, ldx, W, ldw, M, K, rows, act);
     uint8_t *space = static_cast<uint8_t *>(workspace);
     Operand dz{dY, lddy, false}, xo{X, ldx, true}, wo{W, ldw, true};
+    bool beside = false;             // the next kernel needs nothing of the one before
     if (dX || dW) {
         PackArgs px{}, pw{};
         if (dW && sp.x >= 0) {
@@ -242,23 +243,27 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
             wo = {pw.to, pad8(K), true};
         }
         if (launch_rows_pack(px, pw, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
+        beside = px.from || pw.from;
     }
     if (dbias || ((dX || dW) && sp.dz >= 0)) {
         uint16_t *to = sp.dz >= 0 && (dX || dW) ? reinterpret_cast<uint16_t *>(space + sp.dz) : nullptr;
         const LinearDzArgs d{dY, lddy, act_none ? nullptr : Z, ldz, to, pad8(rows), dbias,
-                             reinterpret_cast<float *>(space + sp.partial), M, N, act};
+                             reinterpret_cast<float *>(space + sp.partial), M, N, act, beside};
         if (launch_linear_dz(d, c, s) != cudaSuccess) return SKINNY_ERR_LAUNCH;
         if (to) dz = {to, pad8(rows), false};
+        beside = dbias && dbias_parts(M) > 1;        // the products do not read the bias gradient
+    } else {
+        beside = false;                              // but the rows laid out
     }
     if (dX) {
         const ProductArgs a{wo, dz, M, K, rows, SKINNY_ACT_NONE, nullptr, nullptr, 0, dX, lddx, nullptr, 0, 1,
-                            dW ? Order::kFirst : Order::kAlone};
+                            beside, !dW};
         st = launch_product(a, c, s);
         if (st != SKINNY_OK) return st;
     }
     if (dW) {
         const ProductArgs a{xo, {dz.p, dz.ld, true}, rows, K, M, SKINNY_ACT_NONE, nullptr, nullptr, 0, dW, lddw, nullptr, 0,
-                            1, dX ? Order::kSecond : Order::kAlone};
+                            1, beside || dX, true};
         st = launch_product(a, c, s);
         if (st != SKINNY_OK) return st;
     }

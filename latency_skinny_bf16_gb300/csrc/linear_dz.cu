@@ -3,10 +3,11 @@
 //     dZ = dY act'(Z);  gated: dY U act'(G) for the gates, dY act(G) for the ups
 // A stream through device memory (dY, Z, dZ once each); the exponentials take three
 // fifths of the issue slots beside it (GB300: 8192 x 2 * 2048 SwiGLU 33 us, 5.0 TB/s;
-// odd widths go element by element, 1001 x 1437 10 us).  A CTA takes 32 lanes
-// of V columns and every eighth of its part of the tokens a row of threads; the
-// bias gradient is summed along a thread's tokens, over the CTA's eight rows and
-// then over the parts by a second kernel, in a fixed order.
+// odd widths go element by element, six CTAs an SM: with its products 1001 x 1437
+// 39.7 us, with three or eight 40.7 and 41.4).  A CTA takes 32 lanes of V columns
+// and every eighth of its part of the tokens a row of threads; the bias gradient is
+// summed along a thread's tokens, over the CTA's eight rows and then over the parts
+// by a second kernel, in a fixed order.
 #include "act.cuh"
 #include "common.cuh"
 #include "experts_gemm.h"
@@ -43,11 +44,11 @@ struct Cols {
 };
 
 template <int V, bool GATED, int ACT>      // ACT: 0 none, 1 SiLU, 2 GELU
-__global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_constant__ LinearDzArgs p)
+__global__ void __launch_bounds__(kThreads, V == 8 ? 3 : 6) linear_dz_kernel(const __grid_constant__ LinearDzArgs p)
 {
     constexpr int G = GATED ? 2 : 1, kBatch = 4;     // rows whose loads go out together
-    griddep_wait();
-    griddep_launch_dependents();
+    if (p.beside) griddep_launch_dependents();
+    else follow();
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int n = (blockIdx.x * 32 + lane) * V;
     const int64_t m0 = p.M * blockIdx.y / gridDim.y, m1 = p.M * (blockIdx.y + 1) / gridDim.y;
@@ -96,7 +97,10 @@ __global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_con
             }
         }
     }
-    if (!p.dbias) return;
+    if (!p.dbias) {
+        if (p.beside) griddep_wait();
+        return;
+    }
     __shared__ float part[kRows][32 * V];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -113,13 +117,13 @@ __global__ void __launch_bounds__(kThreads, 3) linear_dz_kernel(const __grid_con
             p.partial[(int64_t)blockIdx.y * G * p.N + (int64_t)g * p.N + at] = v;
         }
     }
+    if (p.beside) griddep_wait();
 }
 
 // out[i] = the parts' sums in order.
 __global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float *partial, int parts, int n, float *out)
 {
-    griddep_wait();
-    griddep_launch_dependents();
+    follow();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i >= n) return;
     float v = 0.f;
@@ -146,8 +150,7 @@ cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.dY) | reinterpret_cast<uintptr_t>(a.Z) | reinterpret_cast<uintptr_t>(a.dZ);
     const bool wide = bits % 16 == 0 && a.N % 8 == 0 && a.lddy % 8 == 0 && (!a.Z || a.ldz % 8 == 0) && (!a.dZ || a.lddz % 8 == 0);
     const int V = wide ? 8 : 1, rows = gated ? 2 * a.N : a.N;
-    // a part is four rows a thread at least, what it loads at once; one part's sums are the bias gradient itself
-    const int64_t least = 4 * kRows, want = (a.M + least - 1) / least, parts = want < kDbiasParts ? want : kDbiasParts;
+    const int parts = dbias_parts(a.M);          // one part's sums are the bias gradient itself
     LinearDzArgs p = a;
     if (parts == 1) p.partial = a.dbias;
     void *args[] = {&p};
@@ -155,7 +158,7 @@ cudaError_t launch_linear_dz(const LinearDzArgs &a, const CallCtx &c, cudaStream
     cudaError_t e = launch_plain(fn, dim3((unsigned)((a.N + 32 * V - 1) / (32 * V)), (unsigned)parts), kThreads, 0, stream, c.pdl, args);
     if (e != cudaSuccess || !a.dbias || parts == 1) return e;
     const float *partial = a.partial;
-    int np = (int)parts, n = rows;
+    int np = parts, n = rows;
     float *out = a.dbias;
     void *sargs[] = {&partial, &np, &n, &out};
     return launch_plain((const void *)sum_parts_kernel, dim3((unsigned)((rows + kThreads - 1) / kThreads)), kThreads, 0, stream, c.pdl, sargs);

@@ -11,8 +11,7 @@ constexpr int kThreads = 256;
 template <bool GATED>
 __global__ void __launch_bounds__(kThreads) linear_empty_kernel(const __grid_constant__ Epilogue e)
 {
-    griddep_wait();
-    griddep_launch_dependents();
+    follow();
     const int n = blockIdx.x * kThreads + threadIdx.x;
     if (n >= e.cols) return;
     for (int64_t r = blockIdx.y; r < e.rows; r += gridDim.y) {

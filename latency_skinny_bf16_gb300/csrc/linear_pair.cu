@@ -108,7 +108,7 @@ struct Params {
     Epilogue e;
     int nt, rt;          // tiles along A and along the rows
     int boxes;           // 64-step boxes of the depth
-    Order order;
+    int beside, last;
     int a3, b3;          // crossed operands by views [index / 64][step][64]: both boxes of a stage in one copy
     int *status;
     uint64_t budget_ns;
@@ -130,6 +130,7 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
     constexpr int kStages = ring_stages(GATED);
     constexpr int TA = GATED ? 64 : 128;             // a CTA's outputs
     extern __shared__ uint8_t smem_raw[];
+    if (p.beside && !p.last) griddep_launch_dependents();
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
@@ -172,7 +173,7 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
     cluster_arrive_release();                        // both CTAs' barriers are there
     cluster_wait_acquire();
     tc_fence_after();
-    if (p.order != Order::kSecond) follow();
+    if (!p.beside) follow();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
@@ -392,7 +393,7 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
     }
     tc_fence_before();
     __syncthreads();
-    if (p.order == Order::kSecond) follow();
+    if (p.beside) follow();
     cluster_arrive_release();                        // neither CTA reads or signals the other from here on
     cluster_wait_acquire();
     if (warp == 1) {
@@ -458,7 +459,8 @@ cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStrea
     p.nt = (a.cols + 2 * TA - 1) / (2 * TA);
     p.rt = (int)((a.rows + 255) / 256);
     p.boxes = (a.depth + 63) / 64;
-    p.order = a.order;
+    p.beside = a.beside;
+    p.last = a.last;
     p.status = c.status;
     p.budget_ns = c.budget_ns;
     const int64_t tiles = (int64_t)p.nt * p.rt;

@@ -64,7 +64,7 @@ struct Params {
     int boxes;           // 64-step boxes of the depth
     int ta;              // outputs of a tile: 8 to 128 (gated: 64)
     int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
-    Order order;
+    int beside, last;
     int *status;
     uint64_t budget_ns;
 };
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     const int TA = p.ta;
     static_assert(!BX || BN >= 64, "crossed boxes hold 64 indexes");
     extern __shared__ uint8_t smem_raw[];
+    if (p.beside && !p.last) griddep_launch_dependents();
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         prefetch_tensormap(&maps.b);
         // A's first boxes, to L2 only: whatever the preceding kernel still writes, the copies behind the wait see it
         // (one token, 2112 x 7168: 8.9 us without, 8.5 so, 8.4 with copies to shared memory here)
-        for (int i = 0; p.order != Order::kSecond && i < pre; ++i) {
+        for (int i = 0; !p.beside && i < pre; ++i) {
             const int c = (b0 + i) * 64;
             if constexpr (AX) {
                 tma_prefetch_2d(&maps.a, n0, c);
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
     tc_fence_after();
     if (own_slots(BN) && S > 1) cluster_arrive_relaxed();              // this CTA is there to be sent to
     const uint32_t tmem = *tmem_slot;
-    if (p.order != Order::kSecond) follow();
+    if (!p.beside) follow();
 
     float acc[BN];
 #pragma unroll
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         }
     };
     epilogue();
-    if (p.order == Order::kSecond) follow();
+    if (p.beside) follow();
 }
 
 template <int BN, bool GATED, bool AX, bool BX>
@@ -464,7 +465,8 @@ cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_
              : encode_bf16_2d(&maps.b, a.B.p, a.depth, (int)a.rows, a.B.ld, BN)))
         return cudaErrorInvalidValue;
     p.e = epilogue_of(a);
-    p.order = a.order;
+    p.beside = a.beside;
+    p.last = a.last;
     p.status = c.status;
     p.budget_ns = c.budget_ns;
     const int64_t ctas = plan.ctas;

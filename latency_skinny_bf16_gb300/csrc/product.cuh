@@ -37,12 +37,6 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// What precedes in the stream is done, and what follows may start.
-__device__ __forceinline__ void follow() {
-    griddep_wait();
-    griddep_launch_dependents();
-}
-
 struct Epilogue {
     const uint16_t *bias;
     const void *R;

@@ -39,8 +39,7 @@ __device__ __forceinline__ uint4 from_lane(const uint4 &v, int lane) {
 
 __global__ void __launch_bounds__(kThreads) rows_pack_kernel(const __grid_constant__ PackParams p)
 {
-    griddep_wait();
-    griddep_launch_dependents();
+    follow();
     const int lane = threadIdx.x & 31;
     const int64_t all = p.units[0] + p.units[1], warps = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < all; u += warps) {
