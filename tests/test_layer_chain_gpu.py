@@ -264,3 +264,37 @@ def test_weights_that_a_call_just_before_writes(M, N, K, act, between, pdl):
         want = run(torch.cuda.synchronize)
         for _ in range(3):
             assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+
+
+@pytest.mark.parametrize("M,N,K,act", [(33, 513, 511, "gelu"), (64, 256, 512, "swiglu"), (700, 640, 1000, None),
+                                       (2000, 1437, 520, "silu"), (1, 130, 70, None), (300, 77, 2048, "geglu")])
+def test_gradients_one_behind_another_in_one_workspace(M, N, K, act):
+    """Any choice of outputs, each call on the workspace of the one before: the same with launches that overlap."""
+    rows = 2 * N if act in ("swiglu", "geglu") else N
+    g = torch.Generator(device="cuda").manual_seed(N)
+
+    def new(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    sets = [(new(M, N), new(M, K), new(rows, K), new(M, rows)) for _ in range(3)]
+    choices = [(dx, dw, db) for dx in (0, 1) for dw in (0, 1) for db in (0, 1) if dx or dw or db]
+    space = torch.empty(sk.linear_grad_workspace(*sets[0][:3], act), device="cuda", dtype=torch.uint8)
+    outs = [(torch.empty(M, K, device="cuda", dtype=torch.bfloat16), torch.empty(rows, K, device="cuda", dtype=torch.bfloat16),
+             torch.empty(rows, device="cuda")) for _ in range(2 * len(choices))]
+
+    def run(pdl):
+        for out in outs:
+            for t in out:
+                t.fill_(-7)
+        with sk.options(pdl=pdl):
+            for i, out in enumerate(outs):
+                dx, dw, db = choices[i * 3 % len(choices)]
+                dy, x, w, z = sets[i % 3]
+                sk.linear_grad(dy, x, w, z if act else None, act, dx=out[0] if dx else None, dw=out[1] if dw else None,
+                               dbias=out[2] if db else None, input_grad=dx, weight_grad=dw, bias_grad=db, workspace=space)
+        torch.cuda.synchronize()
+        return [t.clone() for out in outs for t in out]
+
+    want = run(0)
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(run(1), want))
