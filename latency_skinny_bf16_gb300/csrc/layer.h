@@ -42,6 +42,8 @@ struct ProductArgs {
     bool beside;             // of the kernel before: nothing of it is read or written
     bool last;               // of a call; read with beside
 };
+// 64-step boxes of a depth, which may be the largest int: a gradient's depth is the number of tokens
+constexpr int depth_boxes(int depth) { return depth / 64 + (depth % 64 != 0); }
 // a depth of 0 (linear_empty.cu)
 cudaError_t launch_linear_empty(const ProductArgs &a, const CallCtx &c, cudaStream_t stream);
 

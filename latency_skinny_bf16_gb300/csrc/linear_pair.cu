@@ -435,7 +435,7 @@ cudaError_t linear_pair_prepare() {
 bool linear_pair_faster(const ProductArgs &a, int num_sms) {
     if (a.rows <= 64 && !a.B.crossed) return false;
     const int64_t wide = act_gated(a.act) ? 128 : 256, pairs = num_sms / 2;
-    const int64_t tiles = (a.rows + 255) / 256 * ((a.cols + wide - 1) / wide), boxes = (a.depth + 63) / 64;
+    const int64_t tiles = (a.rows + 255) / 256 * ((a.cols + wide - 1) / wide), boxes = depth_boxes(a.depth);
     return (tiles + pairs - 1) / pairs * (276 * boxes + 500) + 4000 < linear_tc_ns(a, num_sms);
 }
 
@@ -458,7 +458,7 @@ cudaError_t launch_linear_pair(const ProductArgs &a, const CallCtx &c, cudaStrea
     p.b3 = b3;
     p.nt = (a.cols + 2 * TA - 1) / (2 * TA);
     p.rt = (int)((a.rows + 255) / 256);
-    p.boxes = (a.depth + 63) / 64;
+    p.boxes = depth_boxes(a.depth);
     p.beside = a.beside;
     p.last = a.last;
     p.status = c.status;

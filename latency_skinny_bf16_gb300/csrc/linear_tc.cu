@@ -411,7 +411,7 @@ struct Split {
     int64_t ctas;
 };
 Split split_of(const ProductArgs &a, int BN, int num_sms) {
-    const int full = act_gated(a.act) ? 64 : 128, boxes = (a.depth + 63) / 64;
+    const int full = act_gated(a.act) ? 64 : 128, boxes = depth_boxes(a.depth);
     const int64_t mt = (a.rows + BN - 1) / BN, across = mt * ((a.cols + full - 1) / full);
     const int64_t held[4] = {2ll * num_sms, 2ll * num_sms, 288ll * num_sms / 152, 256ll * num_sms / 152};
     int lg = 0;
@@ -434,7 +434,7 @@ Split split_of(const ProductArgs &a, int BN, int num_sms) {
 // depth) 31.4 and 31.4, 512 rows SwiGLU 2048 x 7168 31.8 and 31.4, 2048 x 2048 (four) 13.4 and 12.2.
 int64_t linear_tc_ns(const ProductArgs &a, int num_sms) {
     const Split s = split_of(a, 128, num_sms);
-    const int64_t rounds = (s.ctas + 2 * num_sms - 1) / (2 * num_sms), boxes = ((a.depth + 63) / 64 + s.split - 1) / s.split;
+    const int64_t rounds = (s.ctas + 2 * num_sms - 1) / (2 * num_sms), boxes = (depth_boxes(a.depth) + s.split - 1) / s.split;
     return rounds * (400 * boxes + 3000) + (s.split > 1 ? 6000 : 0);
 }
 
@@ -453,7 +453,7 @@ cudaError_t launch_linear_tc(const ProductArgs &a, const CallCtx &c, cudaStream_
     Params p{};
     const Split plan = split_of(a, BN, c.num_sms);
     p.mt = (a.rows + BN - 1) / BN;
-    p.boxes = (a.depth + 63) / 64;
+    p.boxes = depth_boxes(a.depth);
     p.split = plan.split;
     p.ta = plan.ta;
     const int TA = p.ta;
