@@ -95,7 +95,7 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *ma
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar) : "memory");
 }
 // The issuer waits for every stage, so all copies have landed once both CTAs meet at the end.  After a give-up
-// some stages may never be complete on the barrier: a time in which any copy lands.
+// some stages may never be complete on the barrier: a time in which any copy, and any arrival of a commit, lands.
 __device__ __forceinline__ void let_land() {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < kLandNs) {}
@@ -226,6 +226,18 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
                     s = 0;
                     phase ^= 1;
                 }
+            }
+        }
+        // The MMAs' arrivals on `empty` come to both CTAs: all are here before this CTA may exit and leave its shared
+        // memory to another.  The waits are those of the stages that would follow.
+        for (int k = 0; go && k < kStages; ++k) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), phase, p.budget_ns))) {
+                if (one) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+                go = false;
+            }
+            if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
             }
         }
         if (!go && one) let_land();
@@ -394,9 +406,14 @@ linear_pair_kernel(const __grid_constant__ Maps maps, const Params p)
     tc_fence_before();
     __syncthreads();
     if (p.beside) follow();
-    cluster_arrive_release();                        // neither CTA reads or signals the other from here on
+    cluster_arrive_release();                        // no thread of either CTA reads or signals the other from here on
     cluster_wait_acquire();
     if (warp == 1) {
+        // the last commit's arrival, which the first CTA has seen in its own shared memory, in the second's
+        if (rank == 1 && *mma_ok && !mbar_wait_bounded(done, 0, kDrainNs)) {
+            if (lane == 0) report_status(p.status, SKINNY_ERR_DEVICE_TIMEOUT, kWaitDrain);
+        }
+        __syncwarp();
         tc_fence_after();
         if (*mma_ok) pair_dealloc(tmem);
         // else an issued MMA may still write it: it stays allocated until the CTA exits
