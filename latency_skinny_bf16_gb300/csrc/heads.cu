@@ -145,7 +145,6 @@ struct Piece {
         else memcpy(w, &r, sizeof(Raw));
     }
     __device__ __forceinline__ void load(const E *p) { put(__ldcg(reinterpret_cast<const Raw *>(p))); }
-    __device__ __forceinline__ void load_shared(const E *p) { put(__ldg(reinterpret_cast<const Raw *>(p))); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
         axes[j] = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int pair = pair_of(c, i), ax = pair >= half ? -1 : a.pair_axis ? __ldg(a.pair_axis + pair) : 0;
+            const int pair = pair_of(c, i), ax = pair >= half ? -1 : a.pair_axis ? __ldcg(a.pair_axis + pair) : 0;
             axes[j] |= (uint32_t)(ax >= 0 && ax < a.axes ? ax : 15) << (4 * i);
         }
     }
@@ -310,6 +309,9 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     };
 
     // The angles of token t: cosines and sines of the lane's pairs, and a bit for each pair that is not turned.
+    // Positions and table may be what the preceding kernel writes: ordinary loads behind the wait, which see it, and
+    // which neighbouring tokens' warps share in L1 (8192 tokens, 32 + 8 heads of 61: 48.6 us, past L1 51.5).  Never the
+    // non-coherent path, whose memory has to be constant from the kernel's start on.
     constexpr int kRun = INTER ? V / 2 : V;                  // pairs that follow each other in the table
     auto angles = [&](int t, Vs (&cs)[NC], Vs (&sn)[NC]) {
         uint32_t still = 0;
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                 if (i > 0 && ax == (axes[j] >> (4 * i - 4) & 15)) {
                     at[i] = at[i - 1];
                 } else {
-                    at[i] = ax < 15 ? __ldg(a.positions + (int64_t)ax * a.T + t) : -1;
+                    at[i] = ax < 15 ? a.positions[(int64_t)ax * a.T + t] : -1;
                     if (at[i] < 0 || at[i] >= a.P) at[i] = -1;
                 }
                 if (at[i] < 0) still |= 1u << (j * V + i);
@@ -340,13 +342,13 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
 #pragma unroll
                     for (int k = 0; k < kRun; k += kWide) {
                         if constexpr (kWide == 4) {
-                            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + k));
-                            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + k));
+                            const float4 c4 = *reinterpret_cast<const float4 *>(row + k);
+                            const float4 s4 = *reinterpret_cast<const float4 *>(row + half + k);
                             cv[i + k] = c4.x; cv[i + k + 1] = c4.y; cv[i + k + 2] = c4.z; cv[i + k + 3] = c4.w;
                             sv[i + k] = s4.x; sv[i + k + 1] = s4.y; sv[i + k + 2] = s4.z; sv[i + k + 3] = s4.w;
                         } else if constexpr (kWide == 2) {
-                            const float2 c2 = __ldg(reinterpret_cast<const float2 *>(row + k));
-                            const float2 s2 = __ldg(reinterpret_cast<const float2 *>(row + half + k));
+                            const float2 c2 = *reinterpret_cast<const float2 *>(row + k);
+                            const float2 s2 = *reinterpret_cast<const float2 *>(row + half + k);
                             cv[i + k] = c2.x; cv[i + k + 1] = c2.y;
                             sv[i + k] = s2.x; sv[i + k + 1] = s2.y;
                         }
@@ -358,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                         sv[i + k] = 0.f;
                         if (at[i + k] >= 0) {
                             const float *row = a.table + (int64_t)at[i + k] * R + pair_of(c, i + k);
-                            cv[i + k] = __ldg(row);
-                            sv[i + k] = __ldg(row + half);
+                            cv[i + k] = row[0];
+                            sv[i + k] = row[half];
                         }
                     }
                 }
@@ -392,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
         for (int j = 0; j < NC; ++j) {
             wa[j].zero();
             wb[j].zero();
-            if (weighted && ea[j] >= 0) wa[j].load_shared(static_cast<const E *>(s.w) + ea[j]);
-            if (weighted && eb[j] >= 0) wb[j].load_shared(static_cast<const E *>(s.w) + eb[j]);
+            if (weighted && ea[j] >= 0) wa[j].load(static_cast<const E *>(s.w) + ea[j]);
+            if (weighted && eb[j] >= 0) wb[j].load(static_cast<const E *>(s.w) + eb[j]);
         }
         int t = (int)(begin / steps), b = (int)(begin - (int64_t)t * steps), stage = 0;
         // the place of the step whose loads go out next, kDepth steps ahead of the one computed
