@@ -24,7 +24,8 @@ SOURCES = ["api.cu", "dotprod.cu", "dotprod_f32w.cu", "dotmma.cu", "dotmma_f32w.
            "topk.cu", "rmsnorm.cu", "tmem_gemm.cu", "expert_rows.cu", "experts_api.cu",
            "experts_mma.cu", "experts_tc.cu", "lora.cu", "layer_api.cu", "linear_empty.cu", "linear_dz.cu", "linear_tc.cu", "linear_pair.cu", "rows_pack.cu", "heads.cu"]
 HEADERS = ["common.cuh", "internal.h", "tuning_table.inc", "tma.cuh", "dotmma_f32w.h", "expert_rows.h", "experts_gemm.h",
-           "mma_rows.cuh", "tcgen05.cuh", "tma_stack.cuh", "calls.h", "ranges.h", "layer.h", "act.cuh", "product.cuh"]
+           "mma_rows.cuh", "tcgen05.cuh", "tma_stack.cuh", "calls.h", "ranges.h", "layer.h", "act.cuh", "product.cuh",
+           "element_fetch.h"]
 
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "element_fetch.h"
 #include "experts_gemm.h"
 #include "layer.h"
 
@@ -230,8 +231,13 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __host__ __device__ constexpr int ring_depth(int el, bool grad) { return grad ? (el == 2 ? 3 : 2) : el == 2 ? 4 : 3; }
-// Bytes of a thread's slot.  A single bf16 element comes with the aligned four bytes that hold it: cp.async moves no
-// less, and its neighbour is in the same allocation, whose size is a multiple of that.
+// A single bf16 element to the half of a slot that it has of its word in memory (element_fetch.h).
+__device__ __forceinline__ void copy_element(uint32_t dst, const void *src, uintptr_t first, uintptr_t last) {
+    const ElementFetch f = element_fetch(reinterpret_cast<uintptr_t>(src), first, last);
+    if (f.bytes == 4) copy_async<4>(dst, reinterpret_cast<const void *>(f.from));
+    else asm volatile("st.shared.u32 [%0], %1;" :: "r"(dst), "r"((uint32_t)ldg_u16(src) << (8 * (f.from & 2))) : "memory");
+}
+// Bytes of a thread's slot: a single bf16 element has a word.
 __host__ __device__ constexpr int slot_bytes(int V, int el) { return V * el < 4 ? 4 : V * el; }
 __host__ __device__ constexpr int chunks_per_lane(int V, bool wide) { return V > 1 ? kPairs / V : wide ? 8 : 2; }
 __host__ __device__ constexpr int ring_bytes(int V, int NC, int el, bool grad) {
@@ -409,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             if constexpr (GRAD) ld = static_cast<const E *>(s.d) + (int64_t)lt * s.dst + (int64_t)(lb * HP + hs) * s.dsh;
         };
         load_token();
-        auto issue = [&](int st) {
+        // CAREFUL: the tensor's first or last heads, whose words may reach out of it
+        auto issue = [&](int st, auto CAREFUL) {
             if (left > 0) {
                 --left;
                 const bool live = lb * HP + hs < s.H;
@@ -418,8 +425,15 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                     const int q = i / (2 * NC), j = i / 2 % NC, at = i % 2 ? eb[j] : ea[j];
                     if (at < 0 || !live || (GRAD && q == 0 && !a.norm)) continue;
                     const E *from = (q ? ld : lx) + at;
-                    if constexpr (kHalves) from = reinterpret_cast<const E *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3);
-                    copy_async<kBytes>(slots + slot(st, i), from);
+                    const uint32_t dst = slots + slot(st, i);
+                    if constexpr (decltype(CAREFUL)::value) {
+                        const E *first = static_cast<const E *>(q ? s.d : s.x);
+                        const E *last = first + (a.T - 1) * (q ? s.dst : s.st) + (s.H - 1) * (q ? s.dsh : s.sh) + D - 1;
+                        copy_element(dst, from, reinterpret_cast<uintptr_t>(first), reinterpret_cast<uintptr_t>(last));
+                    } else {
+                        if constexpr (kHalves) from = reinterpret_cast<const E *>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)3);
+                        copy_async<kBytes>(dst, from);
+                    }
                 }
                 lx += xstep;
                 if constexpr (GRAD) ld += dstep;
@@ -431,8 +445,15 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        const int64_t careful = kHalves && end == all ? 1 : 0;       // steps at the share's end
+        auto issue_next = [&](int st, bool starts) {
+            if constexpr (kHalves) {
+                if (left <= careful || (starts && begin == 0)) return issue(st, std::true_type{});
+            }
+            issue(st, std::false_type{});
+        };
 #pragma unroll
-        for (int i = 0; i < kDepth; ++i) issue(i);
+        for (int i = 0; i < kDepth; ++i) issue_next(i, i == 0);
         for (int64_t todo = end - begin; todo > 0; b = 0, ++t) {
             Vs cs[NC], sn[NC];
             const uint32_t still = angles(t, cs, sn);
@@ -497,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
                         to.w[0] = to.w[0] >> (16 * (place & 1)) & 0xFFFFu;
                     }
                 }
-                issue(stage);
+                issue_next(stage, false);
                 if (++stage == kDepth) stage = 0;
                 const bool live = hs < HP && h < s.H;
                 Vs ss = vall<V>(0.f);
