@@ -134,7 +134,8 @@ typedef struct {
  *   q, k     the inputs; H 0: none of the kind (its pointers are not used)
  *   q_out    device, dtype [T, q.H, D], strides q_st, q_sh; k_out likewise.  An output may be its own input
  *            (same pointer and strides); otherwise it overlaps no input and not the other output.  Views that
- *            share a token stride may lie beside each other in each token.
+ *            share a token stride may lie beside each other in each token, and heads may take turns, a query's
+ *            beside its key's, where all strides are multiples of the smallest.
  *   T >= 0, 1 <= D <= 512, 0 <= R <= D even (0: no rotation, the table is not used), 1 <= axes <= 8, 1 <= P.
  */
 SKINNY_API skinny_status_t skinny_qk_norm_rope(const skinny_heads_t *q, const skinny_heads_t *k,

@@ -71,6 +71,12 @@ struct View {
         return p == o.p && T == o.T && H == o.H && (T <= 1 || st == o.st) && (H <= 1 || sh == o.sh);
     }
 };
+// Whether rows of wa and wb bytes, the second b - a = `apart` behind the first and both every `step` bytes, share none.
+bool beside(uintptr_t apart, int64_t step, int64_t wa, int64_t wb) {
+    int64_t d = (int64_t)apart % step;
+    if (d < 0) d += step;
+    return wa <= step && wb <= step && d >= wa && d + wb <= step;
+}
 bool views_meet(const View &a, const View &b) {
     if (a.none() || b.none()) return false;
     const uintptr_t a0 = addr(a.p), b0 = addr(b.p);
@@ -78,12 +84,16 @@ bool views_meet(const View &a, const View &b) {
     // side by side in rows of one stride: neither reaches into the other within a row
     const int64_t s = a.st * a.el, wa = ((int64_t)(a.H - 1) * (a.H > 1 ? a.sh : 0) + a.D) * a.el,
                   wb = ((int64_t)(b.H - 1) * (b.H > 1 ? b.sh : 0) + b.D) * b.el;
-    if (a.T > 1 && b.T > 1 && a.st == b.st && wa <= s && wb <= s) {
-        int64_t d = ((int64_t)(b0 - a0)) % s;
-        if (d < 0) d += s;
-        return !(d >= wa && d + wb <= s);
-    }
-    return true;
+    if (a.T > 1 && b.T > 1 && a.st == b.st && beside(b0 - a0, s, wa, wb)) return false;
+    // heads by turns, a query's beside its key's: all strides are multiples of one, and the heads lie at different
+    // places of it
+    int64_t step = 0;
+    for (const View *v : {&a, &b})
+        for (int64_t m : {v->T > 1 ? v->st : 0, v->H > 1 ? v->sh : 0})
+            if (m && (!step || m < step)) step = m;
+    for (const View *v : {&a, &b})
+        if (step && ((v->T > 1 && v->st % step) || (v->H > 1 && v->sh % step))) step = 0;
+    return !(step && beside(b0 - a0, step * a.el, (int64_t)a.D * a.el, (int64_t)b.D * b.el));
 }
 bool view_meets_range(const View &a, const Range &r) {
     if (a.none() || r.lo >= r.hi) return false;
