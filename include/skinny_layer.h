@@ -39,10 +39,12 @@ typedef enum {
  *     SKINNY_ACT_SWIGLU, GEGLU:      Y[m,n] = act(Z[m,n]) * Z[m,N+n] + R[m,n]         W [2N, K], bias [2N]
  *                                    (act is silu or gelu: gates, then ups)
  *
- * Sums in fp32, within 1e-5 of sum_k |x w| as in skinny_gemm_bf16 (tensor-core
- * chains of at most 16 MMAs, or 64 where there are many rows, then rounded
- * adds), the epilogue in fp32, one rounding to out_dtype.  Z, for the backward pass, is
- * rounded to bf16 beside it; Y is computed from what was not rounded.
+ * Sums in fp32 (tensor-core chains of at most 16 MMAs, or 64 where there are
+ * many rows, then rounded adds): within 1e-5 of sum_k |x w| up to a depth of
+ * 32768, as in skinny_gemm_bf16, and by 2^-32 of it more for each step of the
+ * depth beyond (2.5e-4 at the deepest, K = 2^20).  The epilogue in fp32, one
+ * rounding to out_dtype.  Z, for the backward pass, is rounded to bf16 beside
+ * it; Y is computed from what was not rounded.
  *
  *   X     device, bf16 [M, K], row stride ldx >= K;  W  device, bf16, row stride ldw >= K
  *   bias  device, bf16 [N or 2N], or NULL;  R  device, out_dtype [M, N], row stride ldr >= N, or NULL
@@ -81,8 +83,9 @@ SKINNY_API int64_t skinny_linear_workspace(const uint16_t *X, int ldx, const uin
  *
  * (R's gradient is dY.)  dZ is computed in fp32 and rounded to bf16 for the two
  * products, as the tensor cores take it; dbias sums what was not rounded.  Sums
- * in fp32 as above, one rounding of dX and dW to bf16.  SKINNY_ACT_NONE needs
- * no Z (NULL), and dZ is dY itself.
+ * in fp32 as above, over a depth of N or 2N (dX) or M tokens (dW, dbias), one
+ * rounding of dX and dW to bf16.  SKINNY_ACT_NONE needs no Z (NULL), and dZ is
+ * dY itself.
  *
  *   dY  device, bf16 [M, N];  X, W as above;  Z  device, bf16 [M, N or 2N]
  *   dX  device, bf16 [M, K], or NULL: not computed (W may then be NULL)

@@ -62,7 +62,7 @@ struct Params {
     Epilogue e;
     int64_t mt;          // tiles along the rows of B
     int boxes;           // 64-step boxes of the depth
-    int ta;              // outputs of a tile: 8 to 128 (gated: 64)
+    int ta;              // outputs of a tile: 64 to 128 in steps of 8 (gated: 64)
     int split;           // CTAs of a cluster along the depth: 1, 2, 4 or 8
     int beside, last;
     int *status;
@@ -73,7 +73,7 @@ template <int BN, bool GATED, bool AX, bool BX>
 __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_constant__ Maps maps, const Params p)
 {
     constexpr int kStages = ring_stages(BN), kStage = stage_bytes(BN), kSets = acc_sets(BN), kCols = set_cols(BN);
-    constexpr int P = kCols / BN;                    // accumulators of a set, taken in turn
+    constexpr int P = kCols / BN;                    // accumulators of a set, taken in turn: 4, 2 or 1
     const int TA = p.ta;
     static_assert(!BX || BN >= 64, "crossed boxes hold 64 indexes");
     extern __shared__ uint8_t smem_raw[];
@@ -251,16 +251,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
                 break;
             }
             tc_fence_after();
+            // the set's accumulators among each other first: one add to the long sum for 256 steps
 #pragma unroll
-            for (int q = 0; q < P; ++q)
+            for (int j = 0; j < BN; j += 16) {
+                uint32_t r[P][16];
 #pragma unroll
-                for (int j = 0; j < BN; j += 16) {
-                    uint32_t r[16];
-                    tmem_ld16_nowait(lanes + (uint32_t)(b * kCols + q * BN + j), r);
-                    tmem_ld_wait(r);
+                for (int q = 0; q < P; ++q) tmem_ld16_nowait(lanes + (uint32_t)(b * kCols + q * BN + j), r[q]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[j + i] += __uint_as_float(r[i]);
+                for (int q = 0; q < P; ++q) tmem_ld_wait(r[q]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float v = __uint_as_float(r[0][i]);
+                    if constexpr (P >= 2) v += __uint_as_float(r[1][i]);
+                    if constexpr (P == 4) v += __uint_as_float(r[2][i]) + __uint_as_float(r[3][i]);
+                    acc[j + i] += v;
                 }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acce(b));
