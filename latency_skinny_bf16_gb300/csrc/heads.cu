@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
         axes[j] = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int pair = pair_of(c, i), ax = pair >= half ? -1 : a.pair_axis ? __ldcg(a.pair_axis + pair) : 0;
+            const int pair = pair_of(c, i), ax = pair >= half ? -1 : a.pair_axis ? a.pair_axis[pair] : 0;
             axes[j] |= (uint32_t)(ax >= 0 && ax < a.axes ? ax : 15) << (4 * i);
         }
     }
