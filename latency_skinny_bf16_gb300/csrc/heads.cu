@@ -21,8 +21,9 @@
 // instructions (two thirds of the issue slots at 16 warps an SM, which is what the
 // factors' registers leave).  GB300, bf16 heads of 128, 64 + 8 of them: 8192 tokens
 // 55 us (5.5 TB/s), 16384 with three axes 108, the gradient for 8192 91 (5.0 TB/s);
-// fp32 32 + 8 heads 63 and 91.  Unusual sizes pay in instructions: 32 + 8 heads of
-// 61 47 us (1.7 TB/s), of 72 36, 16 + 2 heads of 80 for 20000 tokens 50.  Tried and
+// neighbours as pairs 55 and 93; fp32 32 + 8 heads 64 and 91.  Unusual sizes pay in
+// instructions: 32 + 8 heads of 61 51 us (1.6 TB/s; the gradient 83), of 72 37, 16 + 2
+// heads of 80 for 20000 tokens 50, 8 + 2 heads of 333 for 2048 tokens 26 (79).  Tried and
 // slower: 24 warps of 80 registers (87 us where 16 take 59), two heads a lane at a
 // time (the same), loads held in registers (60 against 55).
 #include <type_traits>

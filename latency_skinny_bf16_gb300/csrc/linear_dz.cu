@@ -8,6 +8,10 @@
 // and every eighth of its part of the tokens a row of threads; the bias gradient is
 // summed along a thread's tokens, over the CTA's eight rows and then over the parts
 // by a second kernel, in a fixed order.
+// dZ is rounded to bf16 here, once, as the operand of both products: the tensor cores
+// take no fp32, and a second bf16 term for what the rounding drops would double the depth
+// of dX and the rows of dW (8192 tokens, 2 * 2048 x 7168: 250 us each as it is).  It puts
+// both at 0.0023 of their norm from the definition, where their own rounding is 0.0017.
 #include "act.cuh"
 #include "common.cuh"
 #include "experts_gemm.h"

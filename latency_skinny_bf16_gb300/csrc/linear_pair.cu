@@ -21,11 +21,13 @@
 //     MMAs of the next tile go on for two sets.  With a gated activation a CTA's
 //     lanes are 64 gates and their 64 ups; half of the rows of each change sides
 //     through shared memory, so that all eight warps have the same work.
-// What bounds it: the tensor cores, and each call's start and last tile.  GB300:
-// 4864 x 4096 x 8192 174 us (1875 TFLOP/s, 98% of the library's plain product), 8192
-// rows SwiGLU 2048 x 7168 with the sums kept 266, its two backward products 254 and
-// 255 (251 the library's), 2048 rows 7168 x 2048 35 (35), with
-// bias and residual 43.
+// What bounds it: the tensor cores, and each call's start and last tile.  GB300, us, in
+// runs of 20 ms at 2070 MHz, and for seconds under the power limit (about 1440 MHz); in
+// brackets the library's plain product:
+//   4864 x 4096 x 8192                         171 [168], 200 [192]    1910 TFLOP/s, 1634
+//   8192 rows SwiGLU 2048 x 7168, sums kept    260 [247], 303 [282]
+//   its backward products                      248 [238] and 252 [243], 289 [271] and 293 [279]
+//   2048 rows 7168 x 2048                      35 [33], 40 [37]; with bias and residual 41, 46
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing
 // from there on, and both CTAs of a pair still meet at the end.
 #include <cuda.h>

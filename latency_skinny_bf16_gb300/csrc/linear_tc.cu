@@ -20,8 +20,8 @@
 // What bounds it: device memory for the weight, and, as far as calls follow each
 // other, what lies between the preceding call's end and the first sums, and between
 // the last sums and the stores (about 3 us).  GB300, us, chained with PDL, one token
-// and 64: 2112 x 7168 8.1 and 10.4 (floor 4.5), 24576 x 1536 13.0 and 15.2 (11.3),
-// SwiGLU 2048 x 7168 11.3 and 13.9 (8.8), 8192 x 8192 21.7 and 24.9 (20.0).
+// and 64, no bias: 2112 x 7168 8.1 and 10.4 (floor 4.5), 24576 x 1536 13.4 and 15.1 (11.3),
+// SwiGLU 2048 x 7168 11.6 and 14.2 (8.8), 8192 x 8192 22.7 and 25.8 (20.0).
 // Every wait is bounded; a CTA whose wait gave up reports it and stores nothing.
 #include <cuda.h>
 #include <type_traits>
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_tc_kernel(const __grid_con
         fence_mbarrier_init_cluster();
         prefetch_tensormap(&maps.b);
         // A's first boxes, to L2 only: whatever the preceding kernel still writes, the copies behind the wait see it
-        // (one token, 2112 x 7168: 8.9 us without, 8.5 so, 8.4 with copies to shared memory here)
+        // (one token, 2112 x 7168 with a bias: 8.9 us without, 8.5 so, 8.4 with copies to shared memory here)
         for (int i = 0; !p.beside && i < pre; ++i) {
             const int c = (b0 + i) * 64;
             if constexpr (AX) {
