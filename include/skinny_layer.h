@@ -49,7 +49,8 @@ typedef enum {
  *   X     device, bf16 [M, K], row stride ldx >= K;  W  device, bf16, row stride ldw >= K
  *   bias  device, bf16 [N or 2N], or NULL;  R  device, out_dtype [M, N], row stride ldr >= N, or NULL
  *   Y     device, out_dtype [M, N], row stride ldy >= N.  R may be Y itself (same row stride);
- *         otherwise Y and Z overlap no input and not each other
+ *         otherwise Y and Z overlap no input and not each other.  Columns of one buffer side by side (one
+ *         row stride) do not overlap.
  *   Z     device, bf16 [M, N or 2N], row stride ldz, or NULL
  *   workspace  device, 16-byte aligned, skinny_linear_workspace(...) bytes for the same arguments, not
  *         shared with a call that may run at the same time; NULL where that is 0

@@ -20,6 +20,27 @@ skinny_status_t check_product(int M, int N, int K, int act) {
 
 bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
+// Whether rows of wa and wb bytes, the second b - a = `apart` behind the first and both every `step` bytes, share none.
+bool beside(uintptr_t apart, int64_t step, int64_t wa, int64_t wb) {
+    int64_t d = (int64_t)apart % step;
+    if (d < 0) d += step;
+    return wa <= step && wb <= step && d >= wa && d + wb <= step;
+}
+// The bytes of a matrix, and its rows' distance and width (one row or a plain range: 0).
+struct Rows : Range {
+    int64_t step = 0, width = 0;
+};
+Rows rows_of(const void *p, int64_t rows, int64_t cols, int64_t ld, int el) {
+    const Range r = span(p, rows, cols, ld, el);
+    return {r, rows > 1 ? ld * el : 0, cols * el};
+}
+// Whether a matrix that is written shares elements with one of the others; columns of one buffer side by side do not.
+bool rows_meet(const Rows &w, std::initializer_list<Rows> others) {
+    for (const Rows &o : others)
+        if (meets(w, {o}) && !(w.step > 0 && w.step == o.step && beside(o.lo - w.lo, w.step, w.width, o.width))) return true;
+    return false;
+}
+
 // Where the pieces of a call lie in its workspace (-1: not used).
 struct Space {
     int64_t x = -1, w = -1, dz = -1, partial = -1, bytes = 0;
@@ -71,12 +92,6 @@ struct View {
         return p == o.p && T == o.T && H == o.H && (T <= 1 || st == o.st) && (H <= 1 || sh == o.sh);
     }
 };
-// Whether rows of wa and wb bytes, the second b - a = `apart` behind the first and both every `step` bytes, share none.
-bool beside(uintptr_t apart, int64_t step, int64_t wa, int64_t wb) {
-    int64_t d = (int64_t)apart % step;
-    if (d < 0) d += step;
-    return wa <= step && wb <= step && d >= wa && d + wb <= step;
-}
 bool views_meet(const View &a, const View &b) {
     if (a.none() || b.none()) return false;
     const uintptr_t a0 = addr(a.p), b0 = addr(b.p);
@@ -162,12 +177,12 @@ skinny_status_t skinny_linear_bf16(const uint16_t *X, int ldx, const uint16_t *W
     if (!aligned(Y, ob) || !aligned(R, ob) || !aligned(Z, 2) || !aligned(bias, 2) ||
         (K > 0 && (!aligned(X, 2) || !aligned(W, 2))) || (need > 0 && !aligned(workspace, 16)))
         return SKINNY_ERR_MISALIGNED;
-    const Range y = span(Y, M, N, ldy, ob), z = span(Z, M, rows, ldz, 2), b = span(bias, 1, rows, rows, 2),
-                x = K > 0 ? span(X, M, K, ldx, 2) : Range{0, 0}, w = K > 0 ? span(W, rows, K, ldw, 2) : Range{0, 0},
-                r = span(R, M, N, ldr, ob), ws = {addr(workspace), addr(workspace) + (uintptr_t)need};
+    const Rows none{}, y = rows_of(Y, M, N, ldy, ob), z = rows_of(Z, M, rows, ldz, 2), b = rows_of(bias, 1, rows, rows, 2),
+               x = K > 0 ? rows_of(X, M, K, ldx, 2) : none, w = K > 0 ? rows_of(W, rows, K, ldw, 2) : none,
+               r = rows_of(R, M, N, ldr, ob), ws = {{addr(workspace), addr(workspace) + (uintptr_t)need}};
     const bool in_place = R == Y && (M == 1 || ldr == ldy);
-    if (meets(y, {x, w, b, z, ws}) || (!in_place && meets(y, {r})) || meets(z, {x, w, b, r, ws}) ||
-        meets(ws, {x, w, b, r}))
+    if (rows_meet(y, {x, w, b, z, ws}) || (!in_place && rows_meet(y, {r})) || rows_meet(z, {x, w, b, r, ws}) ||
+        rows_meet(ws, {x, w, b, r}))
         return SKINNY_ERR_INVALID_VALUE;
     CallCtx c;
     st = call_context(&c);
@@ -211,8 +226,8 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
     if (!dX && !dW && !dbias) return SKINNY_OK;
     if ((dX && lddx < K) || (dW && lddw < K)) return SKINNY_ERR_INVALID_VALUE;
     if (!aligned(dX, 2) || !aligned(dW, 2) || !aligned(dbias, 4)) return SKINNY_ERR_MISALIGNED;
-    const Range gx = span(dX, M, K, lddx, 2), gw = span(dW, rows, K, lddw, 2), gb = span(dbias, 1, rows, rows, 4);
-    if (meets(gx, {gw, gb}) || meets(gw, {gb})) return SKINNY_ERR_INVALID_VALUE;
+    const Rows none{}, gx = rows_of(dX, M, K, lddx, 2), gw = rows_of(dW, rows, K, lddw, 2), gb = rows_of(dbias, 1, rows, rows, 4);
+    if (rows_meet(gx, {gw, gb}) || rows_meet(gw, {gb})) return SKINNY_ERR_INVALID_VALUE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallCtx c;
     if (M == 0 || N == 0) {          // empty sums
@@ -231,10 +246,11 @@ skinny_status_t skinny_linear_grad_bf16(const uint16_t *dY, int lddy, const uint
     if (!aligned(dY, 2) || (!act_none && !aligned(Z, 2)) || (dX && !aligned(W, 2)) || (dW && !aligned(X, 2)) ||
         !aligned(workspace, 16))
         return SKINNY_ERR_MISALIGNED;
-    const Range y = span(dY, M, N, lddy, 2), z = act_none ? Range{0, 0} : span(Z, M, rows, ldz, 2),
-                x = dW ? span(X, M, K, ldx, 2) : Range{0, 0}, w = dX ? span(W, rows, K, ldw, 2) : Range{0, 0},
-                ws = {addr(workspace), addr(workspace) + (uintptr_t)need};
-    if (meets(gx, {y, z, x, w, ws}) || meets(gw, {y, z, x, w, ws}) || meets(gb, {y, z, x, w, ws}) || meets(ws, {y, z, x, w}))
+    const Rows y = rows_of(dY, M, N, lddy, 2), z = act_none ? none : rows_of(Z, M, rows, ldz, 2),
+               x = dW ? rows_of(X, M, K, ldx, 2) : none, w = dX ? rows_of(W, rows, K, ldw, 2) : none,
+               ws = {{addr(workspace), addr(workspace) + (uintptr_t)need}};
+    if (rows_meet(gx, {y, z, x, w, ws}) || rows_meet(gw, {y, z, x, w, ws}) || rows_meet(gb, {y, z, x, w, ws}) ||
+        rows_meet(ws, {y, z, x, w}))
         return SKINNY_ERR_INVALID_VALUE;
     st = call_context(&c);
     if (st != SKINNY_OK) return st;
