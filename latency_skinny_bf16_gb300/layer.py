@@ -224,7 +224,9 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, pre=None, 
     ``w`` [2N, K], ``out = act(z[:, :N]) * z[:, N:] + residual``: ``x`` bf16
     [M, K], ``bias`` bf16, ``out`` bf16 (default) or fp32 [M, N], ``residual``
     as ``out`` (it may be ``out`` itself).  ``pre``, bf16 and as wide as ``w``
-    has rows, keeps z for :func:`linear_grad`.  Any number of rows.  See
+    has rows, keeps z for :func:`linear_grad`.  Any number of rows.  Rows that
+    do not lie on 16-byte boundaries are laid out in ``workspace`` on every
+    call (:func:`linear_workspace` bytes, allocated where none is given).  See
     ``skinny_linear_bf16``."""
     if torch is None:
         _import_torch()

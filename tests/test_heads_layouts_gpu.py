@@ -1,8 +1,10 @@
-"""Heads of queries, keys and values by turns, [T, H, 3, D]: in place and into a buffer of the same order, as apart."""
+"""Heads of queries, keys and values by turns, [T, H, 3, D]: in place and into a buffer of the same order, against 64
+bits with the bounds of the other layouts."""
 import pytest
 import torch
 
 import latency_skinny_bf16_gb300 as sk
+import layer_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -25,22 +27,17 @@ def test_by_turns(first, T, H, D, R, interleaved, dtype):
     angle = torch.arange(500, device="cuda")[:, None] * 0.8 ** torch.arange(R // 2, device="cuda")
     args = dict(q_weight=w[0], k_weight=w[1], table=torch.cat([angle.cos(), angle.sin()], 1).float(), interleaved=interleaved,
                 positions=torch.randint(0, 500, (T,), generator=g, device="cuda", dtype=torch.int32))
-    want, rest = sk.qk_norm_rope(q.contiguous(), k.contiguous(), **args), v.clone()
-    dwant = sk.qk_norm_rope_grad(dq.contiguous(), dk.contiguous(), q.contiguous(), k.contiguous(), **args)
-
-    def close(a, b):       # other boundaries: sums in another order, then a rounding
-        step = 2.0 ** -8 if a.dtype is torch.bfloat16 else 2.0 ** -18
-        size = 8.0 if a.dim() == 3 else 8.0 * T * H
-        assert ((a.double() - b.double()).abs() <= step * (b.double().abs() + size * 2.0 ** -8)).all()
-
-    out = rows()
+    rest, out = v.clone(), rows()
     kept = out[2].clone()
-    for a, b in zip(sk.qk_norm_rope(q, k, **args, q_out=out[0], k_out=out[1]), want):
-        close(a, b)
-    assert torch.equal(out[2], kept)
+    cos, sin = ref.angles(args["table"], args["positions"], None, T)
+    sk.qk_norm_rope(q, k, **args, q_out=out[0], k_out=out[1])
     again = [t.clone() for t in sk.qk_norm_rope_grad(dq, dk, q, k, **args)]
-    for a, b in zip(again, dwant):
-        close(a, b)
+    for i, (x, d) in enumerate(((q, dq), (k, dk))):
+        ref.check(out[i], *ref.heads(x, w[i], cos, sin, 1e-6, interleaved, dtype))
+        dx, dw = ref.heads_grad(d, x, w[i], cos, sin, 1e-6, interleaved, dtype)
+        ref.check(again[i], *dx)
+        ref.check(again[2 + i], *dw)
+    assert torch.equal(out[2], kept)
     got = sk.qk_norm_rope_grad(dq, dk, q, k, **args, dq_in=dq, dk_in=dk)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     first_out = [t.clone() for t in out[:2]]
